@@ -563,6 +563,208 @@ FP4LIN_API fp4_status fp4_gemm_mxfp4_grouped(const uint8_t* a, const uint8_t* sa
                                   const int32_t* row_offsets, int32_t E, int64_t total_M,
                                   int64_t N, int64_t K, void* stream);
 
+/* ============================ around the FP4 linear layer: one decoder layer
+ *
+ * What a decoder layer of the same checkpoints needs beside the FP4 linear
+ * layers: the linear layers the checkpoint keeps in FP8, rotary positions,
+ * the key/value cache in the library's MX formats, and attention over it.
+ * The conventions at the top of this header hold for all of them.
+ */
+
+/* ------------------------------------------- FP8 linear, blocks of 128
+ *
+ * [AMD] pipeline description: FP8 layers of a mixed-precision checkpoint are
+ * loaded as they are.  Weights are E4M3 codes with one float32 scale per
+ * 128 x 128 block, activations are quantized per token and 128 elements:
+ *   weights      codes [N, K] u8, scales [ceil(N/128)][ceil(K/128)] float32
+ *   activations  codes [M, K] u8, scales [ceil(K/128)][Mp] float32,
+ *                Mp = M rounded up to 4 (fp4_fp8_act_scale_bytes bytes)
+ * Value of an element: E4M3(code) * scale of its block.
+ * K must be a multiple of 16 (the last block may be short), N of 8.         */
+
+/* Bytes of the activation scales (0 for an invalid shape). */
+FP4LIN_API size_t fp4_fp8_act_scale_bytes(int64_t M, int64_t K);
+
+/* bf16 [M, K] -> E4M3 codes and scales.  Per row and block of 128, all in
+ * float32: a = max(amax, 2^-110), scale = a / 448, code = E4M3 of
+ * x * (448 / a), nearest with ties to even, saturating.  A block with a NaN
+ * or Inf gets a NaN scale and zero codes.  Pointers 16-byte aligned.        */
+FP4LIN_API fp4_status fp4_quant_act_fp8_b128(const void* x_bf16, uint8_t* codes, float* scales,
+                                  int64_t M, int64_t K, void* stream);
+
+/* The same rule for a weight bf16 [N, K], one scale per 128 x 128 block.    */
+FP4LIN_API fp4_status fp4_quant_weight_fp8_b128(const void* w_bf16, uint8_t* codes, float* scales,
+                                     int64_t N, int64_t K, void* stream);
+
+/* out[m, n] = bf16( sum_b sa[b, m] sb[n/128, b] sum_{k in b} a[m,k] b[n,k]
+ *                   + bias[n] ),  both sums in float32, one rounding.
+ * The products sa * sb must be finite float32 (or NaN, which reaches every
+ * output of its row or block column).  bias may be NULL.  All pointers
+ * 16-byte aligned (sb: 4).  Weights stream through the tensor cores' M side;
+ * no workspace.                                                             */
+FP4LIN_API fp4_status fp4_gemm_fp8_b128(const uint8_t* a, const float* sa, const uint8_t* b,
+                             const float* sb, const void* bias_bf16, void* out_bf16,
+                             int64_t M, int64_t N, int64_t K, void* stream);
+
+/* The layer in one call: fp4_quant_act_fp8_b128 into the workspace, then
+ * fp4_gemm_fp8_b128.  workspace: 256-byte aligned, at least
+ * fp4_linear_fp8_b128_workspace_size bytes, no initialization needed; calls
+ * that share one must not overlap in time.                                  */
+FP4LIN_API size_t fp4_linear_fp8_b128_workspace_size(int64_t M, int64_t N, int64_t K);
+FP4LIN_API fp4_status fp4_linear_fp8_b128(const void* x_bf16, const uint8_t* b, const float* sb,
+                               const void* bias_bf16, void* out_bf16, int64_t M, int64_t N,
+                               int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------ rotary positions */
+
+/* Pairs (a, b) of the first rot_dim elements of a head turn by the angle of
+ * their frequency at the token's position: a' = a cos - b sin,
+ * b' = b cos + a sin.  HALF pairs element i with i + rot_dim/2, INTERLEAVED
+ * 2i with 2i + 1.  The rest of the head is copied.                          */
+typedef enum { FP4_ROPE_HALF = 0, FP4_ROPE_INTERLEAVED = 1 } fp4_rope_layout;
+
+/* Turn by the negative angle (the transposed map: it undoes the rotation and
+ * is its backward pass when cos^2 + sin^2 = 1).                             */
+#define FP4_ROPE_INVERSE 1u
+
+typedef struct {
+    const float* table;       /* device [table_positions][rot_dim]: rot_dim/2 cosines, then
+                               * rot_dim/2 sines; 16-byte aligned                            */
+    int64_t table_positions;  /* positions outside [0, table_positions) use the nearest row  */
+    int32_t rot_dim;          /* multiple of 16, at most the head dimension                  */
+    int32_t layout;           /* fp4_rope_layout */
+    uint32_t flags;           /* FP4_ROPE_INVERSE or 0 */
+} fp4_rope_params;
+
+/* Frequencies for contexts longer than the model was trained on.
+ *   UNSCALED  w_i = base^(-2i / rot_dim)
+ *   LINEAR    w_i / factor
+ *   BY_PARTS  w_i where the original context holds more than turns_fast turns,
+ *             w_i / factor where it holds fewer than turns_slow, a linear ramp
+ *             over the frequency index between; cosines and sines times
+ *             magnitude.  The ramp's ends, as indexes, are
+ *             rot_dim/2 * ln(original_positions / (2 pi turns)) / ln(base),
+ *             rounded down (fast, at least 0) and up (slow, at most
+ *             rot_dim/2 - 1).                                               */
+typedef enum { FP4_ROPE_UNSCALED = 0, FP4_ROPE_LINEAR = 1, FP4_ROPE_BY_PARTS = 2 } fp4_rope_scaling_kind;
+typedef struct {
+    int32_t kind;               /* fp4_rope_scaling_kind */
+    double factor;              /* >= 1 (LINEAR, BY_PARTS) */
+    int64_t original_positions; /* BY_PARTS, as the rest */
+    double turns_fast;          /* >= turns_slow > 0 */
+    double turns_slow;
+    double magnitude;           /* > 0 */
+} fp4_rope_scaling;
+
+/* Fills table [positions][rot_dim] (device, float32), angles and functions
+ * in 64 bits, rounded once.  base > 1; scaling NULL = UNSCALED.             */
+FP4LIN_API fp4_status fp4_rope_table(float* table, int64_t positions, int32_t rot_dim, double base,
+                          const fp4_rope_scaling* scaling, void* stream);
+
+/* out = x rotated, bf16 [tokens][heads][head_dim]; float32 arithmetic, one
+ * rounding.  Strides in elements, multiples of 8, pointers 16-byte aligned;
+ * head_dim a multiple of 16 up to 1024.  out may be x itself (same strides),
+ * and must not overlap it otherwise.  positions: int32 [tokens] (device).   */
+FP4LIN_API fp4_status fp4_rope(const void* x_bf16, void* out_bf16, const int32_t* positions,
+                    const fp4_rope_params* rope, int64_t tokens, int32_t heads, int32_t head_dim,
+                    int64_t x_token_stride, int64_t x_head_stride, int64_t out_token_stride,
+                    int64_t out_head_stride, void* stream);
+
+/* ----------------------------------------------- MX-quantized paged cache */
+
+/* Keys and values of a layer in pages of page_size tokens, in MXFP8 (E4M3
+ * elements, FP4_ACT_MXFP8) or MXFP4 (E2M1, two per byte, FP4_ACT_MXFP4) with
+ * an E8M0 scale byte per 32 elements of a head (the library's OCP rule):
+ *   codes   [num_pages][kv_heads][page_size][head_dim bytes, or head_dim/2]
+ *   scales  [num_pages][kv_heads][page_size][head_dim/32]
+ * head_dim 64 or 128; page_size a multiple of 16 up to 4096; codes 16-byte
+ * aligned.  fp4_kv_code_bytes / fp4_kv_scale_bytes give the size of one of
+ * the two code / scale arrays.                                              */
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t format;   /* FP4_ACT_MXFP4 or FP4_ACT_MXFP8 */
+} fp4_kv_cache;
+
+FP4LIN_API size_t fp4_kv_code_bytes(const fp4_kv_cache* cache);
+FP4LIN_API size_t fp4_kv_scale_bytes(const fp4_kv_cache* cache);
+
+/* Quantizes the keys and values (bf16 [tokens][kv_heads][head_dim], strides
+ * in elements, multiples of 8) of `tokens` tokens into the cache.  Token t
+ * goes to slot slots[t] = page * page_size + offset (int64, device); a slot
+ * outside the cache is skipped (padding); slots must differ from one another.
+ * With `rope` not NULL the keys are rotated first (positions: int32
+ * [tokens]), in float32 and without a rounding in between.  A block with a
+ * NaN or Inf gets scale 0xFF and zero codes.                                */
+FP4LIN_API fp4_status fp4_kv_append(const fp4_kv_cache* cache, const void* k_bf16, const void* v_bf16,
+                         int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                         int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                         const fp4_rope_params* rope, const int32_t* positions, void* stream);
+
+/* Reads tokens back as bf16 (one rounding): the tokens of sequence b, from
+ * its first, become rows cu_lens[b] ... cu_lens[b + 1] - 1 of k and v
+ * [rows][kv_heads][head_dim].
+ *   block_table  [batch][block_table_stride] int32 page of each page_size
+ *                tokens of a sequence (device)
+ *   cu_lens      [batch + 1] int32, ascending from 0 (device)
+ * Rows whose page lies outside the cache or the table are not written.      */
+FP4LIN_API fp4_status fp4_kv_read(const fp4_kv_cache* cache, const int32_t* block_table,
+                       int64_t block_table_stride, const int32_t* cu_lens, int32_t batch,
+                       int64_t rows, void* k_bf16, void* v_bf16, void* stream);
+
+/* -------------------------------------- attention of drafted tokens */
+
+/* Softmax attention of the drafted tokens of each sequence over its cache.
+ * Sequence b has context_lens[b] tokens that all its drafted tokens see, and
+ * n_b = q_offsets[b + 1] - q_offsets[b] drafted tokens, rows q_offsets[b] ...
+ * of q, whose own keys and values are in the cache behind the context (at
+ * token context_lens[b] + j).  Drafted token i sees j where bit j of its mask
+ * row is set (word j / 32, bit j % 32); without a mask, where j <= i.  One
+ * drafted token per sequence is the ordinary decode step.  Query head h
+ * reads key/value head h / (q_heads / kv_heads).
+ *   out  bf16: sum over the seen tokens of softmax(softmax_scale q . k) v;
+ *        zeros for a row that sees nothing
+ *   lse  float32 [tokens][q_heads] or NULL: log of the sum of
+ *        exp(softmax_scale q . k); -inf for a row that sees nothing
+ * What a row does not see has no influence on it, NaN included (cache blocks
+ * with scale 0xFF are NaN).  Keys and values keep their relative precision
+ * between 2^-62 and 2^66 (smaller ones become multiples of 2^-69, larger ones
+ * are not supported), and E4M3 NaN codes, which fp4_kv_append does not write,
+ * are not either.                                                           */
+typedef struct {
+    const void* q_bf16;          /* [tokens][q_heads][head_dim] */
+    void* out_bf16;              /* the same shape */
+    float* lse;
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;  /* elements, multiples of 8 */
+    const int32_t* block_table;  /* [batch][block_table_stride], as for fp4_kv_read */
+    int64_t block_table_stride;
+    const int32_t* context_lens; /* [batch] */
+    const int32_t* q_offsets;    /* [batch + 1], ascending from 0 to tokens */
+    const uint32_t* tree_mask;   /* [tokens][mask_words] or NULL */
+    int32_t mask_words;          /* at least max_draft / 32, rounded up */
+    int32_t batch;               /* 1 .. 65535 */
+    int64_t tokens;
+    int32_t q_heads;
+    int32_t max_draft;           /* bound of n_b (host), 1 .. 1024: tokens past it are not computed */
+    int64_t max_seq_len;         /* bound of context_lens[b] + n_b (host): longer contexts are cut */
+    float softmax_scale;         /* > 0 */
+} fp4_kv_attention_args;
+
+/* workspace: 256-byte aligned, at least the bytes that the size function
+ * gives for the same shape (0: NULL will do), no initialization needed;
+ * calls that share one must not overlap in time.                            */
+FP4LIN_API size_t fp4_kv_attention_workspace_size(int32_t batch, int64_t tokens, int32_t q_heads,
+                                       int32_t kv_heads, int32_t head_dim, int64_t max_seq_len,
+                                       int32_t max_draft);
+FP4LIN_API fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_args* args,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -125,6 +125,14 @@ constexpr int64_t kMaxDim = int64_t(1) << 31;
 
 }  // namespace
 
+namespace fp4lin {
+
+int api_current_device(unsigned int** status) { return static_cast<int>(current_device(status)); }
+
+unsigned long long api_wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+}  // namespace fp4lin
+
 extern "C" {
 
 size_t fp4_sf_bytes(int64_t rows, int64_t K, int32_t sf_layout)

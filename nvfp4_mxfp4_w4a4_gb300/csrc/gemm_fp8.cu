@@ -1,0 +1,504 @@
+// gemm_fp8.cu -- the FP8 linear layer with a scale per block of 128: the
+// layers that a mixed-precision checkpoint keeps out of FP4 ("Efficiently
+// Serving NVFP4 Models on AMD Instinct MI350X/MI355X ... via Online NVFP4 to
+// Quark MXFP4 Requantization", pipeline description: FP8 layers are loaded
+// as they are).
+//
+//   out[m, n] = bf16( sum_b sa[b, m] sw[n / 128, b]
+//                       sum_{k in block b} A[m, k] B[n, k]  + bias[n] )
+//
+// A [M, K] and B [N, K] are E4M3, b runs over the blocks of 128 along K; sa
+// is float32 per row and block, sw float32 per 128 x 128 block.
+//
+// The tensor cores multiply E4M3 without scales (tcgen05.mma kind::f8f6f4),
+// so a block's products are summed in TMEM and each block's sum is scaled
+// and added to a running fp32 sum in registers ("promotion"): one fused
+// multiply-add per output and block, by warps that read one accumulator
+// while the MMAs fill the next.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "formats.cuh"
+#include "gemm_fp8.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fp4lin {
+namespace {
+
+constexpr int kBlock = 128;  // elements of K per scale, and bytes of K per pipeline stage
+constexpr int kThreadsQ = 256;
+// blocks whose largest magnitude is below this are scaled as if it were this,
+// so that neither the scale nor its inverse leaves the normal float32 range
+constexpr float kAmaxFloor = 7.703719777548943e-34f;  // 2^-110
+constexpr float kE4m3Max = 448.0f;
+
+// ------------------------------------------------------------ quantizers
+
+struct BlockScale {
+    float scale, inverse;
+};
+
+// From the bit pattern of the block's largest |x|; NaN and Inf give a NaN
+// scale (and the caller zero codes).
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits)
+{
+    BlockScale r;
+    if (amax_bits >= 0x7F800000u) {
+        r.scale = __uint_as_float(0x7FC00000u);
+        r.inverse = 0.0f;
+        return r;
+    }
+    const float a = fmaxf(__uint_as_float(amax_bits), kAmaxFloor);
+    r.scale = __fdiv_rn(a, kE4m3Max);
+    r.inverse = __fdiv_rn(kE4m3Max, a);
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x8_amax(uint4 v)
+{
+    const uint32_t a = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return max(a & 0xFFFFu, a >> 16);
+}
+
+__device__ __forceinline__ uint2 e4m3x8(uint4 v, float inv, bool zero)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(__uint_as_float(w[j] << 16), inv),
+                                                    __fmul_rn(__uint_as_float(w[j] & 0xFFFF0000u), inv)),
+                                        __NV_SATFINITE, __NV_E4M3);
+    return zero ? make_uint2(0u, 0u) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Activations: 16 lanes take one row's block of 128, 8 elements each.
+__global__ void __launch_bounds__(kThreadsQ) quant_act_fp8_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                  uint8_t* __restrict__ codes,
+                                                                  float* __restrict__ scales, int64_t blocks, int M,
+                                                                  int K, int kb, int ms)
+{
+    grid_dependency_wait();
+    launch_dependents();
+    const int64_t item = (static_cast<int64_t>(blockIdx.x) * kThreadsQ + threadIdx.x) >> 4;
+    const int lane = threadIdx.x & 15;
+    const bool live = item < blocks;
+    const int64_t row = live ? item / kb : 0;
+    const int b = static_cast<int>(live ? item - row * kb : 0);
+    const int col = b * kBlock + lane * 8;
+    const bool in = live && col < K;
+    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(x + row * K + col)) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t am = bf16x8_amax(v);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1)
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, d));
+    const BlockScale s = block_scale(am << 16);
+    if (in)
+        *reinterpret_cast<uint2*>(codes + row * K + col) = e4m3x8(v, s.inverse, s.inverse == 0.0f);
+    if (live && lane == 0)
+        scales[static_cast<int64_t>(b) * ms + row] = s.scale;
+}
+
+// Weights: one CTA per 128 x 128 block; the block stays in registers between
+// its maximum and its codes.
+__global__ void __launch_bounds__(kThreadsQ) quant_weight_fp8_kernel(const __nv_bfloat16* __restrict__ w,
+                                                                     uint8_t* __restrict__ codes,
+                                                                     float* __restrict__ scales, int64_t N, int K, int kb)
+{
+    __shared__ uint32_t part[kThreadsQ / 32];
+    grid_dependency_wait();
+    launch_dependents();
+    const int64_t nb = blockIdx.x / kb;
+    const int b = static_cast<int>(blockIdx.x - nb * kb);
+    const int col = b * kBlock + (threadIdx.x & 15) * 8;
+    const int64_t row0 = nb * kBlock + (threadIdx.x >> 4);
+    uint4 v[8];
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = row0 + 16 * i;
+        v[i] = (row < N && col < K) ? __ldg(reinterpret_cast<const uint4*>(w + row * K + col)) : make_uint4(0u, 0u, 0u, 0u);
+        am = max(am, bf16x8_amax(v[i]));
+    }
+    am = __reduce_max_sync(0xFFFFFFFFu, am);
+    if ((threadIdx.x & 31) == 0)
+        part[threadIdx.x >> 5] = am;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreadsQ / 32; ++i)
+        am = max(am, part[i]);
+    const BlockScale s = block_scale(am << 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = row0 + 16 * i;
+        if (row < N && col < K)
+            *reinterpret_cast<uint2*>(codes + row * K + col) = e4m3x8(v[i], s.inverse, s.inverse == 0.0f);
+    }
+    if (threadIdx.x == 0)
+        scales[nb * kb + b] = s.scale;
+}
+
+// ------------------------------------------- GEMM, weights on the M side
+//
+// One CTA: 128 weight rows x NT tokens, a run of the K blocks.  The CTAs of a
+// cluster share one output tile and split K; at the end each reduces its
+// share of the tile from all CTAs' shared memory, in their order.
+//   warp 0  TMA of the weights (which no kernel of the same call writes, so
+//           they stream before the quantizer ahead of this kernel is done)
+//   warp 1  TMEM, MMAs: four of K = 32 per block into one of BUFS accumulators
+//   warp 2  TMA of the tokens
+//   warp 3  the tokens' scales of a block, to a ring in shared memory
+//   warps 4..  promotion: lane = weight row, NT / WGS columns per warp
+template <int NT>
+struct SwapCfg {
+    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int WGS = NT >= 64 ? 2 : 1;   // promotion warpgroups
+    static constexpr int COLS = NT / WGS;          // columns per promotion warp
+    static constexpr int BUFS = NT >= 128 ? 2 : 4;
+    static constexpr int RING = 8;                 // blocks of token scales in shared memory
+    static constexpr int W_BYTES = 128 * kBlock;
+    static constexpr int X_BYTES = NT * kBlock;
+    static constexpr int OFF_X = STAGES * W_BYTES;
+    static constexpr int OFF_SA = OFF_X + STAGES * X_BYTES;
+    static constexpr int OFF_BAR = OFF_SA + RING * NT * 4;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 2 * RING;
+    static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // + alignment slack
+    static constexpr int TMEM_COLS = BUFS * NT < 32 ? 32 : BUFS * NT;
+    static constexpr int THREADS = 128 + 128 * WGS;
+    static_assert(NT * 128 * 4 <= OFF_SA, "the reduction buffer reuses the stages");
+    static_assert(TMEM_COLS <= 256 && SMEM <= 113 * 1024, "two CTAs per SM");
+};
+
+struct SwapParams {
+    const float* sa;
+    const float* sw;
+    const __nv_bfloat16* bias;
+    __nv_bfloat16* out;
+    int M, N;
+    int kb;       // blocks of K
+    int ms;       // row stride of sa
+    int splits;   // cluster size
+    int early_w;  // the weights are complete before this kernel may start
+    unsigned long long wait_ns;
+    unsigned int* status;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
+    gemm_fp8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                         const SwapParams p)
+{
+    using C = SwapCfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* acc_full = empty + C::STAGES;
+    uint64_t* acc_empty = acc_full + C::BUFS;
+    uint64_t* sa_full = acc_empty + C::BUFS;
+    uint64_t* sa_empty = sa_full + C::RING;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x;
+    const int n0 = blockIdx.y * 128, m0 = blockIdx.z * NT;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.kb) * split / p.splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.kb) * (split + 1) / p.splits);
+    const int nkb = kb1 - kb0;
+    const uint64_t limit = p.wait_ns;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 2);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < C::BUFS; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 4 * C::WGS);
+        }
+        for (int s = 0; s < C::RING; ++s) {
+            mbar_init(&sa_full[s], 32);
+            mbar_init(&sa_empty[s], 4 * C::WGS);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&tmW);
+        tma_prefetch_map(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    launch_dependents();
+
+    float acc[C::COLS];
+    if (warp == 0 || warp == 2) {
+        // ---------------------------------------------------- TMA producers
+        if (lane == 0) {
+            const bool w = warp == 0;
+            if (!w || !p.early_w)
+                grid_dependency_wait();
+            uint8_t* base = w ? smem : smem + C::OFF_X;
+            const int bytes = w ? C::W_BYTES : C::X_BYTES;
+            int it = 0;
+            for (; it < nkb; ++it) {
+                const int s = it % C::STAGES;
+                if (!mbar_wait_bounded(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.status, kStatusTimeout, limit))
+                    break;
+                mbar_arrive_expect_tx(&full[s], bytes);
+                tma_load_2d(base + s * bytes, w ? &tmW : &tmX, &full[s], (kb0 + it) * kBlock, w ? n0 : m0);
+            }
+            // gave up: the copies in flight land before the CTA leaves
+            if (it < nkb)
+                for (int j = max(0, it - C::STAGES); j < it; ++j)
+                    mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1, p.status, kStatusTimeout, limit);
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3(128, NT);
+            const uint64_t wd = smem_desc(smem_u32(smem), 16, 1024, 2);
+            const uint64_t xd = smem_desc(smem_u32(smem + C::OFF_X), 16, 1024, 2);
+            for (int it = 0; it < nkb; ++it) {
+                const int s = it % C::STAGES, b = it % C::BUFS;
+                if (!mbar_wait_bounded(&acc_empty[b], ((it / C::BUFS) & 1) ^ 1, p.status, kStatusTimeout, limit) ||
+                    !mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, p.status, kStatusTimeout, limit))
+                    break;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_f8f6f4(tmem + b * NT, wd + ((s * C::W_BYTES + 32 * k) >> 4), xd + ((s * C::X_BYTES + 32 * k) >> 4),
+                                  idesc, k != 0);
+                tc_commit(&empty[s]);
+                tc_commit(&acc_full[b]);
+            }
+        }
+    } else if (warp == 3) {
+        // -------------------------------------------------- token scales
+        grid_dependency_wait();
+        float* ring = reinterpret_cast<float*>(smem + C::OFF_SA);
+        for (int it = 0; it < nkb; ++it) {
+            const int r = it % C::RING;
+            const bool ok = lane != 0 || mbar_wait_bounded(&sa_empty[r], ((it / C::RING) & 1) ^ 1, p.status,
+                                                           kStatusTimeout, limit);
+            if (!__all_sync(0xFFFFFFFFu, ok))
+                break;
+            if (lane < NT / 4) {
+                const int m = m0 + lane * 4;  // rows are padded to a multiple of 4
+                cp_async_16(ring + r * NT + lane * 4,
+                            p.sa + static_cast<int64_t>(kb0 + it) * p.ms + (m < p.ms ? m : 0), m < p.ms);
+            }
+            cp_async_arrive(&sa_full[r]);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------ promotion
+        const int quad = warp & 3, col0 = ((warp - 4) >> 2) * C::COLS;
+#pragma unroll
+        for (int j = 0; j < C::COLS; ++j)
+            acc[j] = 0.0f;
+        const float* sw = p.sw + static_cast<int64_t>(blockIdx.y) * p.kb + kb0;
+        const float* ring = reinterpret_cast<const float*>(smem + C::OFF_SA);
+        if (!p.early_w)
+            grid_dependency_wait();
+        float wscale = nkb > 0 ? __ldg(sw) : 0.0f;
+        for (int it = 0; it < nkb; ++it) {
+            const int b = it % C::BUFS, r = it % C::RING;
+            const float wnext = it + 1 < nkb ? __ldg(sw + it + 1) : 0.0f;
+            const bool ok = mbar_wait_bounded(&sa_full[r], (it / C::RING) & 1, p.status, kStatusTimeout, limit) &&
+                            mbar_wait_bounded(&acc_full[b], (it / C::BUFS) & 1, p.status, kStatusTimeout, limit);
+            if (!__all_sync(0xFFFFFFFFu, ok))
+                break;
+            tc_fence_after_sync();
+            uint32_t d[C::COLS];
+            const uint32_t addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * NT + col0;
+#pragma unroll
+            for (int c = 0; c < C::COLS; c += 32) {
+                if constexpr (C::COLS >= 32)
+                    tmem_ld_32x32b_x32(addr + c, d + c);
+                else
+                    tmem_ld_32x32b_x16(addr, d);
+            }
+            tmem_ld_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&acc_empty[b]);
+#pragma unroll
+            for (int j = 0; j < C::COLS; j += 4) {
+                const float4 s = *reinterpret_cast<const float4*>(ring + r * NT + col0 + j);
+                acc[j] = fmaf(__uint_as_float(d[j]), s.x * wscale, acc[j]);
+                acc[j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y * wscale, acc[j + 1]);
+                acc[j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z * wscale, acc[j + 2]);
+                acc[j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w * wscale, acc[j + 3]);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sa_empty[r]);
+            wscale = wnext;
+        }
+    }
+
+    // ---------------------------------------------------- reduce and store
+    // every MMA has been read (each accumulator was waited for) and every copy
+    // has landed, so the stages' memory can hold the partial tile [NT][128]
+    __syncthreads();
+    float* tile = reinterpret_cast<float*>(smem);
+    if (warp >= 4) {
+        const int quad = warp & 3, col0 = ((warp - 4) >> 2) * C::COLS;
+#pragma unroll
+        for (int j = 0; j < C::COLS; ++j)
+            tile[(col0 + j) * 128 + quad * 32 + lane] = acc[j];
+    }
+    if (p.splits > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    {
+        // 8 outputs of a row per thread; the rows of the tile are dealt over the cluster
+        const int rows = min(NT, p.M - m0);
+        const int per = (rows + p.splits - 1) / p.splits;
+        const int r_end = min(rows, (split + 1) * per);
+        for (int i = threadIdx.x; i < per * 16; i += C::THREADS) {
+            const int r = split * per + (i >> 4), c = (i & 15) * 8;
+            if (r >= r_end || n0 + c >= p.N)
+                continue;
+            float f[8] = {};
+            const uint32_t at = smem_u32(tile + r * 128 + c);
+            for (int k = 0; k < p.splits; ++k) {
+                const uint32_t src = mapa_shared(at, k);
+                const float4 u = ld_cluster_f4(src), v = ld_cluster_f4(src + 16);
+                f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
+                f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+            }
+            if (p.bias != nullptr) {
+                const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + n0 + c);
+                const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] += __uint_as_float(bw[j] << 16);
+                    f[2 * j + 1] += __uint_as_float(bw[j] & 0xFFFF0000u);
+                }
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                o[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(m0 + r) * p.N + n0 + c) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+    tc_fence_before_sync();
+    if (p.splits > 1)
+        cluster_sync_all();  // the peers have read this CTA's partial tile
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+template <int NT>
+cudaError_t launch_swap(const Fp8GemmArgs& a, int splits, cudaStream_t stream)
+{
+    using C = SwapCfg<NT>;
+    CUtensorMap tmW, tmX;
+    if (!make_operand_map(&tmW, a.b, a.N, a.K, 128, 1, kOpBytes) ||
+        !make_operand_map(&tmX, a.a, a.M, a.K, NT, 1, kOpBytes))
+        return cudaErrorInvalidValue;
+    SwapParams p;
+    p.sa = a.sa;
+    p.sw = a.sb;
+    p.bias = static_cast<const __nv_bfloat16*>(a.bias);
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.M = static_cast<int>(a.M);
+    p.N = static_cast<int>(a.N);
+    p.kb = static_cast<int>((a.K + kBlock - 1) / kBlock);
+    p.ms = static_cast<int>((a.M + 3) / 4 * 4);
+    p.splits = splits;
+    p.early_w = a.early_weights ? 1 : 0;
+    p.wait_ns = a.wait_ns;
+    p.status = a.status;
+    auto kern = gemm_fp8_swap_kernel<NT>;
+    static std::mutex mu;
+    static unsigned long long configured[64] = {};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || dev < 0 || dev >= 64)
+        return err != cudaSuccess ? err : cudaErrorInvalidDevice;
+    {
+        // per device and context, once: the shared-memory opt-in
+        std::lock_guard<std::mutex> lock(mu);
+        const unsigned long long ctx = current_context_id();
+        if (configured[dev] == 0 || configured[dev] != ctx) {
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (err != cudaSuccess)
+                return err;
+            configured[dev] = ctx;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, static_cast<unsigned>((a.N + 127) / 128), static_cast<unsigned>((a.M + NT - 1) / NT));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_act_fp8(const void* x, uint8_t* codes, float* scales, int64_t M, int64_t K,
+                                 cudaStream_t stream)
+{
+    const int kb = static_cast<int>((K + kBlock - 1) / kBlock);
+    const int64_t blocks = M * kb;
+    return launch_pdl(quant_act_fp8_kernel, dim3(static_cast<unsigned>((blocks * 16 + kThreadsQ - 1) / kThreadsQ)),
+                      dim3(kThreadsQ), 0, stream, static_cast<const __nv_bfloat16*>(x), codes, scales, blocks,
+                      static_cast<int>(M), static_cast<int>(K), kb, static_cast<int>((M + 3) / 4 * 4));
+}
+
+cudaError_t launch_quant_weight_fp8(const void* w, uint8_t* codes, float* scales, int64_t N, int64_t K,
+                                    cudaStream_t stream)
+{
+    const int kb = static_cast<int>((K + kBlock - 1) / kBlock);
+    return launch_pdl(quant_weight_fp8_kernel, dim3(static_cast<unsigned>((N + 127) / 128 * kb)), dim3(kThreadsQ), 0,
+                      stream, static_cast<const __nv_bfloat16*>(w), codes, scales, N, static_cast<int>(K), kb);
+}
+
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream)
+{
+    const int64_t kb = (a.K + kBlock - 1) / kBlock;
+    const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+    const int64_t tiles = (a.N + 127) / 128 * ((a.M + nt - 1) / nt);
+    // split K while the tiles leave SMs idle (two CTAs fit an SM) and every
+    // part keeps four blocks
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * sm_count() && kb / (splits * 2) >= 4)
+        splits *= 2;
+    switch (nt) {
+    case 16: return launch_swap<16>(a, splits, stream);
+    case 32: return launch_swap<32>(a, splits, stream);
+    case 64: return launch_swap<64>(a, splits, stream);
+    default: return launch_swap<128>(a, splits, stream);
+    }
+}
+
+}  // namespace fp4lin

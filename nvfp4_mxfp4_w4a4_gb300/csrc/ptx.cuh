@@ -107,6 +107,31 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes)
     }
 }
 
+// 16 bytes global -> shared, asynchronously (zeros when `live` is false), and
+// an arrive on `bar` when every such copy of this thread so far has landed
+// (counted among the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool live)
+{
+    const uint32_t bytes = live ? 16u : 0u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Four floats of the shared memory of a CTA of the cluster (address from mapa_shared).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
 // 2-D tiled load of one box into shared memory; completion is signalled as
 // transaction bytes on `bar`.  c0 is the innermost coordinate (bytes here).
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,
@@ -275,6 +300,19 @@ __device__ __forceinline__ void tc_mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc,
         : "memory");
 }
 
+// D(tmem) (+)= A(smem) * B(smem)^T with 8-bit floating-point operands and no
+// block scales (K = 32 per instruction).
+__device__ __forceinline__ void tc_mma_f8f6f4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Each lane of the warp reads 32 consecutive 32-bit columns of its own
 // TMEM lane (lane = 32 * (warp % 4) + laneid).
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t* r)
@@ -415,6 +453,18 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc
         : "memory");
 }
 
+// The 256-row form of tc_mma_f8f6f4 for a CTA pair (issued by the leader only).
+__device__ __forceinline__ void tc_mma_f8f6f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                   uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on the mbarrier at this shared offset in every CTA of `mask`
 // when the pair operations this thread issued before have completed.
 __device__ __forceinline__ void tc_commit_pair_multicast(uint64_t* bar, uint16_t mask)
@@ -478,6 +528,12 @@ constexpr uint32_t kTypeE2M1 = 5;
 __host__ __device__ constexpr uint32_t idesc_mxf8f6f4(uint32_t m, uint32_t n, uint32_t a_type, uint32_t b_type)
 {
     return (a_type << 7) | (b_type << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24);
+}
+
+// kind::f8f6f4 (no block scales): fp32 accumulator (1 in bits 4-5), E4M3 A and B.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t m, uint32_t n)
+{
+    return (1u << 4) | (kTypeE4M3 << 7) | (kTypeE4M3 << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 __device__ __forceinline__ uint32_t idesc_with_sf_id(uint32_t idesc, uint32_t sf_id)

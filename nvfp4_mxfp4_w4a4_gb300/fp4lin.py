@@ -39,6 +39,10 @@ SYMBOLS = (
     "fp4_smooth_prepare", "fp4_quant_act_mxfp4_smooth", "fp4_quant_act_mxfp8_smooth",
     "fp4_linear_workspace_size", "fp4_linear", "fp4_linear_grouped_workspace_size", "fp4_linear_grouped",
     "fp4_debug_set_wait_fault", "fp4_quant_dualscale", "fp4_gemm_mxfp4_dualscale",
+    "fp4_fp8_act_scale_bytes", "fp4_quant_act_fp8_b128", "fp4_quant_weight_fp8_b128", "fp4_gemm_fp8_b128",
+    "fp4_linear_fp8_b128_workspace_size", "fp4_linear_fp8_b128", "fp4_rope_table", "fp4_rope",
+    "fp4_kv_code_bytes", "fp4_kv_scale_bytes", "fp4_kv_append", "fp4_kv_read",
+    "fp4_kv_attention_workspace_size", "fp4_kv_attention",
 )
 
 
@@ -63,6 +67,40 @@ class fp4_linear_opts(ctypes.Structure):
 FP4_ACT_MXFP4 = 0
 FP4_ACT_MXFP8 = 1
 FP4_LINEAR_FUSED_QUANT = 2
+
+FP4_ROPE_HALF = 0
+FP4_ROPE_INTERLEAVED = 1
+FP4_ROPE_INVERSE = 1
+FP4_ROPE_UNSCALED = 0
+FP4_ROPE_LINEAR = 1
+FP4_ROPE_BY_PARTS = 2
+
+
+class fp4_rope_params(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class fp4_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_positions", ctypes.c_int64),
+                ("turns_fast", ctypes.c_double), ("turns_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class fp4_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class fp4_kv_attention_args(ctypes.Structure):
+    _fields_ = [("q_bf16", ctypes.c_void_p), ("out_bf16", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+                ("context_lens", ctypes.c_void_p), ("q_offsets", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+                ("mask_words", ctypes.c_int32), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int32), ("max_draft", ctypes.c_int32), ("max_seq_len", ctypes.c_int64),
+                ("softmax_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -118,6 +156,23 @@ def load(path: str = LIB_PATH):
             "fp4_linear_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, ctypes.POINTER(fp4_linear_opts)]),
             "fp4_linear": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, ctypes.c_size_t,
                                           ctypes.POINTER(fp4_linear_opts), _p]),
+            "fp4_fp8_act_scale_bytes": (ctypes.c_size_t, [_i64, _i64]),
+            "fp4_quant_act_fp8_b128": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _p]),
+            "fp4_quant_weight_fp8_b128": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _p]),
+            "fp4_gemm_fp8_b128": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
+            "fp4_linear_fp8_b128_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64]),
+            "fp4_linear_fp8_b128": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, ctypes.c_size_t, _p]),
+            "fp4_rope_table": (ctypes.c_int, [_p, _i64, _i32, ctypes.c_double, ctypes.POINTER(fp4_rope_scaling), _p]),
+            "fp4_rope": (ctypes.c_int, [_p, _p, _p, ctypes.POINTER(fp4_rope_params), _i64, _i32, _i32, _i64, _i64, _i64,
+                                        _i64, _p]),
+            "fp4_kv_code_bytes": (ctypes.c_size_t, [ctypes.POINTER(fp4_kv_cache)]),
+            "fp4_kv_scale_bytes": (ctypes.c_size_t, [ctypes.POINTER(fp4_kv_cache)]),
+            "fp4_kv_append": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), _p, _p, _i64, _i64, _i64, _i64, _i64, _p,
+                                             ctypes.POINTER(fp4_rope_params), _p, _p]),
+            "fp4_kv_read": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), _p, _i64, _p, _i32, _i64, _p, _p, _p]),
+            "fp4_kv_attention_workspace_size": (ctypes.c_size_t, [_i32, _i64, _i32, _i32, _i32, _i64, _i32]),
+            "fp4_kv_attention": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), ctypes.POINTER(fp4_kv_attention_args), _p,
+                                                ctypes.c_size_t, _p]),
             "fp4_linear_grouped_workspace_size": (ctypes.c_size_t, [_i64, _i32, _i64]),
             "fp4_linear_grouped": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _p, _p, _p, _i64, _i64, _p, ctypes.c_size_t,
                                                   ctypes.POINTER(fp4_quant_opts), _p]),
@@ -390,3 +445,140 @@ def fp4_gemm_mxfp4_dualscale(a, sa, b, sb, coarse, bias_bf16, out_bf16, M, N, K,
     st = load().fp4_gemm_mxfp4_dualscale(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(coarse), _ptr(bias_bf16),
                                          _ptr(out_bf16), M, N, K, _ptr(workspace), workspace_bytes, _stream(stream))
     _check(st, "fp4_gemm_mxfp4_dualscale")
+
+
+# ----------------------------------------------------- around the FP4 linear
+
+
+def fp4_fp8_act_scale_bytes(M, K):
+    return load().fp4_fp8_act_scale_bytes(M, K)
+
+
+def fp4_quant_act_fp8_b128(x_bf16, codes, scales, M, K, stream=None):
+    """scales: float32 [ceil(K / 128)][M rounded up to 4]."""
+    _check(load().fp4_quant_act_fp8_b128(_ptr(x_bf16), _ptr(codes), _ptr(scales), M, K, _stream(stream)),
+           "fp4_quant_act_fp8_b128")
+
+
+def fp4_quant_weight_fp8_b128(w_bf16, codes, scales, N, K, stream=None):
+    """scales: float32 [ceil(N / 128)][ceil(K / 128)]."""
+    _check(load().fp4_quant_weight_fp8_b128(_ptr(w_bf16), _ptr(codes), _ptr(scales), N, K, _stream(stream)),
+           "fp4_quant_weight_fp8_b128")
+
+
+def fp4_gemm_fp8_b128(a, sa, b, sb, bias_bf16, out_bf16, M, N, K, stream=None):
+    _check(load().fp4_gemm_fp8_b128(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(bias_bf16), _ptr(out_bf16), M, N, K,
+                                    _stream(stream)), "fp4_gemm_fp8_b128")
+
+
+def fp4_linear_fp8_b128_workspace_size(M, N, K):
+    return load().fp4_linear_fp8_b128_workspace_size(M, N, K)
+
+
+def fp4_linear_fp8_b128(x_bf16, b, sb, bias_bf16, out_bf16, M, N, K, workspace, workspace_bytes=None, stream=None):
+    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check(load().fp4_linear_fp8_b128(_ptr(x_bf16), _ptr(b), _ptr(sb), _ptr(bias_bf16), _ptr(out_bf16), M, N, K,
+                                      _ptr(workspace), nbytes, _stream(stream)), "fp4_linear_fp8_b128")
+
+
+class rope_params:
+    """fp4_rope_params of a table tensor [positions, rot_dim] (kept alive)."""
+
+    def __init__(self, table, rot_dim, layout=FP4_ROPE_HALF, inverse=False):
+        self.table = table
+        self.struct = fp4_rope_params(table.data_ptr(), table.shape[0], rot_dim, layout,
+                                      FP4_ROPE_INVERSE if inverse else 0)
+        self.ref = ctypes.byref(self.struct)
+
+
+class kv_cache:
+    """fp4_kv_cache of four uint8 tensors (kept alive): codes [pages, kv_heads,
+    page_size, head_dim or head_dim / 2], scales [pages, kv_heads, page_size,
+    head_dim / 32]."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, page_size, format):
+        self.tensors = (k_codes, k_scales, v_codes, v_scales)
+        for t in self.tensors:
+            if not t.is_contiguous():
+                raise ValueError("cache tensors are contiguous")
+        pages, heads, page, width = k_codes.shape
+        dim = width if format == FP4_ACT_MXFP8 else 2 * width
+        if page != page_size or v_codes.shape != k_codes.shape or any(
+                s.shape != (pages, heads, page, dim // 32) for s in (k_scales, v_scales)):
+            raise ValueError("cache tensors do not belong together")
+        self.struct = fp4_kv_cache(*(t.data_ptr() for t in self.tensors), pages, page_size, heads, dim, format)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _strides(t):
+    """(token, head) strides of a [tokens, heads, dim] tensor with contiguous heads."""
+    a, b, c = t.stride()
+    if c != 1 and t.shape[2] != 1:
+        raise ValueError("the elements of a head are contiguous")
+    return a, b
+
+
+def fp4_rope_table(table, positions, rot_dim, base, kind=FP4_ROPE_UNSCALED, factor=1.0, original_positions=0,
+                   turns_fast=32.0, turns_slow=1.0, magnitude=1.0, stream=None):
+    """Fills table float32 [positions, rot_dim] on the device."""
+    sc = fp4_rope_scaling(kind, factor, original_positions, turns_fast, turns_slow, magnitude)
+    _check(load().fp4_rope_table(_ptr(table), positions, rot_dim, base, ctypes.byref(sc), _stream(stream)),
+           "fp4_rope_table")
+
+
+def fp4_rope(x, out, positions, rope, stream=None):
+    """x, out: bf16 [tokens, heads, head_dim] with any token and head strides
+    that are multiples of 8; positions: int32 [tokens]; rope: rope_params."""
+    tokens, heads, dim = x.shape
+    if out.shape != x.shape:
+        raise ValueError("x and out have one shape")
+    xt, xh = _strides(x)
+    ot, oh = _strides(out)
+    _check(load().fp4_rope(x.data_ptr(), out.data_ptr(), positions.data_ptr(), rope.ref, tokens, heads, dim, xt, xh, ot,
+                           oh, _stream(stream)), "fp4_rope")
+
+
+def fp4_kv_append(cache, k, v, slots, rope=None, positions=None, stream=None):
+    """k, v: bf16 [tokens, kv_heads, head_dim]; slots: int64 [tokens]; with
+    `rope` the keys are rotated first (positions: int32 [tokens])."""
+    s = cache.struct
+    if k.shape != v.shape or tuple(k.shape[1:]) != (s.kv_heads, s.head_dim):
+        raise ValueError("k and v are [tokens, kv_heads, head_dim] of the cache")
+    kt, kh = _strides(k)
+    vt, vh = _strides(v)
+    _check(load().fp4_kv_append(cache.ref, k.data_ptr(), v.data_ptr(), k.shape[0], kt, kh, vt, vh, slots.data_ptr(),
+                                None if rope is None else rope.ref, _ptr(positions), _stream(stream)), "fp4_kv_append")
+
+
+def fp4_kv_read(cache, block_table, cu_lens, k_out, v_out, stream=None):
+    """block_table: int32 [batch, pages]; cu_lens: int32 [batch + 1]; k_out,
+    v_out: contiguous bf16 [rows, kv_heads, head_dim]."""
+    if not (k_out.is_contiguous() and v_out.is_contiguous()) or k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out are contiguous and have one shape")
+    _check(load().fp4_kv_read(cache.ref, block_table.data_ptr(), block_table.stride(0), cu_lens.data_ptr(),
+                              block_table.shape[0], k_out.shape[0], k_out.data_ptr(), v_out.data_ptr(),
+                              _stream(stream)), "fp4_kv_read")
+
+
+def fp4_kv_attention_workspace_size(batch, tokens, q_heads, kv_heads, head_dim, max_seq_len, max_draft):
+    return load().fp4_kv_attention_workspace_size(batch, tokens, q_heads, kv_heads, head_dim, max_seq_len, max_draft)
+
+
+def fp4_kv_attention(cache, q, out, block_table, context_lens, q_offsets, max_seq_len, max_draft, workspace=None,
+                     tree_mask=None, lse=None, softmax_scale=None, stream=None):
+    """q, out: bf16 [tokens, q_heads, head_dim]; block_table: int32 [batch,
+    pages]; context_lens: int32 [batch]; q_offsets: int32 [batch + 1];
+    tree_mask: int32 or uint32 [tokens, words] or None (causal); lse: float32
+    [tokens, q_heads] or None; softmax_scale defaults to head_dim ** -0.5."""
+    tokens, heads, dim = q.shape
+    if out.shape != q.shape or dim != cache.struct.head_dim:
+        raise ValueError("q and out are [tokens, q_heads, head_dim]")
+    qt, qh = _strides(q)
+    ot, oh = _strides(out)
+    a = fp4_kv_attention_args(q.data_ptr(), out.data_ptr(), _ptr(lse), qt, qh, ot, oh, block_table.data_ptr(),
+                              block_table.stride(0), context_lens.data_ptr(), q_offsets.data_ptr(), _ptr(tree_mask),
+                              0 if tree_mask is None else tree_mask.shape[1], block_table.shape[0], tokens, heads,
+                              max_draft, max_seq_len, dim ** -0.5 if softmax_scale is None else softmax_scale)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().fp4_kv_attention(cache.ref, ctypes.byref(a), _ptr(workspace), nbytes, _stream(stream)),
+           "fp4_kv_attention")
