@@ -677,8 +677,8 @@ FP4LIN_API fp4_status fp4_rope(const void* x_bf16, void* out_bf16, const int32_t
  * an E8M0 scale byte per 32 elements of a head (the library's OCP rule):
  *   codes   [num_pages][kv_heads][page_size][head_dim bytes, or head_dim/2]
  *   scales  [num_pages][kv_heads][page_size][head_dim/32]
- * head_dim 64 or 128; page_size a multiple of 16 up to 4096; codes 16-byte
- * aligned.  fp4_kv_code_bytes / fp4_kv_scale_bytes give the size of one of
+ * head_dim 64 or 128; page_size a multiple of 16 up to 4096; the four arrays
+ * 16-byte aligned.  fp4_kv_code_bytes / fp4_kv_scale_bytes give the size of one of
  * the two code / scale arrays.                                              */
 typedef struct {
     uint8_t* k_codes;

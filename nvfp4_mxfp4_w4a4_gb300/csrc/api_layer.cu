@@ -52,7 +52,7 @@ fp4_status check_cache(const fp4_kv_cache* c, fp4lin::KvCache* out)
     if (c->num_pages <= 0 || c->num_pages >= kMaxDim || c->page_size <= 0 || c->page_size % 16 != 0 ||
         c->page_size > 4096 || c->kv_heads <= 0 || c->kv_heads > 1024 || (c->head_dim != 64 && c->head_dim != 128))
         return FP4_ERR_SHAPE;
-    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16))
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16))
         return FP4_ERR_ALIGNMENT;
     out->k_codes = c->k_codes;
     out->k_scales = c->k_scales;

@@ -463,6 +463,347 @@ cudaError_t launch_swap(const Fp8GemmArgs& a, int splits, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
 }
 
+// ------------------------------------------------- GEMM on CTA pairs
+//
+// Large problems: 256 x 256 output tiles of a cluster of two CTAs, as the FP4
+// pair kernel (a 256-row MMA needs half the operand bytes per SM and cycle of
+// two 128-row ones).  Each CTA holds 128 rows of A and of B per stage of 128
+// K-elements, and the sums of its 128 rows x 256 columns.
+//   warp 0, 2  TMA of A and of B, counted on the leader's full barrier
+//   warp 1     TMEM; in the leader, the pair's MMAs: one scale block into one
+//              of two accumulators of 256 columns
+//   warps 4..11  promotion: warp (quad, half) owns 32 rows x 128 columns in
+//              registers, a row per lane, the 128 columns one weight block: one
+//              scale product per lane and block; then bias, bf16, TMA store
+struct PairCfg {
+    static constexpr int STAGES = 6;
+    static constexpr int BYTES = 128 * kBlock;  // of A, and of B, per stage and CTA
+    static constexpr int OFF_B = STAGES * BYTES;
+    static constexpr int OFF_EPI = 2 * STAGES * BYTES;
+    static constexpr int BOX_COLS = 64;
+    static constexpr int BOX_BYTES = 32 * BOX_COLS * 2;
+    static constexpr int OFF_BAR = OFF_EPI + 8 * BOX_BYTES;
+    static constexpr int NUM_BARS = 2 * STAGES + 4;
+    static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // + alignment slack
+    static constexpr int THREADS = 384;
+    static constexpr int REGS_LOW = 72, REGS_HIGH = 216;
+    static_assert(REGS_LOW * 128 + REGS_HIGH * 256 <= 168 * THREADS, "register split");
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct Fp8PairParams {
+    const float* sa;
+    const float* sw;
+    const __nv_bfloat16* bias;
+    int M, N;
+    int kb;       // blocks of K
+    int ms;       // row stride of sa
+    int nb;       // 128-row blocks of B
+    int m_pairs;  // 256-row tiles of A
+    int tiles;
+    unsigned long long wait_ns;
+    unsigned int* status;
+};
+
+// a.xy + b.xy * c.xy, two fused multiply-adds in one instruction
+__device__ __forceinline__ void fma2(float2& a, uint32_t b0, uint32_t b1, float2 c)
+{
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%0, %1};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "+f"(a.x), "+f"(a.y)
+        : "r"(b0), "r"(b1), "f"(c.x), "f"(c.y));
+}
+
+__global__ void __launch_bounds__(PairCfg::THREADS, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                         const __grid_constant__ CUtensorMap tmO, const Fp8PairParams p)
+{
+    using C = PairCfg;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // leader: both CTAs' operands landed
+    uint64_t* empty = full + C::STAGES;                               // stage consumed by the pair's MMAs
+    uint64_t* acc_full = empty + C::STAGES;                           // a block's sums are complete
+    uint64_t* acc_empty = acc_full + 2;                               // leader: both CTAs have read them
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    const uint64_t limit = p.wait_ns;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 16);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
+        tma_prefetch_map(&tmO);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();
+    tc_fence_after_sync();
+    grid_dependency_wait();
+    launch_dependents();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_LOW));
+        if ((warp == 0 || warp == 2) && lane == 0) {
+            // ------------------------------------------------ TMA producers
+            const bool is_a = warp == 0;
+            const CUtensorMap* map = is_a ? &tmA : &tmB;
+            uint8_t* base = smem + (is_a ? 0 : C::OFF_B);
+            const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; t < p.tiles && ok; t += pairs) {
+                const int row0 = (is_a ? (t % p.m_pairs) : (t / p.m_pairs)) * 256 + 128 * rank;
+                for (int kb = 0; kb < p.kb; ++kb, ++it) {
+                    const int s = static_cast<int>(it % C::STAGES);
+                    if (!mbar_wait_bounded(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, p.status, kStatusTimeout, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader && is_a)
+                        mbar_arrive_expect_tx(&full[s], 4u * C::BYTES);
+                    tma_load_2d_pair(base + s * C::BYTES, map, full_leader + 8u * s, kb * kBlock, row0);
+                }
+            }
+            // gave up: the pair's copies in flight land before the CTAs leave
+            if (!ok && leader && is_a)
+                for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                    mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1u, p.status, kStatusTimeout, limit);
+        } else if (warp == 1 && leader && lane == 0) {
+            // --------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc = idesc_e4m3(256, 256);
+            const uint64_t ad = smem_desc(smem_u32(smem), 16, 1024, 2);
+            const uint64_t bd = smem_desc(smem_u32(smem + C::OFF_B), 16, 1024, 2);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = pair; t < p.tiles && ok; t += pairs) {
+                for (int kb = 0; kb < p.kb; ++kb, ++it) {
+                    const uint32_t s = it % C::STAGES, b = it & 1u;
+                    if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1u, p.status, kStatusTimeout, limit) ||
+                        !mbar_wait_bounded(&acc_empty[b], ((it >> 1) & 1u) ^ 1u, p.status, kStatusTimeout, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t off = (s * C::BYTES) >> 4;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f8f6f4_pair(tmem + b * 256, ad + off + 2 * k, bd + off + 2 * k, idesc, k != 0);
+                    tc_commit_pair_multicast(&empty[s], 0x3);
+                    tc_commit_pair_multicast(&acc_full[b], 0x3);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_HIGH));
+        // ------------------------------------------- promotion and epilogue
+        const int ew = warp - 4, quad = warp & 3, half = ew >> 2;
+        const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        uint8_t* stg = smem + C::OFF_EPI + ew * C::BOX_BYTES;
+        uint32_t it = 0;
+        bool stored = false;
+        for (int t = pair; t < p.tiles; t += pairs) {
+            const int row0 = (t % p.m_pairs) * 256 + 128 * rank + 32 * quad;
+            const int n0 = (t / p.m_pairs) * 256 + 128 * half;
+            const int row = row0 + lane;
+            const float* sa = p.sa + min(row, p.ms - 1);
+            const float* sw = p.sw + static_cast<int64_t>(min(n0 / 128, p.nb - 1)) * p.kb;
+            float2 acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+                acc[j] = make_float2(0.0f, 0.0f);
+            float a_next = __ldg(sa), w_next = __ldg(sw);
+            bool ok = true;
+            for (int kb = 0; kb < p.kb; ++kb, ++it) {
+                const uint32_t b = it & 1u;
+                const float s = a_next * w_next;
+                if (kb + 1 < p.kb) {
+                    a_next = __ldg(sa + static_cast<int64_t>(kb + 1) * p.ms);
+                    w_next = __ldg(sw + kb + 1);
+                }
+                ok = mbar_wait_bounded(&acc_full[b], (it >> 1) & 1u, p.status, kStatusTimeout, limit);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t addr = tmem + lanes + b * 256 + half * 128;
+                const float2 ss = make_float2(s, s);
+                uint32_t d[2][32];
+                tmem_ld_32x32b_x32(addr, d[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait();
+                    if (c < 3) {
+                        tmem_ld_32x32b_x32(addr + 32 * (c + 1), d[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_cluster(acc_empty_leader + 8u * b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        fma2(acc[16 * c + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], ss);
+                }
+            }
+            if (!ok)
+                break;
+            // ---- bias, bf16, boxes of 32 rows x 64 columns
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col0 = n0 + c * C::BOX_COLS;
+                if (stored && lane == 0)
+                    bulk_wait_group_read0();
+                __syncwarp();
+                uint8_t* my_row = stg + lane * (C::BOX_COLS * 2);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[2 * i] = acc[c * 32 + j * 4 + i].x;
+                        f[2 * i + 1] = acc[c * 32 + j * 4 + i].y;
+                    }
+                    if (p.bias != nullptr && col0 + 8 * j < p.N) {
+                        const uint4 bb = __ldg(reinterpret_cast<const uint4*>(p.bias + col0 + 8 * j));
+                        const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f[2 * i] += __uint_as_float(bw[i] << 16);
+                            f[2 * i + 1] += __uint_as_float(bw[i] & 0xFFFF0000u);
+                        }
+                    }
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                        o[i] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    // 128-byte swizzle of the box
+                    *reinterpret_cast<uint4*>(my_row + ((j ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                // boxes past the output's edge are clipped, whole ones skipped
+                if (row0 < p.M && col0 < p.N) {
+                    if (lane == 0) {
+                        tma_store_2d(&tmO, stg, col0, row0);
+                        bulk_commit_group();
+                    }
+                    stored = true;
+                }
+            }
+        }
+        if (stored && lane == 0)
+            bulk_wait_group_read0();  // shared memory stays valid until the last store has read it
+    }
+
+    // both CTAs are done with the pair's barriers, shared memory and TMEM
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+cudaError_t launch_pair(const Fp8GemmArgs& a, cudaStream_t stream)
+{
+    using C = PairCfg;
+    CUtensorMap tmA, tmB, tmO;
+    if (!make_operand_map(&tmA, a.a, a.M, a.K, 128, 1, kOpBytes) ||
+        !make_operand_map(&tmB, a.b, a.N, a.K, 128, 1, kOpBytes) ||
+        !make_output_map(&tmO, a.out, a.M, a.N, C::BOX_COLS, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    Fp8PairParams p;
+    p.sa = a.sa;
+    p.sw = a.sb;
+    p.bias = static_cast<const __nv_bfloat16*>(a.bias);
+    p.M = static_cast<int>(a.M);
+    p.N = static_cast<int>(a.N);
+    p.kb = static_cast<int>((a.K + kBlock - 1) / kBlock);
+    p.ms = static_cast<int>((a.M + 3) / 4 * 4);
+    p.nb = static_cast<int>((a.N + 127) / 128);
+    p.m_pairs = static_cast<int>((a.M + 255) / 256);
+    const int64_t tiles = p.m_pairs * ((a.N + 255) / 256);
+    p.tiles = static_cast<int>(tiles);
+    p.wait_ns = a.wait_ns;
+    p.status = a.status;
+    // per device and context, once: the shared-memory opt-in, the register
+    // split check (setmaxnreg.inc waits until the registers it asks for are
+    // free: never launch a split that the launch's allocation cannot cover) and
+    // the number of pairs that fit on the GPU at once
+    static std::mutex mu;
+    static int resident[64] = {};
+    static unsigned long long configured[64] = {};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || dev < 0 || dev >= 64)
+        return err != cudaSuccess ? err : cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const unsigned long long ctx = current_context_id();
+        if (resident[dev] == 0 || configured[dev] != ctx) {
+            err = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (err != cudaSuccess)
+                return err;
+            cudaFuncAttributes fa;
+            err = cudaFuncGetAttributes(&fa, gemm_fp8_pair_kernel);
+            if (err != cudaSuccess)
+                return err;
+            if (fa.numRegs * C::THREADS < C::REGS_LOW * 128 + C::REGS_HIGH * 256)
+                return cudaErrorInvalidConfiguration;
+            cfg.gridDim = dim3(2);
+            cfg.numAttrs = 1;
+            int clusters = 0;
+            err = cudaOccupancyMaxActiveClusters(&clusters, gemm_fp8_pair_kernel, &cfg);
+            if (err != cudaSuccess || clusters <= 0)
+                return err != cudaSuccess ? err : cudaErrorInvalidConfiguration;
+            configured[dev] = ctx;
+            resident[dev] = std::min(clusters, sm_count() / 2);
+        }
+    }
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, resident[dev])));
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel, tmA, tmB, tmO, p);
+}
+
 }  // namespace
 
 cudaError_t launch_quant_act_fp8(const void* x, uint8_t* codes, float* scales, int64_t M, int64_t K,
@@ -486,6 +827,9 @@ cudaError_t launch_quant_weight_fp8(const void* w, uint8_t* codes, float* scales
 cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream)
 {
     const int64_t kb = (a.K + kBlock - 1) / kBlock;
+    const int64_t pair_tiles = (a.M + 255) / 256 * ((a.N + 255) / 256);
+    if (a.M > 128 && 4 * pair_tiles >= sm_count())
+        return launch_pair(a, stream);
     const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
     const int64_t tiles = (a.N + 127) / 128 * ((a.M + nt - 1) / nt);
     // split K while the tiles leave SMs idle (two CTAs fit an SM) and every

@@ -193,11 +193,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(s):
-    if s is None:
-        import torch
+_current_stream = None
 
-        return torch.cuda.current_stream().cuda_stream
+
+def _stream(s):
+    global _current_stream
+    if s is None:
+        if _current_stream is None:
+            import torch
+
+            # the handle alone, where this torch has it: the Stream object that
+            # torch.cuda.current_stream() builds costs as much as a launch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            dev = getattr(torch._C, "_cuda_getDevice", None)
+            torch.cuda.init()
+            _current_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -86,6 +86,8 @@ def test_weight_quantizer_is_exact(L, N, K):
 SHAPES = [(1, 8, 16), (1, 4096, 4096), (7, 136, 272), (16, 128, 128), (17, 264, 1040), (33, 1000, 400), (64, 2048, 1024),
           (65, 520, 640), (128, 384, 2048), (129, 256, 528), (300, 1032, 784), (515, 1288, 1296), (1024, 2048, 256),
           (2041, 1032, 400)]
+# problems with many 256 x 256 tiles (CTA pairs): odd rows, short last blocks, N ends inside a tile
+SHAPES += [(300, 5128, 1040), (1500, 2056, 272), (129, 9736, 144), (2048, 2048, 384)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
