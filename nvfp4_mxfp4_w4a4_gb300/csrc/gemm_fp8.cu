@@ -151,26 +151,33 @@ __global__ void __launch_bounds__(kThreadsQ) quant_weight_fp8_kernel(const __nv_
 //           they stream before the quantizer ahead of this kernel is done)
 //   warp 1  TMEM, MMAs: four of K = 32 per block into one of BUFS accumulators
 //   warp 2  TMA of the tokens
-//   warp 3  the tokens' scales of a block, to a ring in shared memory
+//   warp 3  a block's scales, to a ring in shared memory
 //   warps 4..  promotion: lane = weight row, NT / WGS columns per warp
+// A block has two barriers, `ready` (its operands and scales have landed and
+// its accumulator has been read) and `done` (its MMAs are complete), so that
+// the MMA thread, the one serial part, waits and commits once per block.
 template <int NT>
 struct SwapCfg {
     static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
     static constexpr int WGS = NT >= 64 ? 2 : 1;   // promotion warpgroups
     static constexpr int COLS = NT / WGS;          // columns per promotion warp
     static constexpr int BUFS = NT >= 128 ? 2 : 4;
-    static constexpr int RING = 8;                 // blocks of token scales in shared memory
+    // blocks of scales in shared memory: a slot is written when the block STAGES
+    // before is done, when the promotion is at most BUFS blocks behind that
+    static constexpr int RING = STAGES + BUFS;
+    static constexpr int SLOT = NT + 4;            // the tokens' scales, then the weight's
     static constexpr int W_BYTES = 128 * kBlock;
     static constexpr int X_BYTES = NT * kBlock;
     static constexpr int OFF_X = STAGES * W_BYTES;
     static constexpr int OFF_SA = OFF_X + STAGES * X_BYTES;
-    static constexpr int OFF_BAR = OFF_SA + RING * NT * 4;
-    static constexpr int NUM_BARS = 2 * STAGES + 2 * BUFS + 2 * RING;
+    static constexpr int OFF_BAR = OFF_SA + RING * SLOT * 4;
+    static constexpr int NUM_BARS = 2 * STAGES;
     static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // + alignment slack
     static constexpr int TMEM_COLS = BUFS * NT < 32 ? 32 : BUFS * NT;
     static constexpr int THREADS = 128 + 128 * WGS;
     static_assert(NT * 128 * 4 <= OFF_SA, "the reduction buffer reuses the stages");
+    static_assert(BUFS <= STAGES, "an accumulator's release counts on the barrier of a later block");
     static_assert(TMEM_COLS <= 256 && SMEM <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -196,12 +203,8 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
     using C = SwapCfg<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* empty = full + C::STAGES;
-    uint64_t* acc_full = empty + C::STAGES;
-    uint64_t* acc_empty = acc_full + C::BUFS;
-    uint64_t* sa_full = acc_empty + C::BUFS;
-    uint64_t* sa_empty = sa_full + C::RING;
+    uint64_t* ready = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* done = ready + C::STAGES;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x;
@@ -213,16 +216,8 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], 2);
-            mbar_init(&empty[s], 1);
-        }
-        for (int s = 0; s < C::BUFS; ++s) {
-            mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], 4 * C::WGS);
-        }
-        for (int s = 0; s < C::RING; ++s) {
-            mbar_init(&sa_full[s], 32);
-            mbar_init(&sa_empty[s], 4 * C::WGS);
+            mbar_init(&ready[s], 2 + 32 + 4 * C::WGS);  // two producers, the scales' lanes, the promotion warps
+            mbar_init(&done[s], 1);
         }
         fence_mbar_init();
         tma_prefetch_map(&tmW);
@@ -250,15 +245,12 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
             int it = 0;
             for (; it < nkb; ++it) {
                 const int s = it % C::STAGES;
-                if (!mbar_wait_bounded(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.status, kStatusTimeout, limit))
+                // (a wait that gives up has given the copies in flight its whole limit to land)
+                if (!mbar_wait_bounded(&done[s], ((it / C::STAGES) & 1) ^ 1, p.status, kStatusTimeout, limit))
                     break;
-                mbar_arrive_expect_tx(&full[s], bytes);
-                tma_load_2d(base + s * bytes, w ? &tmW : &tmX, &full[s], (kb0 + it) * kBlock, w ? n0 : m0);
+                mbar_arrive_expect_tx(&ready[s], bytes);
+                tma_load_2d(base + s * bytes, w ? &tmW : &tmX, &ready[s], (kb0 + it) * kBlock, w ? n0 : m0);
             }
-            // gave up: the copies in flight land before the CTA leaves
-            if (it < nkb)
-                for (int j = max(0, it - C::STAGES); j < it; ++j)
-                    mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1, p.status, kStatusTimeout, limit);
         }
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer
@@ -267,57 +259,56 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
             const uint64_t wd = smem_desc(smem_u32(smem), 16, 1024, 2);
             const uint64_t xd = smem_desc(smem_u32(smem + C::OFF_X), 16, 1024, 2);
             for (int it = 0; it < nkb; ++it) {
-                const int s = it % C::STAGES, b = it % C::BUFS;
-                if (!mbar_wait_bounded(&acc_empty[b], ((it / C::BUFS) & 1) ^ 1, p.status, kStatusTimeout, limit) ||
-                    !mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, p.status, kStatusTimeout, limit))
+                const int s = it % C::STAGES;
+                if (!mbar_wait_bounded(&ready[s], (it / C::STAGES) & 1, p.status, kStatusTimeout, limit))
                     break;
                 tc_fence_after_sync();
+                const uint32_t acc_addr = tmem + (it % C::BUFS) * NT;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    tc_mma_f8f6f4(tmem + b * NT, wd + ((s * C::W_BYTES + 32 * k) >> 4), xd + ((s * C::X_BYTES + 32 * k) >> 4),
+                    tc_mma_f8f6f4(acc_addr, wd + ((s * C::W_BYTES + 32 * k) >> 4), xd + ((s * C::X_BYTES + 32 * k) >> 4),
                                   idesc, k != 0);
-                tc_commit(&empty[s]);
-                tc_commit(&acc_full[b]);
+                tc_commit(&done[s]);
             }
         }
     } else if (warp == 3) {
-        // -------------------------------------------------- token scales
+        // --------------------------------------------------------- scales
         grid_dependency_wait();
         float* ring = reinterpret_cast<float*>(smem + C::OFF_SA);
+        const float* sw = p.sw + static_cast<int64_t>(blockIdx.y) * p.kb + kb0;
         for (int it = 0; it < nkb; ++it) {
-            const int r = it % C::RING;
-            const bool ok = lane != 0 || mbar_wait_bounded(&sa_empty[r], ((it / C::RING) & 1) ^ 1, p.status,
+            const int s = it % C::STAGES;
+            float* slot = ring + (it % C::RING) * C::SLOT;
+            const bool ok = lane != 0 || mbar_wait_bounded(&done[s], ((it / C::STAGES) & 1) ^ 1, p.status,
                                                            kStatusTimeout, limit);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
             if (lane < NT / 4) {
                 const int m = m0 + lane * 4;  // rows are padded to a multiple of 4
-                cp_async_16(ring + r * NT + lane * 4,
-                            p.sa + static_cast<int64_t>(kb0 + it) * p.ms + (m < p.ms ? m : 0), m < p.ms);
+                cp_async_16(slot + lane * 4, p.sa + static_cast<int64_t>(kb0 + it) * p.ms + (m < p.ms ? m : 0), m < p.ms);
             }
-            cp_async_arrive(&sa_full[r]);
+            if (lane == 0)
+                cp_async_4(slot + NT, sw + it);
+            cp_async_arrive(&ready[s]);
         }
+        cp_async_wait_all();
     } else if (warp >= 4) {
         // ------------------------------------------------------ promotion
         const int quad = warp & 3, col0 = ((warp - 4) >> 2) * C::COLS;
 #pragma unroll
         for (int j = 0; j < C::COLS; ++j)
             acc[j] = 0.0f;
-        const float* sw = p.sw + static_cast<int64_t>(blockIdx.y) * p.kb + kb0;
         const float* ring = reinterpret_cast<const float*>(smem + C::OFF_SA);
-        if (!p.early_w)
-            grid_dependency_wait();
-        float wscale = nkb > 0 ? __ldg(sw) : 0.0f;
+        if (lane == 0)  // the accumulators start free
+            for (int i = 0; i < C::BUFS; ++i)
+                mbar_arrive(&ready[i]);
         for (int it = 0; it < nkb; ++it) {
-            const int b = it % C::BUFS, r = it % C::RING;
-            const float wnext = it + 1 < nkb ? __ldg(sw + it + 1) : 0.0f;
-            const bool ok = mbar_wait_bounded(&sa_full[r], (it / C::RING) & 1, p.status, kStatusTimeout, limit) &&
-                            mbar_wait_bounded(&acc_full[b], (it / C::BUFS) & 1, p.status, kStatusTimeout, limit);
+            const bool ok = mbar_wait_bounded(&done[it % C::STAGES], (it / C::STAGES) & 1, p.status, kStatusTimeout, limit);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
             tc_fence_after_sync();
             uint32_t d[C::COLS];
-            const uint32_t addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * NT + col0;
+            const uint32_t addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (it % C::BUFS) * NT + col0;
 #pragma unroll
             for (int c = 0; c < C::COLS; c += 32) {
                 if constexpr (C::COLS >= 32)
@@ -326,22 +317,21 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
                     tmem_ld_32x32b_x16(addr, d);
             }
             tmem_ld_wait();
+            // block it + BUFS may overwrite the accumulator
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&acc_empty[b]);
+                mbar_arrive(&ready[(it + C::BUFS) % C::STAGES]);
+            const float* slot = ring + (it % C::RING) * C::SLOT;
+            const float w = slot[NT];
 #pragma unroll
             for (int j = 0; j < C::COLS; j += 4) {
-                const float4 s = *reinterpret_cast<const float4*>(ring + r * NT + col0 + j);
-                acc[j] = fmaf(__uint_as_float(d[j]), s.x * wscale, acc[j]);
-                acc[j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y * wscale, acc[j + 1]);
-                acc[j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z * wscale, acc[j + 2]);
-                acc[j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w * wscale, acc[j + 3]);
+                const float4 s = *reinterpret_cast<const float4*>(slot + col0 + j);
+                acc[j] = fmaf(__uint_as_float(d[j]), s.x * w, acc[j]);
+                acc[j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y * w, acc[j + 1]);
+                acc[j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z * w, acc[j + 2]);
+                acc[j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w * w, acc[j + 3]);
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sa_empty[r]);
-            wscale = wnext;
         }
     }
 
@@ -469,9 +459,17 @@ cudaError_t launch_swap(const Fp8GemmArgs& a, int splits, cudaStream_t stream)
 // pair kernel (a 256-row MMA needs half the operand bytes per SM and cycle of
 // two 128-row ones).  Each CTA holds 128 rows of A and of B per stage of 128
 // K-elements, and the sums of its 128 rows x 256 columns.
-//   warp 0, 2  TMA of A and of B, counted on the leader's full barrier
+//   warp 0, 2  TMA of A and of B, counted on the leader's ready barrier
 //   warp 1     TMEM; in the leader, the pair's MMAs: one scale block into one
-//              of two accumulators of 256 columns
+//              of two accumulators of 256 columns.  A barrier wait costs this
+//              thread a few hundred cycles even when the phase is complete, and
+//              a commit costs it too, against the 512 cycles of a block's MMAs;
+//              so a block has one wait and one commit: `ready` of its stage
+//              counts the operands and the promotion warps that have read the
+//              accumulator (two blocks before), and `done` of its stage tells
+//              both the producers and the promotion warps.  (2041 x 18432 x
+//              7168 with the additions left out: 177 us with separate barriers,
+//              150 us so.)
 //   warps 4..11  promotion: warp (quad, half) owns 32 rows x 128 columns in
 //              registers, a row per lane, the 128 columns one weight block: one
 //              scale product per lane and block; then bias, bf16, TMA store
@@ -483,11 +481,11 @@ struct PairCfg {
     static constexpr int BOX_COLS = 64;
     static constexpr int BOX_BYTES = 32 * BOX_COLS * 2;
     static constexpr int OFF_BAR = OFF_EPI + 8 * BOX_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 4;
+    static constexpr int NUM_BARS = 2 * STAGES;
     static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // + alignment slack
     static constexpr int THREADS = 384;
-    static constexpr int REGS_LOW = 72, REGS_HIGH = 216;
+    static constexpr int REGS_LOW = 40, REGS_HIGH = 232;
     static_assert(REGS_LOW * 128 + REGS_HIGH * 256 <= 168 * THREADS, "register split");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -526,10 +524,10 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     using C = PairCfg;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // leader: both CTAs' operands landed
-    uint64_t* empty = full + C::STAGES;                               // stage consumed by the pair's MMAs
-    uint64_t* acc_full = empty + C::STAGES;                           // a block's sums are complete
-    uint64_t* acc_empty = acc_full + 2;                               // leader: both CTAs have read them
+    // leader: both CTAs' operands have landed and their promotion warps have
+    // read the block's accumulator
+    uint64_t* ready = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* done = ready + C::STAGES;  // the block's MMAs are complete
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -539,12 +537,8 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 16);
+            mbar_init(&ready[s], 1 + 16);  // the bytes, 8 promotion warps x 2 CTAs
+            mbar_init(&done[s], 1);
         }
         fence_mbar_init();
         tma_prefetch_map(&tmA);
@@ -569,26 +563,23 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             const bool is_a = warp == 0;
             const CUtensorMap* map = is_a ? &tmA : &tmB;
             uint8_t* base = smem + (is_a ? 0 : C::OFF_B);
-            const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+            const uint32_t ready_leader = mapa_shared(smem_u32(ready), 0);
             uint32_t it = 0;
             bool ok = true;
             for (int t = pair; t < p.tiles && ok; t += pairs) {
                 const int row0 = (is_a ? (t % p.m_pairs) : (t / p.m_pairs)) * 256 + 128 * rank;
                 for (int kb = 0; kb < p.kb; ++kb, ++it) {
                     const int s = static_cast<int>(it % C::STAGES);
-                    if (!mbar_wait_bounded(&empty[s], ((it / C::STAGES) & 1u) ^ 1u, p.status, kStatusTimeout, limit)) {
+                    if (!mbar_wait_bounded(&done[s], ((it / C::STAGES) & 1u) ^ 1u, p.status, kStatusTimeout, limit)) {
                         ok = false;
                         break;
                     }
                     if (leader && is_a)
-                        mbar_arrive_expect_tx(&full[s], 4u * C::BYTES);
-                    tma_load_2d_pair(base + s * C::BYTES, map, full_leader + 8u * s, kb * kBlock, row0);
+                        mbar_arrive_expect_tx(&ready[s], 4u * C::BYTES);
+                    tma_load_2d_pair(base + s * C::BYTES, map, ready_leader + 8u * s, kb * kBlock, row0);
                 }
             }
-            // gave up: the pair's copies in flight land before the CTAs leave
-            if (!ok && leader && is_a)
-                for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                    mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1u, p.status, kStatusTimeout, limit);
+            // gave up: the copies in flight have had the wait's limit to land
         } else if (warp == 1 && leader && lane == 0) {
             // --------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = idesc_e4m3(256, 256);
@@ -599,8 +590,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
             for (int t = pair; t < p.tiles && ok; t += pairs) {
                 for (int kb = 0; kb < p.kb; ++kb, ++it) {
                     const uint32_t s = it % C::STAGES, b = it & 1u;
-                    if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1u, p.status, kStatusTimeout, limit) ||
-                        !mbar_wait_bounded(&acc_empty[b], ((it >> 1) & 1u) ^ 1u, p.status, kStatusTimeout, limit)) {
+                    if (!mbar_wait_bounded(&ready[s], (it / C::STAGES) & 1u, p.status, kStatusTimeout, limit)) {
                         ok = false;
                         break;
                     }
@@ -609,8 +599,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc_mma_f8f6f4_pair(tmem + b * 256, ad + off + 2 * k, bd + off + 2 * k, idesc, k != 0);
-                    tc_commit_pair_multicast(&empty[s], 0x3);
-                    tc_commit_pair_multicast(&acc_full[b], 0x3);
+                    tc_commit_pair_multicast(&done[s], 0x3);
                 }
             }
         }
@@ -618,59 +607,74 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_HIGH));
         // ------------------------------------------- promotion and epilogue
         const int ew = warp - 4, quad = warp & 3, half = ew >> 2;
-        const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+        const uint32_t ready_leader = mapa_shared(smem_u32(ready), 0);
+        if (lane == 0) {  // both accumulators start free
+            mbar_arrive_cluster(ready_leader);
+            mbar_arrive_cluster(ready_leader + 8u);
+        }
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         uint8_t* stg = smem + C::OFF_EPI + ew * C::BOX_BYTES;
-        uint32_t it = 0;
+        uint32_t stage = 0, phase = 0, buf = 0;
         bool stored = false;
         for (int t = pair; t < p.tiles; t += pairs) {
-            const int row0 = (t % p.m_pairs) * 256 + 128 * rank + 32 * quad;
-            const int n0 = (t / p.m_pairs) * 256 + 128 * half;
-            const int row = row0 + lane;
-            const float* sa = p.sa + min(row, p.ms - 1);
-            const float* sw = p.sw + static_cast<int64_t>(min(n0 / 128, p.nb - 1)) * p.kb;
+            const float* sa = p.sa + min((t % p.m_pairs) * 256 + 128 * rank + 32 * quad + lane, p.ms - 1);
+            const float* sw = p.sw + static_cast<int64_t>(min((t / p.m_pairs) * 2 + half, p.nb - 1)) * p.kb;
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j)
                 acc[j] = make_float2(0.0f, 0.0f);
             float a_next = __ldg(sa), w_next = __ldg(sw);
             bool ok = true;
-            for (int kb = 0; kb < p.kb; ++kb, ++it) {
-                const uint32_t b = it & 1u;
+            for (int left = p.kb; left > 0; --left) {
                 const float s = a_next * w_next;
-                if (kb + 1 < p.kb) {
-                    a_next = __ldg(sa + static_cast<int64_t>(kb + 1) * p.ms);
-                    w_next = __ldg(sw + kb + 1);
+                if (left > 1) {
+                    sa += p.ms;
+                    ++sw;
+                    a_next = __ldg(sa);
+                    w_next = __ldg(sw);
                 }
-                ok = mbar_wait_bounded(&acc_full[b], (it >> 1) & 1u, p.status, kStatusTimeout, limit);
+                ok = mbar_wait_bounded(&done[stage], phase, p.status, kStatusTimeout, limit);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const uint32_t addr = tmem + lanes + b * 256 + half * 128;
+                const uint32_t addr = tmem + lanes + buf * 256 + half * 128;
                 const float2 ss = make_float2(s, s);
+                // 32 columns at a time; the third and fourth loads run under the
+                // first two's additions, so that a block shows the load's latency once
                 uint32_t d[2][32];
                 tmem_ld_32x32b_x32(addr, d[0]);
+                tmem_ld_32x32b_x32(addr + 32, d[1]);
+                tmem_ld_wait();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait();
-                    if (c < 3) {
-                        tmem_ld_32x32b_x32(addr + 32 * (c + 1), d[(c + 1) & 1]);
-                    } else {
+                    if (c == 2) {
+                        tmem_ld_wait();
+                        // the block after the next may overwrite the accumulator
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive_cluster(acc_empty_leader + 8u * b);
+                            mbar_arrive_cluster(ready_leader +
+                                                8u * (stage + 2 < C::STAGES ? stage + 2 : stage + 2 - C::STAGES));
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         fma2(acc[16 * c + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], ss);
+                    if (c < 2)
+                        tmem_ld_32x32b_x32(addr + 64 + 32 * c, d[c]);
+                }
+                buf ^= 1u;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
             if (!ok)
                 break;
             // ---- bias, bf16, boxes of 32 rows x 64 columns
+            const int row0 = (t % p.m_pairs) * 256 + 128 * rank + 32 * quad;
+            const int n0 = (t / p.m_pairs) * 256 + 128 * half;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col0 = n0 + c * C::BOX_COLS;

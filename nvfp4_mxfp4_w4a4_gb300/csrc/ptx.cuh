@@ -107,14 +107,22 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes)
     }
 }
 
-// 16 bytes global -> shared, asynchronously (zeros when `live` is false), and
-// an arrive on `bar` when every such copy of this thread so far has landed
+// 16 or 4 bytes global -> shared, asynchronously (zeros when `live` is false),
+// and an arrive on `bar` when every such copy of this thread so far has landed
 // (counted among the barrier's expected arrivals).
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src, bool live)
 {
     const uint32_t bytes = live ? 16u : 0u;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
 }
+
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Waits until every such copy of this thread has landed.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar)
 {
