@@ -145,8 +145,10 @@ __global__ void __launch_bounds__(kThreadsQ) quant_weight_fp8_kernel(const __nv_
 // ------------------------------------------- GEMM, weights on the M side
 //
 // One CTA: 128 weight rows x NT tokens, a run of the K blocks.  The CTAs of a
-// cluster share one output tile and split K; at the end each reduces its
-// share of the tile from all CTAs' shared memory, in their order.
+// cluster share one output tile and split K; at the end each writes its sums
+// to the shared memory of the CTA that owns the token, which adds them in the
+// CTAs' order: one cluster barrier (about 1 us), no memory traffic, no second
+// kernel.
 //   warp 0  TMA of the weights (which no kernel of the same call writes, so
 //           they stream before the quantizer ahead of this kernel is done)
 //   warp 1  TMEM, MMAs: four of K = 32 per block into one of BUFS accumulators
@@ -158,10 +160,11 @@ __global__ void __launch_bounds__(kThreadsQ) quant_weight_fp8_kernel(const __nv_
 // the MMA thread, the one serial part, waits and commits once per block.
 template <int NT>
 struct SwapCfg {
-    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int STAGES = NT == 16 ? 5 : NT == 32 ? 4 : NT == 64 ? 3 : 4;
     static constexpr int WGS = NT >= 64 ? 2 : 1;   // promotion warpgroups
     static constexpr int COLS = NT / WGS;          // columns per promotion warp
-    static constexpr int BUFS = NT >= 128 ? 2 : 4;
+    static constexpr int BUFS = NT >= 64 ? 2 : 4;
+    static constexpr int CTAS = NT >= 128 ? 1 : 2;   // per SM
     // blocks of scales in shared memory: a slot is written when the block STAGES
     // before is done, when the promotion is at most BUFS blocks behind that
     static constexpr int RING = STAGES + BUFS;
@@ -169,16 +172,16 @@ struct SwapCfg {
     static constexpr int W_BYTES = 128 * kBlock;
     static constexpr int X_BYTES = NT * kBlock;
     static constexpr int OFF_X = STAGES * W_BYTES;
-    static constexpr int OFF_SA = OFF_X + STAGES * X_BYTES;
+    static constexpr int OFF_SUM = OFF_X + STAGES * X_BYTES;  // [splits][tokens of this CTA][128] floats
+    static constexpr int OFF_SA = OFF_SUM + NT * 128 * 4;
     static constexpr int OFF_BAR = OFF_SA + RING * SLOT * 4;
     static constexpr int NUM_BARS = 2 * STAGES;
     static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM = OFF_SLOT + 16 + 1024;  // + alignment slack
     static constexpr int TMEM_COLS = BUFS * NT < 32 ? 32 : BUFS * NT;
     static constexpr int THREADS = 128 + 128 * WGS;
-    static_assert(NT * 128 * 4 <= OFF_SA, "the reduction buffer reuses the stages");
     static_assert(BUFS <= STAGES, "an accumulator's release counts on the barrier of a later block");
-    static_assert(TMEM_COLS <= 256 && SMEM <= 113 * 1024, "two CTAs per SM");
+    static_assert(TMEM_COLS * CTAS <= 512 && SMEM * CTAS <= 226 * 1024, "CTAs per SM");
 };
 
 struct SwapParams {
@@ -196,7 +199,7 @@ struct SwapParams {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
+__global__ void __launch_bounds__(SwapCfg<NT>::THREADS, SwapCfg<NT>::CTAS)
     gemm_fp8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                          const SwapParams p)
 {
@@ -230,6 +233,8 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (p.splits > 1)
+        cluster_arrive();  // waited for before the first access to another CTA
     const uint32_t tmem = *tmem_slot;
     launch_dependents();
 
@@ -307,90 +312,98 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS)
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
             tc_fence_after_sync();
-            uint32_t d[C::COLS];
             const uint32_t addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + (it % C::BUFS) * NT + col0;
-#pragma unroll
-            for (int c = 0; c < C::COLS; c += 32) {
-                if constexpr (C::COLS >= 32)
-                    tmem_ld_32x32b_x32(addr + c, d + c);
-                else
-                    tmem_ld_32x32b_x16(addr, d);
-            }
-            tmem_ld_wait();
-            // block it + BUFS may overwrite the accumulator
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&ready[(it + C::BUFS) % C::STAGES]);
             const float* slot = ring + (it % C::RING) * C::SLOT;
             const float w = slot[NT];
+            constexpr int CH = C::COLS < 32 ? C::COLS : 32;
 #pragma unroll
-            for (int j = 0; j < C::COLS; j += 4) {
-                const float4 s = *reinterpret_cast<const float4*>(slot + col0 + j);
-                acc[j] = fmaf(__uint_as_float(d[j]), s.x * w, acc[j]);
-                acc[j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y * w, acc[j + 1]);
-                acc[j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z * w, acc[j + 2]);
-                acc[j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w * w, acc[j + 3]);
+            for (int c = 0; c < C::COLS; c += CH) {
+                uint32_t d[CH];
+                if constexpr (CH == 32)
+                    tmem_ld_32x32b_x32(addr + c, d);
+                else
+                    tmem_ld_32x32b_x16(addr, d);
+                tmem_ld_wait();
+                if (c + CH == C::COLS) {
+                    // block it + BUFS may overwrite the accumulator
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&ready[(it + C::BUFS) % C::STAGES]);
+                }
+#pragma unroll
+                for (int j = 0; j < CH; j += 4) {
+                    const float4 s = *reinterpret_cast<const float4*>(slot + col0 + c + j);
+                    acc[c + j] = fmaf(__uint_as_float(d[j]), s.x * w, acc[c + j]);
+                    acc[c + j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y * w, acc[c + j + 1]);
+                    acc[c + j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z * w, acc[c + j + 2]);
+                    acc[c + j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w * w, acc[c + j + 3]);
+                }
             }
         }
     }
 
     // ---------------------------------------------------- reduce and store
-    // every MMA has been read (each accumulator was waited for) and every copy
-    // has landed, so the stages' memory can hold the partial tile [NT][128]
-    __syncthreads();
-    float* tile = reinterpret_cast<float*>(smem);
+    // token r of the tile belongs to CTA r / per of the cluster
+    __syncwarp();
+    const int rows = min(NT, p.M - m0);
+    const int per = (rows + p.splits - 1) / p.splits;
+    float* sums = reinterpret_cast<float*>(smem + C::OFF_SUM);  // [splits][per][128]
+    if (p.splits > 1)
+        cluster_wait();
     if (warp >= 4) {
         const int quad = warp & 3, col0 = ((warp - 4) >> 2) * C::COLS;
+        const uint32_t mine = smem_u32(sums + split * per * 128 + quad * 32 + lane);
+        int owner = col0 / per, r = col0 - owner * per;
+        uint32_t dst = mapa_shared(mine, min(owner, p.splits - 1));
 #pragma unroll
-        for (int j = 0; j < C::COLS; ++j)
-            tile[(col0 + j) * 128 + quad * 32 + lane] = acc[j];
-    }
-    if (p.splits > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
-    {
-        // 8 outputs of a row per thread; the rows of the tile are dealt over the cluster
-        const int rows = min(NT, p.M - m0);
-        const int per = (rows + p.splits - 1) / p.splits;
-        const int r_end = min(rows, (split + 1) * per);
-        for (int i = threadIdx.x; i < per * 16; i += C::THREADS) {
-            const int r = split * per + (i >> 4), c = (i & 15) * 8;
-            if (r >= r_end || n0 + c >= p.N)
-                continue;
-            float f[8] = {};
-            const uint32_t at = smem_u32(tile + r * 128 + c);
-            for (int k = 0; k < p.splits; ++k) {
-                const uint32_t src = mapa_shared(at, k);
-                const float4 u = ld_cluster_f4(src), v = ld_cluster_f4(src + 16);
-                f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
-                f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+        for (int j = 0; j < C::COLS; ++j) {
+            if (col0 + j < rows)
+                st_cluster_f32(dst + r * 512, acc[j]);
+            if (++r == per) {
+                r = 0;
+                ++owner;
+                dst = mapa_shared(mine, min(owner, p.splits - 1));
             }
-            if (p.bias != nullptr) {
-                const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + n0 + c);
-                const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[2 * j] += __uint_as_float(bw[j] << 16);
-                    f[2 * j + 1] += __uint_as_float(bw[j] & 0xFFFF0000u);
-                }
-            }
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-                o[j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(m0 + r) * p.N + n0 + c) =
-                make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     tc_fence_before_sync();
     if (p.splits > 1)
-        cluster_sync_all();  // the peers have read this CTA's partial tile
+        cluster_sync_all();
     else
         __syncthreads();
+    // 8 outputs of a token per thread
+    const int own = max(0, min(per, rows - split * per));
+    for (int i = threadIdx.x; i < own * 16; i += C::THREADS) {
+        const int r = i >> 4, c = (i & 15) * 8;
+        if (n0 + c >= p.N)
+            continue;
+        float f[8] = {};
+#pragma unroll 2
+        for (int k = 0; k < p.splits; ++k) {
+            const float4* src = reinterpret_cast<const float4*>(sums + (k * per + r) * 128 + c);
+            const float4 u = src[0], v = src[1];
+            f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
+            f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+        }
+        if (p.bias != nullptr) {
+            const uint4 bb = *reinterpret_cast<const uint4*>(p.bias + n0 + c);
+            const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[2 * j] += __uint_as_float(bw[j] << 16);
+                f[2 * j + 1] += __uint_as_float(bw[j] & 0xFFFF0000u);
+            }
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+            o[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(m0 + split * per + r) * p.N + n0 + c) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+    }
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::TMEM_COLS);
@@ -831,15 +844,19 @@ cudaError_t launch_quant_weight_fp8(const void* w, uint8_t* codes, float* scales
 cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream)
 {
     const int64_t kb = (a.K + kBlock - 1) / kBlock;
-    const int64_t pair_tiles = (a.M + 255) / 256 * ((a.N + 255) / 256);
-    if (a.M > 128 && 4 * pair_tiles >= sm_count())
-        return launch_pair(a, stream);
     const int nt = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
     const int64_t tiles = (a.N + 127) / 128 * ((a.M + nt - 1) / nt);
-    // split K while the tiles leave SMs idle (two CTAs fit an SM) and every
-    // part keeps four blocks
+    const int64_t slots = nt == 128 ? sm_count() : 2 * sm_count();  // CTAs resident at once
+    // Tiles of 128 x 128 while they fit the GPU at once, CTA pairs beyond:
+    // 512 x 4096 x 4096 (128 tiles) 19.4 / 19.1 us, 256 x 14336 x 4096 (224)
+    // 37.8 / 21.8 us, 256 x 4096 x 4096 (64, K in two) 12.8 / 18.4 us.
+    if (a.M > 128 && tiles > slots)
+        return launch_pair(a, stream);
+    // Split K as far as one wave of CTAs goes and every part keeps two blocks:
+    // 64 x 14336 x 4096 (112 tiles, 304 slots) 23.7 / 16.8 / 22.8 us in 1 / 2 / 4
+    // parts, 1 x 4096 x 4096 (32 tiles) 13.4 / 8.8 / 7.2 / 6.8 us in 1 / 2 / 4 / 8.
     int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= 2 * sm_count() && kb / (splits * 2) >= 4)
+    while (splits < 8 && tiles * splits * 2 <= slots && kb / (splits * 2) >= 2)
         splits *= 2;
     switch (nt) {
     case 16: return launch_swap<16>(a, splits, stream);
