@@ -378,8 +378,9 @@ fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_ar
     if (!aligned(args->block_table, 4) || !aligned(args->context_lens, 4) || !aligned(args->q_offsets, 4) ||
         !aligned(args->tree_mask, 4) || !aligned(args->lse, 4) || (need > 0 && !aligned(workspace, 256)))
         return FP4_ERR_ALIGNMENT;
-    if ((st = device()) != FP4_OK)
+    if ((st = device(&a.status)) != FP4_OK)
         return st;
+    a.wait_ns = fp4lin::api_wait_limit_ns();
     a.q = args->q_bf16;
     a.out = args->out_bf16;
     a.lse = args->lse;

@@ -47,6 +47,7 @@
 
 #include "formats.cuh"
 #include "internal.h"
+#include "kv_attention.cuh"
 #include "kv_cache.h"
 #include "ptx.cuh"
 
@@ -56,34 +57,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;         // tokens a warp takes at a time
 constexpr int kStages = 3;        // steps in a warp's ring
-constexpr int kMaxSplits = 1024;  // of one context
-constexpr float kUnscale = 18446744073709551616.0f;  // 2^64
-constexpr int kScaleShift = 64;
-
-struct AttnParams {
-    KvCache cache;
-    const __nv_bfloat16* q;
-    __nv_bfloat16* out;
-    float* lse;
-    int64_t qt, qh, ot, oh;
-    const int32_t* block_table;
-    int64_t table_stride;
-    const int32_t* context_lens;
-    const int32_t* q_offsets;
-    const uint32_t* mask;
-    int mask_words;
-    int batch;
-    int T;
-    int q_heads;
-    int group;
-    int row_tiles;
-    int chunk;      // tokens per split, a multiple of kWarps * kStep
-    DivMagic page_div;
-    int max_len;    // tokens a sequence's block table row can name
-    float xscale;   // scale * log2(e)
-    float* part_o;  // [splits][T * q_heads][dim]
-    float* part_ml; // [splits][T * q_heads][2]
-};
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1)
 {
@@ -108,26 +81,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v)
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
@@ -162,37 +115,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t* out)
             "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
             : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
             : "r"(w));
-    }
-}
-
-// bf16 bits of the multiplier of a value block: 2^(s - 127) times the
-// placement's 2^120 (E4M3) or 2^126 (E2M1) times 2^-64; NaN for the NaN scale.
-template <int kFmt>
-__device__ __forceinline__ uint32_t block_multiplier(uint32_t s)
-{
-    const uint32_t field = min(s + (kFmt == kKvMxfp8 ? 120u : 126u) - kScaleShift, 254u);
-    return s == 0xFFu ? 0x7FC0u : field << 7;
-}
-
-// The codes of a word whose halves hold one element each per position, as
-// bf16 pairs (times 2^-120 / 2^-126, see above).  These integer operations run
-// on the ALU pipe at half the issue rate, so right shifts are kept few and
-// left shifts are written as multiplications, which the multiply-add pipe can
-// take.
-//   E4M3  byte 0 and 2 -> out[0], byte 1 and 3 -> out[1]
-//   E2M1  nibble j of both halves -> out[j]
-template <int kFmt>
-__device__ __forceinline__ void place_codes(uint32_t w, uint32_t* out)
-{
-    if constexpr (kFmt == kKvMxfp8) {
-        out[0] = ((w * 256u) & 0x80008000u) | ((w * 16u) & 0x07F007F0u);
-        out[1] = (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u);
-    } else {
-        const uint32_t w6 = w >> 6;
-        out[0] = ((w * 4096u) & 0x80008000u) | ((w * 64u) & 0x01C001C0u);
-        out[1] = ((w * 256u) & 0x80008000u) | ((w * 4u) & 0x01C001C0u);
-        out[2] = ((w * 16u) & 0x80008000u) | ((w6 * 16u) & 0x01C001C0u);
-        out[3] = (w & 0x80008000u) | (w6 & 0x01C001C0u);
     }
 }
 
@@ -273,7 +195,7 @@ __device__ __forceinline__ uint32_t visible16(const AttnParams& p, int64_t token
 }
 
 template <int kFmt, int kDim, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) kv_attention_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_kernel(const AttnParams p)
 {
     using S = Shape<kFmt, kDim>;
     constexpr int ROWS = 8 * NT;
@@ -729,10 +651,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(cons
         p.lse[row] = (mx + log2f(ls)) * 0.69314718055994531f;
 }
 
-// How the work is cut: column tiles per warp, row tiles per key/value head,
-// tokens per split.
+// How the work is cut: rows per tile (8 or 16: the kernel above; more: the
+// tile kernel), row tiles per key/value head, tokens per split.
 struct Plan {
-    int nt;
+    int rows;
     int row_tiles;
     int chunk;
     int splits;  // at max_seq
@@ -742,15 +664,19 @@ Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draf
 {
     Plan pl;
     const int rows = group * max_draft;
-    pl.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+    pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * pl.row_tiles;
-    // eight steps a warp at least: a context of up to 512 tokens is done without
-    // a second kernel (503 tokens, 8 heads: 9.3 us against 13 us cut in two)
-    constexpr int kMin = 8 * kWarps * kStep;
-    const int64_t want = std::max<int64_t>(1, (static_cast<int64_t>(sm_count()) * 16 + units - 1) / units);
-    int64_t chunk = (max_seq + std::min<int64_t>(want, kMaxSplits) - 1) / std::min<int64_t>(want, kMaxSplits);
-    chunk = std::max<int64_t>(kMin, (chunk + kWarps * kStep - 1) / (kWarps * kStep) * (kWarps * kStep));
+    const bool stream = pl.rows <= 16;
+    // Stream: eight steps a warp at least, so that a context of up to 512 tokens
+    // is done without a second kernel (503 tokens, 8 heads: 9.3 us against 13 us
+    // cut in two), and about 16 CTAs per SM, four of them resident (64 sequences
+    // up to 8190 tokens: 152 / 145 / 149 us with 8 / 16 / 32).  Tile: one CTA is
+    // resident, four tiles at least.
+    const int64_t least = stream ? 8 * kWarps * kStep : 4 * 128, unit = stream ? kWarps * kStep : 128;
+    const int64_t ctas = static_cast<int64_t>(sm_count()) * (stream ? 16 : 3);
+    const int64_t want = std::min<int64_t>(std::max<int64_t>(1, (ctas + units - 1) / units), kMaxSplits);
+    const int64_t chunk = std::max(least, ((max_seq + want - 1) / want + unit - 1) / unit * unit);
     pl.chunk = static_cast<int>(chunk);
     pl.splits = static_cast<int>((max_seq + chunk - 1) / chunk);
     return pl;
@@ -786,9 +712,9 @@ cudaError_t launch_stream(const AttnParams& p, const Plan& pl, cudaStream_t stre
 template <int kFmt, int kDim>
 cudaError_t launch_rows(const AttnParams& p, const Plan& pl, cudaStream_t stream)
 {
-    cudaError_t err = pl.nt == 1   ? launch_stream<kFmt, kDim, 1>(p, pl, stream)
-                      : pl.nt == 2 ? launch_stream<kFmt, kDim, 2>(p, pl, stream)
-                                   : launch_stream<kFmt, kDim, 4>(p, pl, stream);
+    cudaError_t err = pl.rows == 8    ? launch_stream<kFmt, kDim, 1>(p, pl, stream)
+                      : pl.rows == 16 ? launch_stream<kFmt, kDim, 2>(p, pl, stream)
+                                      : launch_kv_attention_tile(p, pl.rows, pl.splits, stream);
     if (err != cudaSuccess || pl.splits <= 1)
         return err;
     const int64_t rows = static_cast<int64_t>(p.T) * p.q_heads;
@@ -829,8 +755,11 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream)
     p.row_tiles = pl.row_tiles;
     p.chunk = pl.chunk;
     p.page_div = div_magic(static_cast<uint32_t>(a.cache.page_size));
+    p.group_div = div_magic(static_cast<uint32_t>(p.group));
     p.max_len = static_cast<int>(std::min<int64_t>(a.max_seq, a.table_stride * a.cache.page_size));
     p.xscale = a.scale * 1.4426950408889634f;
+    p.wait_ns = a.wait_ns;
+    p.status = a.status;
     p.part_o = static_cast<float*>(a.workspace);
     p.part_ml = p.part_o + static_cast<size_t>(pl.splits) * a.T * a.q_heads * a.cache.dim;
     if (a.cache.format == kKvMxfp8)

@@ -71,6 +71,8 @@ struct KvAttentionArgs {
     int max_draft;
     float scale;
     void* workspace;
+    unsigned int* status;
+    unsigned long long wait_ns;
 };
 
 size_t kv_attention_workspace_bytes(int batch, int64_t T, int q_heads, int kv_heads, int dim, int64_t max_seq,
