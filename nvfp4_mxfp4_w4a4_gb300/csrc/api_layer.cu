@@ -28,6 +28,8 @@ inline fp4_status device(unsigned int** status = nullptr)
 
 // ------------------------------------------------------------- FP8 linear
 
+int64_t fp8_blocks(int64_t n) { return (n + 127) / 128; }
+
 bool fp8_dims_ok(int64_t rows, int64_t K)
 {
     return rows >= 0 && K > 0 && K % 16 == 0 && rows < kMaxDim - 256 && K < kMaxDim - 256;
@@ -36,10 +38,8 @@ bool fp8_dims_ok(int64_t rows, int64_t K)
 bool fp8_shape_ok(int64_t M, int64_t N, int64_t K)
 {
     // tiles of 16 rows of M and 128 of N are grid dimensions
-    return fp8_dims_ok(M, K) && N > 0 && N % 8 == 0 && N <= 65535 * int64_t(128) && M <= 65535 * int64_t(128);
+    return fp8_dims_ok(M, K) && M * fp8_blocks(K) < kMaxDim && N > 0 && N % 8 == 0 && N <= 65535 * int64_t(128) && M <= 65535 * int64_t(128);
 }
-
-int64_t fp8_blocks(int64_t n) { return (n + 127) / 128; }
 
 // --------------------------------------------------------- cache and rope
 
@@ -123,7 +123,7 @@ size_t fp4_fp8_act_scale_bytes(int64_t M, int64_t K)
 
 fp4_status fp4_quant_act_fp8_b128(const void* x_bf16, uint8_t* codes, float* scales, int64_t M, int64_t K, void* stream)
 {
-    if (!fp8_dims_ok(M, K))
+    if (!fp8_dims_ok(M, K) || M * fp8_blocks(K) >= kMaxDim)
         return FP4_ERR_SHAPE;
     if (M == 0)
         return FP4_OK;
@@ -257,8 +257,8 @@ fp4_status fp4_rope(const void* x_bf16, void* out_bf16, const int32_t* positions
                     int64_t out_token_stride, int64_t out_head_stride, void* stream)
 {
     if (tokens < 0 || heads <= 0 || heads > 65536 || head_dim <= 0 || head_dim % 16 != 0 || head_dim > 1024 ||
-        tokens >= kMaxDim || tokens * heads >= (int64_t(1) << 32))
-        return FP4_ERR_SHAPE;
+        tokens >= kMaxDim || tokens * heads * (head_dim / 16) >= (int64_t(1) << 32) - 1024)
+        return FP4_ERR_SHAPE;  // 32-bit indexes of 16-element units
     if (tokens == 0)
         return FP4_OK;
     if (!x_bf16 || !out_bf16)
@@ -299,8 +299,8 @@ fp4_status fp4_kv_append(const fp4_kv_cache* cache, const void* k_bf16, const vo
     fp4_status st = check_cache(cache, &c);
     if (st != FP4_OK)
         return st;
-    if (tokens < 0 || tokens * c.heads >= (int64_t(1) << 31))
-        return FP4_ERR_SHAPE;
+    if (tokens < 0 || tokens >= kMaxDim || tokens * c.heads * (c.dim / 4) >= (int64_t(1) << 32) - 1024)
+        return FP4_ERR_SHAPE;  // 32-bit indexes of 8-element vectors
     if (tokens == 0)
         return FP4_OK;
     if (!k_bf16 || !v_bf16 || !slots)

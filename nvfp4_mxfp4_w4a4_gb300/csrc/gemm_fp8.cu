@@ -76,31 +76,47 @@ __device__ __forceinline__ uint2 e4m3x8(uint4 v, float inv, bool zero)
     return zero ? make_uint2(0u, 0u) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Activations: 16 lanes take one row's block of 128, 8 elements each.
+// Activations: 16 lanes take one row's block of 128, 8 elements each, and
+// kActBlocks blocks in turn with their loads started together.
+constexpr int kActBlocks = 4;
+
 __global__ void __launch_bounds__(kThreadsQ) quant_act_fp8_kernel(const __nv_bfloat16* __restrict__ x,
                                                                   uint8_t* __restrict__ codes,
-                                                                  float* __restrict__ scales, int64_t blocks, int M,
-                                                                  int K, int kb, int ms)
+                                                                  float* __restrict__ scales, uint32_t blocks, int K,
+                                                                  DivMagic per_row, int kb, int ms)
 {
     grid_dependency_wait();
     launch_dependents();
-    const int64_t item = (static_cast<int64_t>(blockIdx.x) * kThreadsQ + threadIdx.x) >> 4;
     const int lane = threadIdx.x & 15;
-    const bool live = item < blocks;
-    const int64_t row = live ? item / kb : 0;
-    const int b = static_cast<int>(live ? item - row * kb : 0);
-    const int col = b * kBlock + lane * 8;
-    const bool in = live && col < K;
-    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(x + row * K + col)) : make_uint4(0u, 0u, 0u, 0u);
-    uint32_t am = bf16x8_amax(v);
+    const uint32_t first = blockIdx.x * (kThreadsQ / 16 * kActBlocks) + (threadIdx.x >> 4);
+    uint4 v[kActBlocks];
+    uint32_t row[kActBlocks];
+    int b[kActBlocks];
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1)
-        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, d));
-    const BlockScale s = block_scale(am << 16);
-    if (in)
-        *reinterpret_cast<uint2*>(codes + row * K + col) = e4m3x8(v, s.inverse, s.inverse == 0.0f);
-    if (live && lane == 0)
-        scales[static_cast<int64_t>(b) * ms + row] = s.scale;
+    for (int i = 0; i < kActBlocks; ++i) {
+        const uint32_t item = first + i * (kThreadsQ / 16);
+        row[i] = div_by_magic(item, per_row);
+        b[i] = static_cast<int>(item - row[i] * kb);
+        const int col = b[i] * kBlock + lane * 8;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (item < blocks && col < K)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(row[i]) * K + col));
+    }
+#pragma unroll
+    for (int i = 0; i < kActBlocks; ++i) {
+        const uint32_t item = first + i * (kThreadsQ / 16);
+        uint32_t am = bf16x8_amax(v[i]);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1)
+            am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, d));
+        const BlockScale s = block_scale(am << 16);
+        const int col = b[i] * kBlock + lane * 8;
+        if (item < blocks && col < K)
+            *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(row[i]) * K + col) =
+                e4m3x8(v[i], s.inverse, s.inverse == 0.0f);
+        if (item < blocks && lane == 0)
+            scales[static_cast<int64_t>(b[i]) * ms + row[i]] = s.scale;
+    }
 }
 
 // Weights: one CTA per 128 x 128 block; the block stays in registers between
@@ -828,9 +844,10 @@ cudaError_t launch_quant_act_fp8(const void* x, uint8_t* codes, float* scales, i
 {
     const int kb = static_cast<int>((K + kBlock - 1) / kBlock);
     const int64_t blocks = M * kb;
-    return launch_pdl(quant_act_fp8_kernel, dim3(static_cast<unsigned>((blocks * 16 + kThreadsQ - 1) / kThreadsQ)),
-                      dim3(kThreadsQ), 0, stream, static_cast<const __nv_bfloat16*>(x), codes, scales, blocks,
-                      static_cast<int>(M), static_cast<int>(K), kb, static_cast<int>((M + 3) / 4 * 4));
+    constexpr int per_cta = kThreadsQ / 16 * kActBlocks;
+    return launch_pdl(quant_act_fp8_kernel, dim3(static_cast<unsigned>((blocks + per_cta - 1) / per_cta)), dim3(kThreadsQ),
+                      0, stream, static_cast<const __nv_bfloat16*>(x), codes, scales, static_cast<uint32_t>(blocks),
+                      static_cast<int>(K), div_magic(static_cast<uint32_t>(kb)), kb, static_cast<int>((M + 3) / 4 * 4));
 }
 
 cudaError_t launch_quant_weight_fp8(const void* w, uint8_t* codes, float* scales, int64_t N, int64_t K,
