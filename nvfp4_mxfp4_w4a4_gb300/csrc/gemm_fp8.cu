@@ -181,9 +181,10 @@ struct SwapCfg {
     static constexpr int COLS = NT / WGS;          // columns per promotion warp
     static constexpr int BUFS = NT >= 64 ? 2 : 4;
     static constexpr int CTAS = NT >= 128 ? 1 : 2;   // per SM
-    // blocks of scales in shared memory: a slot is written when the block STAGES
-    // before is done, when the promotion is at most BUFS blocks behind that
-    static constexpr int RING = STAGES + BUFS;
+    // blocks of scales in shared memory: a slot is written when block j - STAGES is
+    // done, which block j - STAGES - BUFS's accumulator had to be read for; the
+    // scales of that block may still be in use then, those of the one before not
+    static constexpr int RING = STAGES + BUFS + 1;
     static constexpr int SLOT = NT + 4;            // the tokens' scales, then the weight's
     static constexpr int W_BYTES = 128 * kBlock;
     static constexpr int X_BYTES = NT * kBlock;

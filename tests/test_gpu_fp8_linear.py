@@ -194,3 +194,27 @@ def test_two_calls_give_the_same_bits(L):
     L.fp4_linear_fp8_b128(x, w, s, None, b, M, N, K, work)
     assert L.fp4_get_device_status() == 0
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [1, 16, 32, 64, 128, 300])
+def test_many_calls_give_the_same_bits(L, M):
+    """Repeated calls back to back, a block's scales differing by powers of two
+    from its neighbours': a scale read of the wrong block would show."""
+    import torch
+
+    N, K = 1536, 8192
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    x = (x * torch.exp2(torch.randint(-9, 9, (K // 128,), generator=g, device="cuda").repeat_interleave(128))).bfloat16()
+    w = torch.randint(0, 120, (N, K), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.exp2(torch.randint(-9, 9, (N // 128, K // 128), generator=g, device="cuda").float())
+    work = torch.zeros(L.fp4_linear_fp8_b128_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
+    out = torch.empty((40, M, N), dtype=torch.bfloat16, device="cuda")
+    for i in range(40):
+        L.fp4_linear_fp8_b128(x, w, s, None, out[i], M, N, K, work)
+    assert L.fp4_get_device_status() == 0
+    assert all(torch.equal(out[0], out[i]) for i in range(1, 40))
+    codes, scales = _quant_act(L, bf16_bits_host(x))
+    _check(bf16_bits_host(out[39]), R.fp8_values(host(codes), host(scales)[:, :M].T, 1), R.fp8_values(host(w), host(s), 128),
+           None, K // 128)
