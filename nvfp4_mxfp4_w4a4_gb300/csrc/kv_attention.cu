@@ -551,113 +551,38 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
     }
 }
 
-// Joins the splits of a row: one CTA per row; its warps take the splits in
-// turn, and their sums are added in the warps' order.
-constexpr int kJoinWarps = 4;
-
+// Joins the splits of a row.
 template <int kDim>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(const AttnParams p)
 {
-    __shared__ float weight[kMaxSplits];
-    __shared__ float red[kJoinWarps];
-    __shared__ float part[kJoinWarps][kDim];
+    __shared__ JoinScratch<kDim> scratch;
     grid_dependency_wait();
     launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x;
     const int64_t total = static_cast<int64_t>(p.T) * p.q_heads;
     const int tok = static_cast<int>(row / p.q_heads);
     const int hq = static_cast<int>(row - static_cast<int64_t>(tok) * p.q_heads);
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(p.q_offsets + mid) <= tok)
-            lo = mid;
-        else
-            hi = mid;
-    }
     int q_start, n;
-    group_rows(p.q_offsets, lo, p.T, &q_start, &n);
+    const int b = sequence_of(p, tok);
+    group_rows(p.q_offsets, b, p.T, &q_start, &n);
     if (tok < q_start || tok >= q_start + n)
         return;
-    const int ctx = max(min(__ldg(p.context_lens + lo), p.max_len - n), 0);
+    const int ctx = max(min(__ldg(p.context_lens + b), p.max_len - n), 0);
     const int splits = min((min(ctx + n, p.max_len) + p.chunk - 1) / p.chunk, kMaxSplits);
     if (splits <= 1)
         return;  // written by the split itself
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row;
-    float mx = -INFINITY;
-    for (int s = threadIdx.x; s < splits; s += kJoinWarps * 32) {
-        const float v = ml[s * total].x;
-        weight[s] = v;
-        mx = fmaxf(mx, v);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-    if (lane == 0)
-        red[warp] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w)
-        mx = fmaxf(mx, red[w]);
-    __syncthreads();
-    float ls = 0.0f;
-    for (int s = threadIdx.x; s < splits; s += kJoinWarps * 32) {
-        // a split without a visible token has m = -inf and zero sums (or NaN sums, which count)
-        const float f = weight[s] == -INFINITY ? 1.0f : exp2_approx(weight[s] - mx);
-        weight[s] = f;
-        ls += f * ml[s * total].y;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        ls += __shfl_xor_sync(0xFFFFFFFFu, ls, d);
-    if (lane == 0)
-        red[warp] = ls;
-    __syncthreads();
-    ls = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w)
-        ls += red[w];
-    constexpr int W = kDim / 32;
-    float acc[W] = {};
-    const float* src = p.part_o + row * kDim + lane * W;
-    const int64_t stride = total * kDim;
-#pragma unroll 8
-    for (int s = warp; s < splits; s += kJoinWarps) {
-        const float f = weight[s];
-        if constexpr (W == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src + s * stride);
-            acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(src + s * stride);
-            acc[0] += f * v.x, acc[1] += f * v.y;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-        part[warp][lane * W + j] = acc[j];
-    __syncthreads();
-    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    for (int d = threadIdx.x * 2; d < kDim; d += kJoinWarps * 64) {
-        float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            a0 += part[w][d];
-            a1 += part[w][d + 1];
-        }
-        *reinterpret_cast<uint32_t*>(p.out + tok * p.ot + hq * p.oh + d) = pack2(a0 * inv, a1 * inv);
-    }
-    if (threadIdx.x == 0 && p.lse != nullptr)
-        p.lse[row] = (mx + log2f(ls)) * 0.69314718055994531f;
+    join_row<kDim>(p, &scratch, tok, hq, splits, [&](int s) { return s * total + row; });
 }
 
 // How the work is cut: rows per tile (8 or 16: the kernel above; more: the
-// tile kernel), row tiles per key/value head, tokens per split.
+// tile kernel, which cuts the contexts itself), row tiles per key/value head,
+// and for the kernel above the tokens per split.
 struct Plan {
     int rows;
     int row_tiles;
     int chunk;
     int splits;  // at max_seq
+    bool tile;
 };
 
 Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draft)
@@ -666,19 +591,18 @@ Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draf
     const int rows = group * max_draft;
     pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
+    pl.tile = pl.rows > 16;
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * pl.row_tiles;
-    const bool stream = pl.rows <= 16;
-    // Stream: eight steps a warp at least, so that a context of up to 512 tokens
-    // is done without a second kernel (503 tokens, 8 heads: 9.3 us against 13 us
-    // cut in two), and about 16 CTAs per SM, four of them resident (64 sequences
-    // up to 8190 tokens: 152 / 145 / 149 us with 8 / 16 / 32).  Tile: one CTA is
-    // resident, four tiles at least.
-    const int64_t least = stream ? 8 * kWarps * kStep : 4 * 128, unit = stream ? kWarps * kStep : 128;
-    const int64_t ctas = static_cast<int64_t>(sm_count()) * (stream ? 16 : 3);
+    // Eight steps a warp at least, so that a context of up to 512 tokens is done
+    // without a second kernel (503 tokens, 8 heads: 9.3 us against 13 us cut in
+    // two), and about 16 CTAs per SM, four of them resident (64 sequences up to
+    // 8190 tokens: 152 / 145 / 149 us with 8 / 16 / 32).
+    constexpr int64_t least = 8 * kWarps * kStep, unit = kWarps * kStep;
+    const int64_t ctas = static_cast<int64_t>(sm_count()) * 16;
     const int64_t want = std::min<int64_t>(std::max<int64_t>(1, (ctas + units - 1) / units), kMaxSplits);
     const int64_t chunk = std::max(least, ((max_seq + want - 1) / want + unit - 1) / unit * unit);
     pl.chunk = static_cast<int>(chunk);
-    pl.splits = static_cast<int>((max_seq + chunk - 1) / chunk);
+    pl.splits = pl.tile ? 1 : static_cast<int>((max_seq + chunk - 1) / chunk);
     return pl;
 }
 
@@ -710,11 +634,11 @@ cudaError_t launch_stream(const AttnParams& p, const Plan& pl, cudaStream_t stre
 }
 
 template <int kFmt, int kDim>
-cudaError_t launch_rows(const AttnParams& p, const Plan& pl, cudaStream_t stream)
+cudaError_t launch_rows(const AttnParams& p, const Plan& pl, void* workspace, cudaStream_t stream)
 {
     cudaError_t err = pl.rows == 8    ? launch_stream<kFmt, kDim, 1>(p, pl, stream)
                       : pl.rows == 16 ? launch_stream<kFmt, kDim, 2>(p, pl, stream)
-                                      : launch_kv_attention_tile(p, pl.rows, pl.splits, stream);
+                                      : launch_kv_attention_tile(p, pl.rows, workspace, stream);
     if (err != cudaSuccess || pl.splits <= 1)
         return err;
     const int64_t rows = static_cast<int64_t>(p.T) * p.q_heads;
@@ -728,6 +652,8 @@ size_t kv_attention_workspace_bytes(int batch, int64_t T, int q_heads, int kv_he
                                     int max_draft)
 {
     const Plan pl = make_plan(batch, kv_heads, q_heads / kv_heads, max_seq, max_draft);
+    if (pl.tile)
+        return kv_attention_tile_workspace(pl.rows, dim, batch);
     if (pl.splits <= 1)
         return 0;
     return static_cast<size_t>(pl.splits) * T * q_heads * (dim + 2) * sizeof(float);
@@ -754,6 +680,8 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream)
     p.group = a.q_heads / a.cache.heads;
     p.row_tiles = pl.row_tiles;
     p.chunk = pl.chunk;
+    p.whole = a.max_seq <= 512;
+    p.prefix = nullptr;
     p.page_div = div_magic(static_cast<uint32_t>(a.cache.page_size));
     p.group_div = div_magic(static_cast<uint32_t>(p.group));
     p.max_len = static_cast<int>(std::min<int64_t>(a.max_seq, a.table_stride * a.cache.page_size));
@@ -763,8 +691,10 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream)
     p.part_o = static_cast<float*>(a.workspace);
     p.part_ml = p.part_o + static_cast<size_t>(pl.splits) * a.T * a.q_heads * a.cache.dim;
     if (a.cache.format == kKvMxfp8)
-        return a.cache.dim == 128 ? launch_rows<kKvMxfp8, 128>(p, pl, stream) : launch_rows<kKvMxfp8, 64>(p, pl, stream);
-    return a.cache.dim == 128 ? launch_rows<kKvMxfp4, 128>(p, pl, stream) : launch_rows<kKvMxfp4, 64>(p, pl, stream);
+        return a.cache.dim == 128 ? launch_rows<kKvMxfp8, 128>(p, pl, a.workspace, stream)
+                                    : launch_rows<kKvMxfp8, 64>(p, pl, a.workspace, stream);
+    return a.cache.dim == 128 ? launch_rows<kKvMxfp4, 128>(p, pl, a.workspace, stream)
+                              : launch_rows<kKvMxfp4, 64>(p, pl, a.workspace, stream);
 }
 
 }  // namespace fp4lin

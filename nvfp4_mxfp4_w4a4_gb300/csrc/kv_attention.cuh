@@ -31,7 +31,7 @@ struct AttnParams {
     int q_heads;
     int group;
     int row_tiles;
-    int chunk;      // tokens per split, a multiple of 64 (stream) or 128 (tile)
+    int chunk;      // tokens per split (stream kernel)
     DivMagic page_div;  // by the page size
     DivMagic group_div;  // by the query heads per key/value head
     int max_len;    // tokens a sequence's block table row can name
@@ -40,11 +40,15 @@ struct AttnParams {
     float* part_ml; // [splits][T * q_heads][2]
     unsigned long long wait_ns;  // limit of the bounded device waits, and where they report
     unsigned int* status;
+    // tile kernel: deal out whole units (short contexts) instead of tiles, and
+    // where it leaves the sequences' first tiles and, behind them, a run's length
+    bool whole;
+    int64_t* prefix;
 };
 
-// The kernel of many rows (kv_attention_tile.cu): row tiles of 32, 64 or 128
-// rows, chunks of a multiple of 128 tokens.
-cudaError_t launch_kv_attention_tile(const AttnParams& p, int rows, int splits, cudaStream_t stream);
+// The kernel of many rows (kv_attention_tile.cu): row tiles of 32, 64 or 128 rows.
+size_t kv_attention_tile_workspace(int rows, int dim, int batch);
+cudaError_t launch_kv_attention_tile(const AttnParams& p, int rows, void* workspace, cudaStream_t stream);
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
@@ -95,6 +99,102 @@ __device__ __forceinline__ void place_codes(uint32_t w, uint32_t* out)
         out[2] = ((w * 16u) & 0x80008000u) | ((w6 * 16u) & 0x01C001C0u);
         out[3] = (w & 0x80008000u) | (w6 & 0x01C001C0u);
     }
+}
+
+// The sequence that holds drafted token `tok`: the last that starts at or before it.
+__device__ __forceinline__ int sequence_of(const AttnParams& p, int tok)
+{
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.q_offsets + mid) <= tok)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Joining a row's parts: one CTA per row; its warps take the parts in turn,
+// and their sums are added in the warps' order.
+constexpr int kJoinWarps = 4;
+
+template <int kDim>
+struct JoinScratch {
+    float weight[kMaxSplits];
+    float red[kJoinWarps];
+    float part[kJoinWarps][kDim];
+};
+
+// index(s): where part s of the row is in part_o and part_ml, in rows.
+template <int kDim, typename Index>
+__device__ __forceinline__ void join_row(const AttnParams& p, JoinScratch<kDim>* sc, int tok, int hq, int parts, Index index)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    float mx = -INFINITY;
+    for (int s = threadIdx.x; s < parts; s += kJoinWarps * 32) {
+        const float v = ml[index(s)].x;
+        sc->weight[s] = v;
+        mx = fmaxf(mx, v);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+    if (lane == 0)
+        sc->red[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+        mx = fmaxf(mx, sc->red[w]);
+    __syncthreads();
+    float ls = 0.0f;
+    for (int s = threadIdx.x; s < parts; s += kJoinWarps * 32) {
+        // a part without a visible token has m = -inf and zero sums (or NaN sums, which count)
+        const float f = sc->weight[s] == -INFINITY ? 1.0f : exp2_approx(sc->weight[s] - mx);
+        sc->weight[s] = f;
+        ls += f * ml[index(s)].y;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        ls += __shfl_xor_sync(0xFFFFFFFFu, ls, d);
+    if (lane == 0)
+        sc->red[warp] = ls;
+    __syncthreads();
+    ls = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+        ls += sc->red[w];
+    constexpr int W = kDim / 32;
+    float acc[W] = {};
+#pragma unroll 8
+    for (int s = warp; s < parts; s += kJoinWarps) {
+        const float f = sc->weight[s];
+        const float* src = p.part_o + index(s) * kDim + lane * W;
+        if constexpr (W == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            acc[0] += f * v.x, acc[1] += f * v.y;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+        sc->part[warp][lane * W + j] = acc[j];
+    __syncthreads();
+    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+    for (int d = threadIdx.x * 2; d < kDim; d += kJoinWarps * 64) {
+        float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            a0 += sc->part[w][d];
+            a1 += sc->part[w][d + 1];
+        }
+        *reinterpret_cast<uint32_t*>(p.out + tok * p.ot + hq * p.oh + d) = pack2(a0 * inv, a1 * inv);
+    }
+    if (threadIdx.x == 0 && p.lse != nullptr)
+        p.lse[static_cast<int64_t>(tok) * p.q_heads + hq] = (mx + log2f(ls)) * 0.69314718055994531f;
 }
 
 }  // namespace fp4lin
