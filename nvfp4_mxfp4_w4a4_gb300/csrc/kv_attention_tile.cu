@@ -112,14 +112,27 @@ struct TileCfg {
     static constexpr int ROW = kFmt == kKvMxfp8 ? kDim : kDim / 2;
     static constexpr int CH = ROW / 16;
     static constexpr int SB = kDim / 32;
+    // With few rows a tile takes less time than its codes from memory, so two
+    // tiles are on their way: 64 KB (E4M3) per SM.
+    static constexpr int AHEAD = NR == 128 ? 1 : 2;
     // registers per thread of the three groups, out of 96 x 640 at launch (a
-    // softmax thread keeps COLS sums)
-    static constexpr int REGS_SOFTMAX = NR == 128 ? 136 : 120, REGS_CONVERT = NR == 128 ? 88 : 96,
-                         REGS_MMA = NR == 128 ? 24 : 40;
+    // softmax thread keeps COLS sums, a converter AHEAD tiles' codes)
+    static constexpr int REGS_SOFTMAX = NR == 128 ? 136 : NR == 64 ? 104 : 88,
+                         REGS_CONVERT = NR == 128 ? 88 : NR == 64 ? 120 : 136, REGS_MMA = NR == 128 ? 24 : 32;
     static constexpr int REGS = 256 * REGS_SOFTMAX + 256 * REGS_CONVERT + 128 * REGS_MMA;
     static_assert(REGS <= 96 * kThreads, "register split");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
+
+// The calling warpgroup's registers per thread, from 96 at launch.
+template <int kRegs>
+__device__ __forceinline__ void set_registers()
+{
+    if constexpr (kRegs > 96)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+    else if constexpr (kRegs < 96)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // Element that is stored at position `pos` of a head.
 template <int kFmt>
@@ -135,6 +148,7 @@ struct Walk {
     int ctx, len, n, q_start;
     int lo;    // first tile of the CTA's run in this unit
     int lead;  // places of the unit's start that lie in the run
+    int head;
 
     __device__ __forceinline__ void sequence(const AttnParams& p)
     {
@@ -155,6 +169,7 @@ struct Walk {
             unit = 0;
             sequence(p);
         }
+        head = row_tiles > 0 ? unit / row_tiles : 0;
     }
     // Tiles of this unit in a run with `left` places to go, which it takes away.
     __device__ __forceinline__ int run(const AttnParams& p, int64_t& left) const
@@ -167,13 +182,13 @@ struct Walk {
         left -= lead + max(here, int64_t(0));
         return static_cast<int>(max(here, int64_t(0)));
     }
-    __device__ __forceinline__ int head() const { return unit / row_tiles; }
-    __device__ __forceinline__ int row0() const { return (unit - unit / row_tiles * row_tiles) * NR; }
+    __device__ __forceinline__ int row0() const { return (unit - head * row_tiles) * NR; }
 };
 
 // A tile for the converters.
 struct TileRef {
-    int t0, ctx, len, head, page[2];
+    int t0, len, head, page[2];
+    bool edge;  // (values) not all its tokens are context
 };
 
 template <int kFmt, int kDim, int NR>
@@ -261,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             const int64_t off = scan->offset;
             const int length = p.whole ? 1 : w.tiles + kUnitTiles;
             w.unit = static_cast<int>(off / length);
+            w.head = w.unit / w.row_tiles;
             const int in_unit = static_cast<int>(off - static_cast<int64_t>(w.unit) * length);
             w.lead = max(kUnitTiles - in_unit, 0);
             w.lo = p.whole ? 0 : max(in_unit - kUnitTiles, 0);
@@ -309,39 +325,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
 
     if (warp >= 16) {
         // ----------------------------------------------------- MMA issuers
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_MMA));
-        if (warp <= 17 && lane == 0) {
-            const bool scores = warp == 16;
-            const uint64_t ad = smem_desc(smem_u32(smem + (scores ? C::OFF_K : C::OFF_V)), scores ? 16 : kSlab, 1024, 2);
-            const uint64_t bd = smem_desc(smem_u32(smem + (scores ? 0 : C::OFF_P)), scores ? 16 : kSlab, 1024, 2);
-            uint64_t* ready = scores ? s_ready : pv_ready;
-            uint64_t* done = scores ? s_done : pv_done;
+        set_registers<C::REGS_MMA>();
+        // (the whole warp walks the loop and one elected lane issues: the operands
+        // of the MMAs then stay in uniform registers)
+        if (warp == 16) {
+            constexpr uint32_t idesc = idesc_bf16(128, NR, 0, 0);
+            const uint64_t kd = smem_desc(smem_u32(smem + C::OFF_K), 16, 1024, 2);
+            const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2);
             for (uint32_t g = 0, end = *total_tiles; g < end; ++g) {
                 const uint32_t f = g & 1u;
-                if (!mbar_wait_bounded(&ready[f], (g >> 1) & 1u, p.status, kStatusTimeout, limit))
+                ok = mbar_wait_bounded(&s_ready[f], (g >> 1) & 1u, p.status, kStatusTimeout, limit);
+                if (!__all_sync(0xFFFFFFFFu, ok))
                     break;
                 tc_fence_after_sync();
-                const uint64_t af = ad + ((f * C::SLABS * kSlab) >> 4);
-                if (scores) {
-                    constexpr uint32_t idesc = idesc_bf16(128, NR, 0, 0);
+                const uint64_t kf = kd + ((f * C::SLABS * kSlab) >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kDim / 16; ++k)
-                        tc_mma_f16(tmem + f * NR, af + (((k >> 2) * kSlab + 32 * (k & 3)) >> 4),
-                                   bd + (((k >> 2) * (NR * 128) + 32 * (k & 3)) >> 4), idesc, k != 0);
-                } else {
-                    constexpr uint32_t idesc = idesc_bf16(128, NR, 1, 1);
-                    const uint64_t pf = bd + ((f * C::P_SLABS * kSlab) >> 4);
-                    const uint32_t add = unit_start[f] ? 0u : 1u;
+                        tc_mma_f16(tmem + f * NR, kf + (((k >> 2) * kSlab + 32 * (k & 3)) >> 4),
+                                   qd + (((k >> 2) * (NR * 128) + 32 * (k & 3)) >> 4), idesc, k != 0);
+                    tc_commit(&s_done[f]);
+                }
+                __syncwarp();
+            }
+        } else if (warp == 17) {
+            constexpr uint32_t idesc = idesc_bf16(128, NR, 1, 1);
+            const uint64_t vd = smem_desc(smem_u32(smem + C::OFF_V), kSlab, 1024, 2);
+            const uint64_t pd = smem_desc(smem_u32(smem + C::OFF_P), kSlab, 1024, 2);
+            for (uint32_t g = 0, end = *total_tiles; g < end; ++g) {
+                const uint32_t f = g & 1u;
+                ok = mbar_wait_bounded(&pv_ready[f], (g >> 1) & 1u, p.status, kStatusTimeout, limit);
+                if (!__all_sync(0xFFFFFFFFu, ok))
+                    break;
+                tc_fence_after_sync();
+                const uint64_t vf = vd + ((f * C::SLABS * kSlab) >> 4), pf = pd + ((f * C::P_SLABS * kSlab) >> 4);
+                const uint32_t add = unit_start[f] ? 0u : 1u;
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTile / 16; ++k)
-                        tc_mma_f16(tmem_o, af + ((2048 * k) >> 4), pf + ((2048 * k) >> 4), idesc, k ? 1u : add);
+                        tc_mma_f16(tmem_o, vf + ((2048 * k) >> 4), pf + ((2048 * k) >> 4), idesc, k ? 1u : add);
+                    tc_commit(&pv_done[f]);
                 }
-                tc_commit(&done[f]);
+                __syncwarp();
             }
         }
     } else if (warp >= kSoftmaxWarps) {
         // --------------------------------------------- codes -> bf16 tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONVERT));
+        set_registers<C::REGS_CONVERT>();
         // 16-byte chunks of the codes, one per lane.  Eight lanes in a row store to
         // one slab, for tokens whose swizzles differ, so that their 16-byte pieces
         // fall in different banks.
@@ -354,123 +384,150 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
         const uint8_t* codes = (value ? p.cache.v_codes : p.cache.k_codes) + sub * C::ROW + chunk * 16;
         const uint8_t* scales =
             (value ? p.cache.v_scales : p.cache.k_scales) + sub * C::SB + (kFmt == kKvMxfp8 ? chunk / 2 : chunk);
-        uint8_t* dst = smem + (value ? C::OFF_V : C::OFF_K);
+        // where the lane's 16-byte pieces of its first token go
+        constexpr int PIECES = kFmt == kKvMxfp8 ? 2 : 4;
+        uint32_t at_piece[PIECES];
+#pragma unroll
+        for (int h = 0; h < PIECES; ++h) {
+            const int piece = PIECES * chunk + h;
+            at_piece[h] = smem_u32(smem + (value ? C::OFF_V : C::OFF_K)) + (piece >> 3) * kSlab + (w32 + sub) * 128 +
+                          (((piece & 7) ^ (sub & 7)) << 4);
+        }
         uint64_t* full = value ? pv_ready : s_ready;
         uint64_t* freed = value ? pv_done : s_done;
-        uint4 raw[C::CH];
-        uint32_t sc[C::CH];
-        // the run's tiles in order; a tile's pages are looked up two tiles ahead
+        // The run's tiles in order: a tile's pages are looked up three tiles ahead, its
+        // tokens' places found two ahead, its codes loaded one ahead.
         Walk<NR> w = *reinterpret_cast<const Walk<NR>*>(smem + C::OFF_WALK);
         int64_t left = count;
         int tiles = w.run(p, left), at = 0;  // of the unit that the look-up is in
-        bool end = false;
-        auto look_up = [&](TileRef& r) {
+        auto look_up = [&](TileRef& r) -> bool {
             while (at == tiles) {  // (a run may hold no tile of its first and last unit)
-                if (left <= 0) {
-                    end = true;
-                    return;
-                }
+                if (left <= 0)
+                    return false;
                 w.next(p);
                 tiles = w.run(p, left);
                 at = 0;
             }
             r.t0 = (w.lo + at) * kTile;
-            r.ctx = w.ctx;
             r.len = w.len;
-            r.head = w.head();
+            r.head = w.head;
+            r.edge = value && r.t0 + kTile > w.ctx;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 r.page[h] = __ldg(p.block_table + w.b * p.table_stride +
                                   div_by_magic(min(r.t0 + w32 + 16 * h, (w.len - 1) & ~15), p.page_div));
             ++at;
+            return true;
         };
         // a group of 16 tokens lies in one page; groups past the end read the last one
-        int64_t group_at[2];
-        auto find_groups = [&](const TileRef& r) {
+        auto find_groups = [&](const TileRef& r, int64_t* group) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = min(r.t0 + w32 + 16 * h, (r.len - 1) & ~15);
                 const int off = t - static_cast<int>(div_by_magic(t, p.page_div)) * p.cache.page_size;
-                const int64_t pg = min(max(static_cast<int64_t>(r.page[h]), int64_t(0)), p.cache.pages - 1);
-                group_at[h] = (pg * p.cache.heads + r.head) * p.cache.page_size + off;
+                const int pg = min(max(r.page[h], 0), static_cast<int>(p.cache.pages - 1));
+                group[h] = (static_cast<int64_t>(pg) * p.cache.heads + r.head) * p.cache.page_size + off;
             }
         };
-        auto load = [&](int i) {
-            const int64_t from = group_at[(i * TPI) >> 4] + ((i * TPI) & 15);
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(codes + from * C::ROW));
-            sc[i] = __ldg(scales + from * C::SB);
-        };
-        TileRef next = {};
-        look_up(next);
-        const bool any = !end;
-        if (any) {
-            find_groups(next);
+        constexpr int AHEAD = C::AHEAD;  // tiles whose codes are in registers or on their way
+        uint4 raw[AHEAD][C::CH];
+        uint32_t sc[AHEAD][C::CH];
+        bool have[AHEAD], edge[AHEAD];
+        int64_t group[2];  // of the tile to load next
+        TileRef r = {};
+        bool look = look_up(r);  // the tile looked up
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            have[k] = look;
+            edge[k] = r.edge;
+            if (look) {
+                find_groups(r, group);
+#pragma unroll
+                for (int i = 0; i < C::CH; ++i) {
+                    const int64_t from = group[(i * TPI) >> 4] + ((i * TPI) & 15);
+                    sc[k][i] = __ldg(scales + from * C::SB);
+                    raw[k][i] = __ldg(reinterpret_cast<const uint4*>(codes + from * C::ROW));
+                }
+                look = look_up(r);
+            }
+        }
+        bool loads = look, edge_next = r.edge;
+        if (look) {
+            find_groups(r, group);
+            look = look_up(r);
+        }
+        // converts the tile in raw[k] into the buffers f and starts the loads of the
+        // tile AHEAD after it
+        auto convert = [&](auto slot, uint32_t f, uint32_t ph) -> bool {
+            constexpr int k = decltype(slot)::value;
+            ok = mbar_wait_bounded(&freed[f], ph, p.status, kStatusTimeout, limit);
+            if (!__all_sync(0xFFFFFFFFu, ok))
+                return false;
+            uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < C::CH; ++i)
-                load(i);
-        }
-        int t0 = next.t0, ctx = next.ctx;  // of the tile in `raw`
-        if (any)
-            look_up(next);
-        bool more = !end;
-        for (uint32_t g = 0; any; ++g) {
-            const uint32_t f = g & 1u;
-            if (more)
-                find_groups(next);
-            const int next_t0 = next.t0, next_ctx = next.ctx;
-            const bool loads = more;
-            if (more) {
-                look_up(next);
-                more = !end;
+                top = max(top, sc[k][i]);
+            // multipliers: in range for all but blocks of very large values and NaN; NaN
+            // values of an edge tile are kept out of the product (see the softmax)
+            constexpr uint32_t PLUS = (kFmt == kKvMxfp8 ? 120u : 126u) - kScaleShift;
+            if (__any_sync(0xFFFFFFFFu, top > 254u - PLUS)) {
+#pragma unroll
+                for (int i = 0; i < C::CH; ++i)
+                    sc[k][i] = edge[k] && sc[k][i] == 0xFFu ? 0u : block_multiplier<kFmt>(sc[k][i]) * 0x10001u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::CH; ++i)
+                    sc[k][i] = sc[k][i] * 0x00800080u + PLUS * 0x00800080u;
             }
-            ok = mbar_wait_bounded(&freed[f], ((g >> 1) & 1u) ^ 1u, p.status, kStatusTimeout, limit);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                break;
-            const bool edge = value && t0 + kTile > ctx;
+            const uint32_t buf = f * C::SLABS * kSlab;
 #pragma unroll
             for (int i = 0; i < C::CH; ++i) {
-                const int tok = w32 + i * TPI + sub;
-                // NaN values of an edge tile are kept out of the product (see the softmax)
-                const uint32_t mul = edge && sc[i] == 0xFFu ? 0u : block_multiplier<kFmt>(sc[i]) * 0x10001u;
-                const uint32_t c4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                uint8_t* row = dst + f * C::SLABS * kSlab + tok * 128;
-                if constexpr (kFmt == kKvMxfp8) {
+                const uint32_t c4[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
+                const uint32_t mul = sc[k][i];
+                // the token's place in its group of 8 turns the pieces: of it, i decides
+                // the bits from TPI up
+                const uint32_t turn = ((i * TPI) & 7) << 4, down = i * TPI * 128;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t a[2], c[2];
-                        place_codes<kFmt>(c4[2 * h], a);
-                        place_codes<kFmt>(c4[2 * h + 1], c);
-                        const int piece = 2 * chunk + h;
-                        *reinterpret_cast<uint4*>(row + (piece >> 3) * kSlab + (((piece & 7) ^ (tok & 7)) << 4)) =
-                            make_uint4(mul_bf16x2(a[0], mul), mul_bf16x2(a[1], mul), mul_bf16x2(c[0], mul),
-                                       mul_bf16x2(c[1], mul));
+                for (int h = 0; h < PIECES; ++h) {
+                    uint32_t o[4];
+                    if constexpr (kFmt == kKvMxfp8) {
+                        place_codes<kFmt>(c4[2 * h], o);
+                        place_codes<kFmt>(c4[2 * h + 1], o + 2);
+                    } else {
+                        place_codes<kFmt>(c4[h], o);
                     }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t a[4];
-                        place_codes<kFmt>(c4[h], a);
-                        const int piece = 4 * chunk + h;
-                        *reinterpret_cast<uint4*>(row + (piece >> 3) * kSlab + (((piece & 7) ^ (tok & 7)) << 4)) =
-                            make_uint4(mul_bf16x2(a[0], mul), mul_bf16x2(a[1], mul), mul_bf16x2(a[2], mul),
-                                       mul_bf16x2(a[3], mul));
-                    }
+                    st_shared_v4(((at_piece[h] + buf) ^ turn) + down, mul_bf16x2(o[0], mul), mul_bf16x2(o[1], mul),
+                                 mul_bf16x2(o[2], mul), mul_bf16x2(o[3], mul));
                 }
-                if (loads)
-                    load(i);
+                if (loads) {
+                    const int64_t from = group[(i * TPI) >> 4] + ((i * TPI) & 15);
+                    raw[k][i] = __ldg(reinterpret_cast<const uint4*>(codes + from * C::ROW));
+                    sc[k][i] = __ldg(scales + from * C::SB);
+                }
             }
+            find_groups(r, group);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&full[f]);
-            if (!loads)
+            have[k] = loads;
+            edge[k] = edge_next;
+            loads = look;
+            edge_next = r.edge;
+            look = look && look_up(r);
+            return true;
+        };
+        for (uint32_t g = 0;; g += 2) {
+            const uint32_t ph = ((g >> 1) & 1u) ^ 1u;
+            if (!have[0] || !convert(std::integral_constant<int, 0>(), 0, ph))
                 break;
-            t0 = next_t0;
-            ctx = next_ctx;
+            constexpr int second = AHEAD > 1 ? 1 : 0;
+            if (!have[second] || !convert(std::integral_constant<int, second>(), 1, ph))
+                break;
         }
     } else {
         // --------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+        set_registers<C::REGS_SOFTMAX>();
         // the two halves of the rows go their own ways within a unit
         const int quad = warp & 3, half = warp >> 2, col0 = half * C::COLS;
         const int token = quad * 32 + lane;  // of the tile
@@ -501,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 named_barrier_sync(5, kSoftmaxWarps * 32);
                 continue;
             }
-            const int head = wk.head(), row0 = wk.row0(), n = wk.n, ctx = wk.ctx, len = wk.len, b = wk.b;
+            const int head = wk.head, row0 = wk.row0(), n = wk.n, ctx = wk.ctx, len = wk.len, b = wk.b;
             const int q_start = wk.q_start, lo = wk.lo;
             const int rows = min(NR, n * p.group - row0);
 
