@@ -552,10 +552,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
 }
 
 // Joins the splits of a row.
+constexpr int kJoinWarps = 4;
+
 template <int kDim>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(const AttnParams p)
 {
-    __shared__ JoinScratch<kDim> scratch;
+    __shared__ JoinScratch<kDim, kJoinWarps> scratch;
     grid_dependency_wait();
     launch_dependents();
     const int64_t row = blockIdx.x;
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(cons
     const int splits = min((min(ctx + n, p.max_len) + p.chunk - 1) / p.chunk, kMaxSplits);
     if (splits <= 1)
         return;  // written by the split itself
-    join_row<kDim>(p, &scratch, tok, hq, splits, [&](int s) { return s * total + row; });
+    join_row<kDim, kJoinWarps>(p, &scratch, tok, hq, splits, [&](int s) { return s * total + row; });
 }
 
 // How the work is cut: rows per tile (8 or 16: the kernel above; more: the

@@ -116,19 +116,19 @@ __device__ __forceinline__ int sequence_of(const AttnParams& p, int tok)
 }
 
 // Joining a row's parts: one CTA per row; its warps take the parts in turn,
-// and their sums are added in the warps' order.
-constexpr int kJoinWarps = 4;
-
-template <int kDim>
+// and their sums are added in the warps' order.  Four warps for rows with many
+// parts, one where most rows have a few (their look-ups' latency, not the
+// bytes, sets the time: 6000 rows of three parts 13 us with four warps a row).
+template <int kDim, int kWarps>
 struct JoinScratch {
     float weight[kMaxSplits];
-    float red[kJoinWarps];
-    float part[kJoinWarps][kDim];
+    float red[kWarps];
+    float part[kWarps][kDim];
 };
 
 // index(s): where part s of the row is in part_o and part_ml, in rows.
-template <int kDim, typename Index>
-__device__ __forceinline__ void join_row(const AttnParams& p, JoinScratch<kDim>* sc, int tok, int hq, int parts, Index index)
+template <int kDim, int kJoinWarps, typename Index>
+__device__ __forceinline__ void join_row(const AttnParams& p, JoinScratch<kDim, kJoinWarps>* sc, int tok, int hq, int parts, Index index)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);

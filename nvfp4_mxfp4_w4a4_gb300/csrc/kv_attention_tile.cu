@@ -888,10 +888,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
 }
 
 // Joins the parts of the rows whose unit fell to several CTAs.
-template <int kDim, int NR>
+template <int kDim, int NR, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_tile_join_kernel(const AttnParams p)
 {
-    __shared__ JoinScratch<kDim> scratch;
+    __shared__ JoinScratch<kDim, kJoinWarps> scratch;
     grid_dependency_wait();
     launch_dependents();
     const int64_t row = blockIdx.x;
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_tile_join_kernel
     const int c0 = static_cast<int>(from / per), c1 = static_cast<int>((from + w.tiles - 1) / per);
     if (c0 == c1)
         return;  // written by its CTA
-    join_row<kDim>(p, &scratch, tok, hq, c1 - c0 + 1, [&](int s) -> int64_t {
+    join_row<kDim, kJoinWarps>(p, &scratch, tok, hq, c1 - c0 + 1, [&](int s) -> int64_t {
         return (2 * static_cast<int64_t>(c0) + (s == 0 ? 1 : 2 * s)) * NR + r % NR;
     });
 }
@@ -948,8 +948,10 @@ cudaError_t launch_tile(const AttnParams& p, cudaStream_t stream)
     err = launch_pdl(kern, dim3(static_cast<unsigned>(sm_count())), dim3(kThreads), C::SMEM, stream, p);
     if (err != cudaSuccess || p.whole)
         return err;
-    return launch_pdl(kv_attention_tile_join_kernel<kDim, NR>, dim3(static_cast<unsigned>(p.T) * p.q_heads),
-                      dim3(kJoinWarps * 32), 0, stream, p);
+    // parts per unit: about the runs over the units
+    const bool few = 4 * static_cast<int64_t>(p.batch) * p.cache.heads * p.row_tiles >= sm_count();
+    return launch_pdl(few ? kv_attention_tile_join_kernel<kDim, NR, 1> : kv_attention_tile_join_kernel<kDim, NR, 4>,
+                      dim3(static_cast<unsigned>(p.T) * p.q_heads), dim3(few ? 32 : 128), 0, stream, p);
 }
 
 template <int kFmt, int kDim>
