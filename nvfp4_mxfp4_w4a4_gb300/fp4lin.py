@@ -529,6 +529,11 @@ def _strides(t):
     return a, b
 
 
+def _table_stride(t):
+    """Row stride of a block table [batch, pages] (one row: its stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def fp4_rope_table(table, positions, rot_dim, base, kind=FP4_ROPE_UNSCALED, factor=1.0, original_positions=0,
                    turns_fast=32.0, turns_slow=1.0, magnitude=1.0, stream=None):
     """Fills table float32 [positions, rot_dim] on the device."""
@@ -566,7 +571,7 @@ def fp4_kv_read(cache, block_table, cu_lens, k_out, v_out, stream=None):
     v_out: contiguous bf16 [rows, kv_heads, head_dim]."""
     if not (k_out.is_contiguous() and v_out.is_contiguous()) or k_out.shape != v_out.shape:
         raise ValueError("k_out and v_out are contiguous and have one shape")
-    _check(load().fp4_kv_read(cache.ref, block_table.data_ptr(), block_table.stride(0), cu_lens.data_ptr(),
+    _check(load().fp4_kv_read(cache.ref, block_table.data_ptr(), _table_stride(block_table), cu_lens.data_ptr(),
                               block_table.shape[0], k_out.shape[0], k_out.data_ptr(), v_out.data_ptr(),
                               _stream(stream)), "fp4_kv_read")
 
@@ -587,7 +592,7 @@ def fp4_kv_attention(cache, q, out, block_table, context_lens, q_offsets, max_se
     qt, qh = _strides(q)
     ot, oh = _strides(out)
     a = fp4_kv_attention_args(q.data_ptr(), out.data_ptr(), _ptr(lse), qt, qh, ot, oh, block_table.data_ptr(),
-                              block_table.stride(0), context_lens.data_ptr(), q_offsets.data_ptr(), _ptr(tree_mask),
+                              _table_stride(block_table), context_lens.data_ptr(), q_offsets.data_ptr(), _ptr(tree_mask),
                               0 if tree_mask is None else tree_mask.shape[1], block_table.shape[0], tokens, heads,
                               max_draft, max_seq_len, dim ** -0.5 if softmax_scale is None else softmax_scale)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

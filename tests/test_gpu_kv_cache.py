@@ -254,3 +254,15 @@ def test_offsets_past_32_bits(L):
     L.fp4_kv_read(cache, table, dev(np.array([0, page], np.int32)), ko, vo)
     want = R.mx_values(*R.mx_quantize(_f32(v), R.MXFP8), R.MXFP8)[0]
     assert np.array_equal(bf16_bits_to_f64(bf16_bits_host(vo[-1])), want)
+
+
+def test_a_table_of_one_row_may_have_any_stride(L):
+    import torch
+
+    cache = _cache(L, R.MXFP8, 2, 1, 16, 64, fill=0x38)
+    cache.tensors[1].fill_(127)
+    cache.tensors[3].fill_(127)
+    table = torch.tensor([1, 0], dtype=torch.int32, device="cuda").as_strided((1, 2), (0, 1))
+    k, v = (torch.zeros((20, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    L.fp4_kv_read(cache, table, dev(np.array([0, 20], np.int32)), k, v)
+    assert torch.all(k == 1.0) and torch.all(v == 1.0)
