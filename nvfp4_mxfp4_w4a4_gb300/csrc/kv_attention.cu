@@ -35,10 +35,13 @@
 // included) are 2^-120 (E4M3) or 2^-126 (E2M1) times the code's value, and one
 // bf16 multiply by a power of two applies the block's scale.  That multiplier
 // carries 2^-64 (put back in fp32 at the end), so that it stays a finite bf16
-// up to values of 2^66.  Scores, softmax statistics and sums are fp32; the
-// probabilities are rounded to bf16 for the second product (relative 2^-8 at
-// most, of the size of the output's own rounding), their sum is taken before
-// that rounding.
+// up to values of 2^66.  Scores, softmax statistics and sums are fp32, and the
+// sum of the probabilities is taken before they are rounded to bf16 for the
+// second product.  Up to 4 rows what that rounding leaves is multiplied too, at
+// no cost: the MMA's columns 4 ... 7 repeat the rows and take it (64 sequences
+// up to 8190 tokens of MXFP8, 8 key heads: 144 us both ways).  More rows keep
+// one rounding, relative 2^-8 at most, the size of the output's own: a second
+// product costs 149 us instead of 143 at 8 rows and 212 instead of 189 at 16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -194,11 +197,14 @@ __device__ __forceinline__ uint32_t visible16(const AttnParams& p, int64_t token
     return bits & 0xFFFFu;
 }
 
-template <int kFmt, int kDim, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_kernel(const AttnParams p)
+// ROWS attention rows in COLS MMA columns; column c holds row c mod ROWS.
+template <int kFmt, int kDim, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_kernel(const AttnParams p)
 {
     using S = Shape<kFmt, kDim>;
-    constexpr int ROWS = 8 * NT;
+    constexpr int NT = ROWS <= 8 ? 1 : ROWS / 8;
+    constexpr int COLS = 8 * NT;
+    constexpr bool TWICE = ROWS < COLS;
     extern __shared__ __align__(128) float smem[];
     grid_dependency_wait();
     launch_dependents();
@@ -226,8 +232,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
     float qs[NT][2];  // the inverse power times xscale, of rows 2 qd and 2 qd + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + 8 * nt + g;
-        const bool live = 8 * nt + g < rows;
+        const int rr = (8 * nt + g) % ROWS;
+        const int r = row0 + rr;
+        const bool live = rr < rows;
         const int i = r / p.group;
         const __nv_bfloat16* src = p.q + static_cast<int64_t>(q_start + i) * p.qt +
                                    static_cast<int64_t>(head * p.group + r - i * p.group) * p.qh + qd * 8;
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int rr = 8 * nt + 2 * qd + e;
+                    const int rr = (8 * nt + 2 * qd + e) % ROWS;
                     const int i = (row0 + rr) / p.group;
                     vis[nt][e] = rr < rows ? visible16(p, q_start + i, i, n, t0 - ctx) : 0u;
                     if (t_end - t0 < kStep)
@@ -424,7 +431,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
                     }
                 }
         }
-        uint32_t pf[NT][2];  // P^T fragments: tokens 2 qd, 2 qd + 1 (and + 8) of row g
+        // P^T fragments: tokens 2 qd, 2 qd + 1 (and + 8) of column g; columns that repeat a
+        // row take what the rounding of its probabilities left
+        uint32_t pf[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float pr[4];
@@ -435,8 +444,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
                 pr[2 + e] = exp2_approx(x[nt][2 + e] - ref);
                 l[nt][e] += pr[e] + pr[2 + e];
             }
-            pf[nt][0] = movmatrix_trans(pack2(pr[0], pr[1]));
-            pf[nt][1] = movmatrix_trans(pack2(pr[2], pr[3]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t v = pack2(pr[2 * j], pr[2 * j + 1]);
+                if (TWICE) {
+                    const uint32_t rest = pack2(pr[2 * j] - __uint_as_float(v << 16),
+                                                pr[2 * j + 1] - __uint_as_float(v & 0xFFFF0000u));
+                    v = qd >= 2 ? rest : v;
+                }
+                pf[nt][j] = movmatrix_trans(v);
+            }
         }
 
         // -------------------------------------------------- O^T += V^T P^T
@@ -491,8 +508,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
     __syncthreads();  // the ring's memory takes the results
 
     // ------------------------------------------------- join the warps
-    float* sm_ml = smem;                         // [kWarps][ROWS][2]
-    float* sm_o = smem + kWarps * ROWS * 2;      // [kWarps][ROWS][kDim]
+    float* sm_ml = smem;                         // [kWarps][COLS][2]
+    float* sm_o = smem + kWarps * COLS * 2;      // [kWarps][COLS][kDim]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -503,10 +520,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
             s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
             const int r = 8 * nt + 2 * qd + e;
             if (g == 0) {
-                sm_ml[(warp * ROWS + r) * 2] = m[nt][e];
-                sm_ml[(warp * ROWS + r) * 2 + 1] = s;
+                sm_ml[(warp * COLS + r) * 2] = m[nt][e];
+                sm_ml[(warp * COLS + r) * 2 + 1] = s;
             }
-            float* dst = sm_o + (warp * ROWS + r) * kDim + g * (kDim / 8);
+            float* dst = sm_o + (warp * COLS + r) * kDim + g * (kDim / 8);
 #pragma unroll
             for (int mt = 0; mt < S::MT; ++mt) {
                 // accumulator rows g and g + 8 are elements 2 mt and 2 mt + 1 of the lane's run
@@ -520,16 +537,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) kv_attention_ker
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-            mx = fmaxf(mx, sm_ml[(w * ROWS + r) * 2]);
+            mx = fmaxf(mx, sm_ml[(w * COLS + r) * 2]);
         float a0 = 0.0f, a1 = 0.0f, ls = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float mw = sm_ml[(w * ROWS + r) * 2];
-            const float lw = sm_ml[(w * ROWS + r) * 2 + 1];
+            const float mw = sm_ml[(w * COLS + r) * 2];
+            const float lw = sm_ml[(w * COLS + r) * 2 + 1];
             // a warp without a visible token has m = -inf and zero sums (or NaN sums, which count)
             const float f = mw == -INFINITY ? 1.0f : exp2_approx(mw - mx);
-            a0 += f * sm_o[(w * ROWS + r) * kDim + d];
-            a1 += f * sm_o[(w * ROWS + r) * kDim + d + 1];
+            const float* po = sm_o + (w * COLS + r) * kDim + d;
+            a0 += f * (TWICE ? po[0] + po[ROWS * kDim] : po[0]);
+            a1 += f * (TWICE ? po[1] + po[ROWS * kDim + 1] : po[1]);
             ls += f * lw;
         }
         a0 *= kUnscale;
@@ -576,7 +594,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(cons
     join_row<kDim, kJoinWarps>(p, &scratch, tok, hq, splits, [&](int s) { return s * total + row; });
 }
 
-// How the work is cut: rows per tile (8 or 16: the kernel above; more: the
+// How the work is cut: rows per tile (4, 8 or 16: the kernel above; more: the
 // tile kernel, which cuts the contexts itself), row tiles per key/value head,
 // and for the kernel above the tokens per split.
 struct Plan {
@@ -591,7 +609,7 @@ Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draf
 {
     Plan pl;
     const int rows = group * max_draft;
-    pl.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
     pl.tile = pl.rows > 16;
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * pl.row_tiles;
@@ -608,12 +626,13 @@ Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draf
     return pl;
 }
 
-template <int kFmt, int kDim, int NT>
+template <int kFmt, int kDim, int ROWS>
 cudaError_t launch_stream(const AttnParams& p, const Plan& pl, cudaStream_t stream)
 {
     // the ring, and in the same memory the warps' results
-    constexpr int smem = std::max(kWarps * kStages * Shape<kFmt, kDim>::STEP_BYTES, kWarps * 8 * NT * (kDim + 2) * 4);
-    auto kern = kv_attention_kernel<kFmt, kDim, NT>;
+    constexpr int cols = std::max(ROWS, 8);
+    constexpr int smem = std::max(kWarps * kStages * Shape<kFmt, kDim>::STEP_BYTES, kWarps * cols * (kDim + 2) * 4);
+    auto kern = kv_attention_kernel<kFmt, kDim, ROWS>;
     if constexpr (smem > 48 * 1024) {
         // per device and context, once: the shared-memory opt-in
         static std::mutex mu;
@@ -638,8 +657,9 @@ cudaError_t launch_stream(const AttnParams& p, const Plan& pl, cudaStream_t stre
 template <int kFmt, int kDim>
 cudaError_t launch_rows(const AttnParams& p, const Plan& pl, void* workspace, cudaStream_t stream)
 {
-    cudaError_t err = pl.rows == 8    ? launch_stream<kFmt, kDim, 1>(p, pl, stream)
-                      : pl.rows == 16 ? launch_stream<kFmt, kDim, 2>(p, pl, stream)
+    cudaError_t err = pl.rows == 4    ? launch_stream<kFmt, kDim, 4>(p, pl, stream)
+                      : pl.rows == 8  ? launch_stream<kFmt, kDim, 8>(p, pl, stream)
+                      : pl.rows == 16 ? launch_stream<kFmt, kDim, 16>(p, pl, stream)
                                       : launch_kv_attention_tile(p, pl.rows, workspace, stream);
     if (err != cudaSuccess || pl.splits <= 1)
         return err;
