@@ -594,8 +594,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(cons
     join_row<kDim, kJoinWarps>(p, &scratch, tok, hq, splits, [&](int s) { return s * total + row; });
 }
 
-// How the work is cut: rows per tile (4, 8 or 16: the kernel above; more: the
-// tile kernel, which cuts the contexts itself), row tiles per key/value head,
+// How the work is cut: rows per tile (4, 8 or 16: the kernel above; 32 and 128:
+// the tile and row kernels, which cut the contexts themselves), row tiles per key/value head,
 // and for the kernel above the tokens per split.
 struct Plan {
     int rows;
@@ -603,15 +603,22 @@ struct Plan {
     int chunk;
     int splits;  // at max_seq
     bool tile;
+    int part_rows;  // of a partial result of the tile and row kernels
 };
 
 Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draft)
 {
     Plan pl;
     const int rows = group * max_draft;
-    pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    // Up to 32 rows the tile kernel: 8 tokens x 4 heads over 4000 tokens, 64
+    // sequences, 147 us with MXFP4 and 163 with MXFP8 (the row kernel 162 and 179).
+    // Above that the row kernel: 31 tokens over 16001, 8 sequences, 80 and 85 us
+    // (units of 128 rows in the tile kernel 113 and 140); 15 tokens 71 and 76
+    // (units of 64 rows 78 and 125).
+    pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
     pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
     pl.tile = pl.rows > 16;
+    pl.part_rows = std::min(pl.rows, (rows + 31) / 32 * 32);
     const int64_t units = static_cast<int64_t>(batch) * kv_heads * pl.row_tiles;
     // Eight steps a warp at least, so that a context of up to 512 tokens is done
     // without a second kernel (503 tokens, 8 heads: 9.3 us against 13 us cut in
@@ -655,12 +662,11 @@ cudaError_t launch_stream(const AttnParams& p, const Plan& pl, cudaStream_t stre
 }
 
 template <int kFmt, int kDim>
-cudaError_t launch_rows(const AttnParams& p, const Plan& pl, void* workspace, cudaStream_t stream)
+cudaError_t launch_rows(const AttnParams& p, const Plan& pl, cudaStream_t stream)
 {
     cudaError_t err = pl.rows == 4    ? launch_stream<kFmt, kDim, 4>(p, pl, stream)
                       : pl.rows == 8  ? launch_stream<kFmt, kDim, 8>(p, pl, stream)
-                      : pl.rows == 16 ? launch_stream<kFmt, kDim, 16>(p, pl, stream)
-                                      : launch_kv_attention_tile(p, pl.rows, workspace, stream);
+                                      : launch_stream<kFmt, kDim, 16>(p, pl, stream);
     if (err != cudaSuccess || pl.splits <= 1)
         return err;
     const int64_t rows = static_cast<int64_t>(p.T) * p.q_heads;
@@ -670,12 +676,15 @@ cudaError_t launch_rows(const AttnParams& p, const Plan& pl, void* workspace, cu
 
 }  // namespace
 
+// int64 [batch + 1] before the partial results, which start on 16 bytes
+static size_t prefix_words(int batch) { return (static_cast<size_t>(batch) + 2) / 2 * 2; }
+
 size_t kv_attention_workspace_bytes(int batch, int64_t T, int q_heads, int kv_heads, int dim, int64_t max_seq,
                                     int max_draft)
 {
     const Plan pl = make_plan(batch, kv_heads, q_heads / kv_heads, max_seq, max_draft);
-    if (pl.tile)
-        return kv_attention_tile_workspace(pl.rows, dim, batch);
+    if (pl.tile)  // the sequences' first tiles, and two partial results per CTA
+        return prefix_words(batch) * sizeof(int64_t) + static_cast<size_t>(2 * sm_count()) * pl.part_rows * (dim + 2) * sizeof(float);
     if (pl.splits <= 1)
         return 0;
     return static_cast<size_t>(pl.splits) * T * q_heads * (dim + 2) * sizeof(float);
@@ -710,13 +719,21 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream)
     p.xscale = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
     p.status = a.status;
+    p.part_rows = pl.part_rows;
+    if (pl.tile) {
+        p.xscale *= kUnscale;  // scores come out of the MMA times 2^-64
+        p.prefix = static_cast<int64_t*>(a.workspace);
+        p.part_o = reinterpret_cast<float*>(p.prefix + prefix_words(a.batch));
+        p.part_ml = p.part_o + static_cast<size_t>(2 * sm_count()) * pl.part_rows * a.cache.dim;
+        return pl.rows == 32 ? launch_kv_attention_tile(p, stream) : launch_kv_attention_rows(p, stream);
+    }
     p.part_o = static_cast<float*>(a.workspace);
     p.part_ml = p.part_o + static_cast<size_t>(pl.splits) * a.T * a.q_heads * a.cache.dim;
     if (a.cache.format == kKvMxfp8)
-        return a.cache.dim == 128 ? launch_rows<kKvMxfp8, 128>(p, pl, a.workspace, stream)
-                                    : launch_rows<kKvMxfp8, 64>(p, pl, a.workspace, stream);
-    return a.cache.dim == 128 ? launch_rows<kKvMxfp4, 128>(p, pl, a.workspace, stream)
-                              : launch_rows<kKvMxfp4, 64>(p, pl, a.workspace, stream);
+        return a.cache.dim == 128 ? launch_rows<kKvMxfp8, 128>(p, pl, stream)
+                                    : launch_rows<kKvMxfp8, 64>(p, pl, stream);
+    return a.cache.dim == 128 ? launch_rows<kKvMxfp4, 128>(p, pl, stream)
+                              : launch_rows<kKvMxfp4, 64>(p, pl, stream);
 }
 
 }  // namespace fp4lin

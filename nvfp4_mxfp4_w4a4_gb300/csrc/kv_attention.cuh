@@ -40,15 +40,17 @@ struct AttnParams {
     float* part_ml; // [splits][T * q_heads][2]
     unsigned long long wait_ns;  // limit of the bounded device waits, and where they report
     unsigned int* status;
-    // tile kernel: deal out whole units (short contexts) instead of tiles, and
+    // tile and row kernels: deal out whole units (short contexts) instead of tiles, and
     // where it leaves the sequences' first tiles and, behind them, a run's length
     bool whole;
+    int part_rows;  // rows of a partial result
     int64_t* prefix;
 };
 
-// The kernel of many rows (kv_attention_tile.cu): row tiles of 32, 64 or 128 rows.
-size_t kv_attention_tile_workspace(int rows, int dim, int batch);
-cudaError_t launch_kv_attention_tile(const AttnParams& p, int rows, void* workspace, cudaStream_t stream);
+// The kernels of 17 to 32 rows and of more (units of 32 and 128 rows), whose
+// partial results' rows p.part_rows counts.
+cudaError_t launch_kv_attention_tile(const AttnParams& p, cudaStream_t stream);
+cudaError_t launch_kv_attention_rows(const AttnParams& p, cudaStream_t stream);
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {

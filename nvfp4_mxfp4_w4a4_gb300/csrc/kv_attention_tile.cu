@@ -1,8 +1,8 @@
-// kv_attention_tile.cu -- attention of many rows (trees of drafted tokens)
-// over the MX-quantized paged cache, on the 5th-generation tensor cores.
+// kv_attention_tile.cu -- attention of 17 to 32 rows (a few drafted tokens) over
+// the MX-quantized paged cache, on the 5th-generation tensor cores.
 //
 // The same operation as kv_attention.cu, whose warps would each convert the
-// cache's codes again for every few rows.  Here a CTA owns up to NR = 128 rows
+// cache's codes again for every few rows.  Here a CTA owns up to NR = 32 rows
 // (drafted token x query head of one key/value head) and walks the context in
 // tiles of 128 tokens; each tile is converted once, to bf16 in shared memory,
 // and multiplied by tcgen05.mma with the tokens on the M side, so that the MMA
@@ -23,15 +23,6 @@
 // order in which their bits come out of a word; Q is stored in that order too,
 // and the output's rows are put back at the end.
 //
-// The work is cut on the device: the tiles of all (sequence, key/value head,
-// row tile) units in one line, with a few places for each unit's start and end,
-// an equal run of the line per CTA, one CTA per SM.
-// A unit whose tiles fall to several CTAs leaves partial results (a CTA has at
-// most two: of the unit that began before its run and of the one that goes on
-// after it), which the join kernel adds.  With a grid of equal chunks instead,
-// the last round of CTAs and every CTA's start and end cost as much as the
-// tiles (8 trees of 31 tokens over up to 16001 tokens: 139 us).
-//
 // Warps: 0-7 softmax (quadrant of tokens x half of the rows; they also load Q
 // and write the results), 8-11 convert keys, 12-15 values, 16 issues the first
 // product's MMAs and 17 the second's (18, 19 fill the register group).  A wait
@@ -39,43 +30,14 @@
 // so each product of a tile has one: its barrier counts the converters and the
 // softmax warps.  K, V, S and P are double-buffered, and the converters run
 // ahead into the CTA's next unit.
-#include <cuda_bf16.h>
-
-#include <algorithm>
-#include <mutex>
-#include <type_traits>
-
-#include "internal.h"
-#include "kv_attention.cuh"
-#include "ptx.cuh"
+#include "kv_attention_walk.cuh"
 
 namespace fp4lin {
 namespace {
 
-constexpr int kTile = 128;  // tokens
-constexpr int kSlab = kTile * 128;  // bytes of 64 bf16 elements of a tile's tokens
-constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 8 + 4) * 32;
-// The work line: a unit is kUnitTiles places (its start and end cost about as
-// much as five tiles: 9 us against 1.8 us with 128 rows) and then its tiles.
-constexpr int kUnitTiles = 5;
-constexpr int kLeastRun = kUnitTiles + 4;
-constexpr float kUnset = -1e30f;  // a row's reference before its first visible token
+constexpr int NR = 32;  // rows of a unit
 constexpr uint32_t kSlackBits = 0x4380u;  // bf16 bits of 2^8: weights above it move the references
 constexpr float kCeiling = 100.0f;        // of a weight's exponent, until they have moved
-
-// d[0..1] = a[0..1] * m + c[0..1] in one instruction.
-__device__ __forceinline__ void fma_pair(float* d, float a0, float a1, float2 m, float c0, float c1)
-{
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%2, %3};\n\t"
-        "mov.b64 y, {%4, %5};\n\t"
-        "mov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, z;\n\t"
-        "mov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d[0]), "=f"(d[1])
-        : "f"(a0), "f"(a1), "f"(m.x), "f"(m.y), "f"(c0), "f"(c1));
-}
 
 // The smaller, or NaN if either is.
 __device__ __forceinline__ float min_nan(float a, float b)
@@ -92,203 +54,46 @@ __device__ __forceinline__ float warp_max(float x)
     return r;
 }
 
-template <int kFmt, int kDim, int NR>
+template <int kFmt, int kDim>
 struct TileCfg {
     static constexpr int SLABS = kDim / 64;
-    static constexpr int P_SLABS = NR > 64 ? 2 : 1;
+    static constexpr int COLS = NR / 2;  // rows per softmax thread
     static constexpr int OFF_K = NR * 128 * SLABS;  // Q first
     static constexpr int OFF_V = OFF_K + 2 * SLABS * kSlab;
     static constexpr int OFF_P = OFF_V + 2 * SLABS * kSlab;
-    static constexpr int OFF_REF = OFF_P + 2 * P_SLABS * kSlab;  // float [NR]: the rows' references, negated
-    static constexpr int OFF_POISON = OFF_REF + NR * 4;          // uint32 [NR]: blocks of a row that are NaN
+    static constexpr int OFF_REF = OFF_P + 2 * kSlab;         // float [NR]: the rows' references, negated
+    static constexpr int OFF_POISON = OFF_REF + NR * 4;       // uint32 [NR]: blocks of a row that are NaN
     static constexpr int OFF_BAR = OFF_POISON + NR * 4;
-    static constexpr int OFF_SLOT = OFF_BAR + 8 * 8;  // TMEM address, flags, the run's tiles
-    static constexpr int OFF_WALK = OFF_SLOT + 32;  // the run's first unit; the softmax's current one
-    static constexpr int OFF_SCRATCH = OFF_WALK + 2 * 64;  // two halves' [5][COLS] floats (below 128 rows)
-    static constexpr int SMEM = OFF_SCRATCH + (NR < 128 ? 5 * NR * 4 : 0) + 1024;  // + alignment slack
-    static constexpr int TMEM_COLS = NR == 32 ? 128 : NR == 64 ? 256 : 512;
-    static constexpr int COLS = NR / 2;  // rows per softmax thread
-    // conversion: 16-byte chunks of a token's codes, one per lane
-    static constexpr int ROW = kFmt == kKvMxfp8 ? kDim : kDim / 2;
-    static constexpr int CH = ROW / 16;
+    static constexpr int OFF_SLOT = OFF_BAR + 8 * 8;          // TMEM address, flags, the run's tiles
+    static constexpr int OFF_WALK = (OFF_SLOT + 32 + 63) / 64 * 64;  // Place [kWalks]
+    static constexpr int OFF_SCRATCH = OFF_WALK + kWalks * 64;  // two halves' [5][COLS] floats
+    static constexpr int SMEM = OFF_SCRATCH + 5 * NR * 4 + 1024;  // + alignment slack
+    static constexpr int TMEM_COLS = 128;
     static constexpr int SB = kDim / 32;
-    // With few rows a tile takes less time than its codes from memory, so two
-    // tiles are on their way: 64 KB (E4M3) per SM.
-    static constexpr int AHEAD = NR == 128 ? 1 : 2;
-    // registers per thread of the three groups, out of 96 x 640 at launch (a
-    // softmax thread keeps COLS sums, a converter AHEAD tiles' codes)
-    static constexpr int REGS_SOFTMAX = NR == 128 ? 136 : NR == 64 ? 104 : 88,
-                         REGS_CONVERT = NR == 128 ? 88 : NR == 64 ? 120 : 136, REGS_MMA = NR == 128 ? 24 : 32;
+    // A tile takes less time than its codes from memory, so two tiles are on their
+    // way: 64 KB (E4M3) per SM.
+    static constexpr int AHEAD = 2;
+    // registers per thread of the three groups
+    static constexpr int REGS_SOFTMAX = 80, REGS_CONVERT = 136, REGS_MMA = 48;
     static constexpr int REGS = 256 * REGS_SOFTMAX + 256 * REGS_CONVERT + 128 * REGS_MMA;
-    static_assert(REGS <= 96 * kThreads, "register split");
+    static_assert(REGS <= kLaunchRegs * kThreads, "register split");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-// The calling warpgroup's registers per thread, from 96 at launch.
-template <int kRegs>
-__device__ __forceinline__ void set_registers()
-{
-    if constexpr (kRegs > 96)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-    else if constexpr (kRegs < 96)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-// Element that is stored at position `pos` of a head.
-template <int kFmt>
-__device__ __forceinline__ int element_at(int pos)
-{
-    return kFmt == kKvMxfp8 ? (pos & ~3) | ((pos & 1) << 1) | ((pos >> 1) & 1) : (pos & ~7) | ((pos & 1) << 2) | ((pos >> 1) & 3);
-}
-
-// One unit after the other: its sequence, head, first row and tiles.
-template <int NR>
-struct Walk {
-    int b, unit, units, row_tiles, tiles;  // units of the sequence, tiles of a unit
-    int ctx, len, n, q_start;
-    int lo;    // first tile of the CTA's run in this unit
-    int lead;  // places of the unit's start that lie in the run
-    int head;
-
-    __device__ __forceinline__ void sequence(const AttnParams& p)
-    {
-        group_rows(p.q_offsets, b, p.T, &q_start, &n);
-        ctx = max(min(__ldg(p.context_lens + b), p.max_len - n), 0);
-        len = min(ctx + n, p.max_len);
-        tiles = (len + kTile - 1) / kTile;
-        row_tiles = min((n * p.group + NR - 1) / NR, p.row_tiles);
-        units = row_tiles * p.cache.heads;
-    }
-    __device__ __forceinline__ void next(const AttnParams& p)
-    {
-        lo = 0;
-        lead = kUnitTiles;
-        ++unit;
-        while (unit >= units && b + 1 < p.batch) {
-            ++b;
-            unit = 0;
-            sequence(p);
-        }
-        head = row_tiles > 0 ? unit / row_tiles : 0;
-    }
-    // Tiles of this unit in a run with `left` places to go, which it takes away.
-    __device__ __forceinline__ int run(const AttnParams& p, int64_t& left) const
-    {
-        if (p.whole) {
-            --left;
-            return tiles;
-        }
-        const int64_t here = min(left - lead, static_cast<int64_t>(tiles - lo));
-        left -= lead + max(here, int64_t(0));
-        return static_cast<int>(max(here, int64_t(0)));
-    }
-    __device__ __forceinline__ int row0() const { return (unit - head * row_tiles) * NR; }
-};
-
-// A tile for the converters.
-struct TileRef {
-    int t0, len, head, page[2];
-    bool edge;  // (values) not all its tokens are context
-};
-
-template <int kFmt, int kDim, int NR>
+template <int kFmt, int kDim>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const AttnParams p)
 {
-    using C = TileCfg<kFmt, kDim, NR>;
+    using C = TileCfg<kFmt, kDim>;
     extern __shared__ uint8_t smem_raw[];
     grid_dependency_wait();
     launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
-    // ------------------------------------------------ this CTA's run of tiles
-    // (p.whole: units instead of tiles are dealt out, and none is cut)
-    static_assert(sizeof(Walk<NR>) <= 64, "its place in shared memory");
-    int64_t count;  // tiles (units) of the run
-    {
-        struct Scan {
-            int64_t warp_sum[kThreads / 32];
-            int64_t offset;
-            int b;
-        };
-        Scan* scan = reinterpret_cast<Scan*>(smem);
-        auto weight = [&](int i) -> int64_t {
-            if (i >= p.batch)
-                return 0;
-            Walk<NR> w;
-            w.b = i;
-            w.sequence(p);
-            return p.whole ? w.units : static_cast<int64_t>(w.units) * (w.tiles + kUnitTiles);
-        };
-        // sum over the block of v, and of the threads before this one
-        auto block_scan = [&](int64_t v, int64_t* before) -> int64_t {
-            int64_t x = v;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-                x += lane >= d ? y : 0;
-            }
-            __syncthreads();
-            if (lane == 31)
-                scan->warp_sum[warp] = x;
-            __syncthreads();
-            int64_t total = 0, base = 0;
-            for (int w = 0; w < kThreads / 32; ++w) {
-                base += w < warp ? scan->warp_sum[w] : 0;
-                total += scan->warp_sum[w];
-            }
-            *before = base + x - v;
-            return total;
-        };
-        int64_t total = 0, before, mine = 0;
-        for (int i = 0; i < p.batch; i += kThreads) {
-            mine = weight(i + threadIdx.x);
-            total += block_scan(mine, &before);
-        }
-        const int64_t per = max((total + gridDim.x - 1) / gridDim.x, int64_t(p.whole ? 1 : kLeastRun));
-        const int64_t start = blockIdx.x * per;
-        count = min(per, total - start);
-        int64_t base = 0;
-        for (int i = 0; i < p.batch; i += kThreads) {
-            const int me = i + threadIdx.x;
-            if (p.batch > kThreads) {
-                mine = weight(me);
-                const int64_t sum = block_scan(mine, &before);
-                before += base;
-                base += sum;
-            }
-            if (start >= before && start < before + mine) {
-                scan->b = me;
-                scan->offset = start - before;
-            }
-            if (blockIdx.x == 0 && me < p.batch)
-                p.prefix[me] = before;
-        }
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            p.prefix[p.batch] = per;
-        __syncthreads();
-        if (count <= 0)
-            return;
-        if (threadIdx.x == 0) {
-            Walk<NR> w;
-            w.b = scan->b;
-            w.sequence(p);
-            const int64_t off = scan->offset;
-            const int length = p.whole ? 1 : w.tiles + kUnitTiles;
-            w.unit = static_cast<int>(off / length);
-            w.head = w.unit / w.row_tiles;
-            const int in_unit = static_cast<int>(off - static_cast<int64_t>(w.unit) * length);
-            w.lead = max(kUnitTiles - in_unit, 0);
-            w.lo = p.whole ? 0 : max(in_unit - kUnitTiles, 0);
-            *reinterpret_cast<Walk<NR>*>(smem + C::OFF_WALK) = w;
-            *reinterpret_cast<Walk<NR>*>(smem + C::OFF_WALK + 64) = w;
-            uint32_t total = 0;
-            for (int64_t left = count; left > 0; w.next(p))
-                total += w.run(p, left);
-            reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT)[7] = total;
-        }
-        __syncthreads();
-    }
+    Place<NR>* places = reinterpret_cast<Place<NR>*>(smem + C::OFF_WALK);
+    const int64_t count = find_run(p, smem, places, reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT) + 7);
+    if (count <= 0)
+        return;
     float* ref = reinterpret_cast<float*>(smem + C::OFF_REF);
     uint32_t* poison = reinterpret_cast<uint32_t*>(smem + C::OFF_POISON);
     // the tile's keys (and its unit's Q) are in shared memory, and the S^T before the last has been read
@@ -358,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 if (!__all_sync(0xFFFFFFFFu, ok))
                     break;
                 tc_fence_after_sync();
-                const uint64_t vf = vd + ((f * C::SLABS * kSlab) >> 4), pf = pd + ((f * C::P_SLABS * kSlab) >> 4);
+                const uint64_t vf = vd + ((f * C::SLABS * kSlab) >> 4), pf = pd + ((f * kSlab) >> 4);
                 const uint32_t add = unit_start[f] ? 0u : 1u;
                 if (elect_one()) {
 #pragma unroll
@@ -370,161 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             }
         }
     } else if (warp >= kSoftmaxWarps) {
-        // --------------------------------------------- codes -> bf16 tiles
         set_registers<C::REGS_CONVERT>();
-        // 16-byte chunks of the codes, one per lane.  Eight lanes in a row store to
-        // one slab, for tokens whose swizzles differ, so that their 16-byte pieces
-        // fall in different banks.
         const bool value = warp >= kSoftmaxWarps + 4;
-        const int w32 = (warp & 3) * 32;              // this warp's tokens of the tile
-        constexpr int TPI = 32 / C::CH;               // tokens per load
-        constexpr int HC = C::CH / C::SLABS;          // chunks of a token per slab
-        const int chunk = ((lane >> 3) % C::SLABS) * HC + lane % HC;
-        const int sub = (lane >> 3) / C::SLABS * (8 / HC) + lane / HC % (8 / HC);
-        const uint8_t* codes = (value ? p.cache.v_codes : p.cache.k_codes) + sub * C::ROW + chunk * 16;
-        const uint8_t* scales =
-            (value ? p.cache.v_scales : p.cache.k_scales) + sub * C::SB + (kFmt == kKvMxfp8 ? chunk / 2 : chunk);
-        // where the lane's 16-byte pieces of its first token go
-        constexpr int PIECES = kFmt == kKvMxfp8 ? 2 : 4;
-        uint32_t at_piece[PIECES];
-#pragma unroll
-        for (int h = 0; h < PIECES; ++h) {
-            const int piece = PIECES * chunk + h;
-            at_piece[h] = smem_u32(smem + (value ? C::OFF_V : C::OFF_K)) + (piece >> 3) * kSlab + (w32 + sub) * 128 +
-                          (((piece & 7) ^ (sub & 7)) << 4);
-        }
-        uint64_t* full = value ? pv_ready : s_ready;
-        uint64_t* freed = value ? pv_done : s_done;
-        // The run's tiles in order: a tile's pages are looked up three tiles ahead, its
-        // tokens' places found two ahead, its codes loaded one ahead.
-        Walk<NR> w = *reinterpret_cast<const Walk<NR>*>(smem + C::OFF_WALK);
-        int64_t left = count;
-        int tiles = w.run(p, left), at = 0;  // of the unit that the look-up is in
-        auto look_up = [&](TileRef& r) -> bool {
-            while (at == tiles) {  // (a run may hold no tile of its first and last unit)
-                if (left <= 0)
-                    return false;
-                w.next(p);
-                tiles = w.run(p, left);
-                at = 0;
-            }
-            r.t0 = (w.lo + at) * kTile;
-            r.len = w.len;
-            r.head = w.head;
-            r.edge = value && r.t0 + kTile > w.ctx;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                r.page[h] = __ldg(p.block_table + w.b * p.table_stride +
-                                  div_by_magic(min(r.t0 + w32 + 16 * h, (w.len - 1) & ~15), p.page_div));
-            ++at;
-            return true;
-        };
-        // a group of 16 tokens lies in one page; groups past the end read the last one
-        auto find_groups = [&](const TileRef& r, int64_t* group) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = min(r.t0 + w32 + 16 * h, (r.len - 1) & ~15);
-                const int off = t - static_cast<int>(div_by_magic(t, p.page_div)) * p.cache.page_size;
-                const int pg = min(max(r.page[h], 0), static_cast<int>(p.cache.pages - 1));
-                group[h] = (static_cast<int64_t>(pg) * p.cache.heads + r.head) * p.cache.page_size + off;
-            }
-        };
-        constexpr int AHEAD = C::AHEAD;  // tiles whose codes are in registers or on their way
-        uint4 raw[AHEAD][C::CH];
-        uint32_t sc[AHEAD][C::CH];
-        bool have[AHEAD], edge[AHEAD];
-        int64_t group[2];  // of the tile to load next
-        TileRef r = {};
-        bool look = look_up(r);  // the tile looked up
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            have[k] = look;
-            edge[k] = r.edge;
-            if (look) {
-                find_groups(r, group);
-#pragma unroll
-                for (int i = 0; i < C::CH; ++i) {
-                    const int64_t from = group[(i * TPI) >> 4] + ((i * TPI) & 15);
-                    sc[k][i] = __ldg(scales + from * C::SB);
-                    raw[k][i] = __ldg(reinterpret_cast<const uint4*>(codes + from * C::ROW));
-                }
-                look = look_up(r);
-            }
-        }
-        bool loads = look, edge_next = r.edge;
-        if (look) {
-            find_groups(r, group);
-            look = look_up(r);
-        }
-        // converts the tile in raw[k] into the buffers f and starts the loads of the
-        // tile AHEAD after it
-        auto convert = [&](auto slot, uint32_t f, uint32_t ph) -> bool {
-            constexpr int k = decltype(slot)::value;
-            ok = mbar_wait_bounded(&freed[f], ph, p.status, kStatusTimeout, limit);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                return false;
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < C::CH; ++i)
-                top = max(top, sc[k][i]);
-            // multipliers: in range for all but blocks of very large values and NaN; NaN
-            // values of an edge tile are kept out of the product (see the softmax)
-            constexpr uint32_t PLUS = (kFmt == kKvMxfp8 ? 120u : 126u) - kScaleShift;
-            if (__any_sync(0xFFFFFFFFu, top > 254u - PLUS)) {
-#pragma unroll
-                for (int i = 0; i < C::CH; ++i)
-                    sc[k][i] = edge[k] && sc[k][i] == 0xFFu ? 0u : block_multiplier<kFmt>(sc[k][i]) * 0x10001u;
-            } else {
-#pragma unroll
-                for (int i = 0; i < C::CH; ++i)
-                    sc[k][i] = sc[k][i] * 0x00800080u + PLUS * 0x00800080u;
-            }
-            const uint32_t buf = f * C::SLABS * kSlab;
-#pragma unroll
-            for (int i = 0; i < C::CH; ++i) {
-                const uint32_t c4[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
-                const uint32_t mul = sc[k][i];
-                // the token's place in its group of 8 turns the pieces: of it, i decides
-                // the bits from TPI up
-                const uint32_t turn = ((i * TPI) & 7) << 4, down = i * TPI * 128;
-#pragma unroll
-                for (int h = 0; h < PIECES; ++h) {
-                    uint32_t o[4];
-                    if constexpr (kFmt == kKvMxfp8) {
-                        place_codes<kFmt>(c4[2 * h], o);
-                        place_codes<kFmt>(c4[2 * h + 1], o + 2);
-                    } else {
-                        place_codes<kFmt>(c4[h], o);
-                    }
-                    st_shared_v4(((at_piece[h] + buf) ^ turn) + down, mul_bf16x2(o[0], mul), mul_bf16x2(o[1], mul),
-                                 mul_bf16x2(o[2], mul), mul_bf16x2(o[3], mul));
-                }
-                if (loads) {
-                    const int64_t from = group[(i * TPI) >> 4] + ((i * TPI) & 15);
-                    raw[k][i] = __ldg(reinterpret_cast<const uint4*>(codes + from * C::ROW));
-                    sc[k][i] = __ldg(scales + from * C::SB);
-                }
-            }
-            find_groups(r, group);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&full[f]);
-            have[k] = loads;
-            edge[k] = edge_next;
-            loads = look;
-            edge_next = r.edge;
-            look = look && look_up(r);
-            return true;
-        };
-        for (uint32_t g = 0;; g += 2) {
-            const uint32_t ph = ((g >> 1) & 1u) ^ 1u;
-            if (!have[0] || !convert(std::integral_constant<int, 0>(), 0, ph))
-                break;
-            constexpr int second = AHEAD > 1 ? 1 : 0;
-            if (!have[second] || !convert(std::integral_constant<int, second>(), 1, ph))
-                break;
-        }
+        convert_run<kFmt, kDim, NR, C::AHEAD>(p, places[1 + warp - kSoftmaxWarps].walk, count, smem + C::OFF_K,
+                                              smem + C::OFF_V, value ? pv_ready : s_ready, value ? pv_done : s_done);
     } else {
         // --------------------------------------------------------- softmax
         set_registers<C::REGS_SOFTMAX>();
@@ -532,21 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
         const int quad = warp & 3, half = warp >> 2, col0 = half * C::COLS;
         const int token = quad * 32 + lane;  // of the tile
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        constexpr int CW = C::COLS == 32 ? 32 : 16;  // columns at a time
+        constexpr int CW = 16;  // columns at a time
         const float2 xs = make_float2(p.xscale, p.xscale);
-        auto load_cols = [&](uint32_t addr, uint32_t* r) {
-            if constexpr (CW == 32)
-                tmem_ld_32x32b_x32(addr, r);
-            else
-                tmem_ld_32x32b_x16(addr, r);
-        };
-        // a half's memory for moving its references: with 128 rows its own part of
-        // P^T's buffer
-        auto scratch = [&](uint8_t* pbuf) {
-            return reinterpret_cast<float*>(NR == 128 ? pbuf + half * kSlab : smem + C::OFF_SCRATCH + half * 5 * C::COLS * 4);
-        };
+        // a half's memory for moving its references
+        float* scratch = reinterpret_cast<float*>(smem + C::OFF_SCRATCH) + half * 5 * C::COLS;
         // the current unit stays in shared memory: one thread moves it on
-        Walk<NR>& wk = *reinterpret_cast<Walk<NR>*>(smem + C::OFF_WALK + 64);
+        Walk<NR>& wk = places[0].walk;
         uint32_t g = 0;
         bool leave = false;
         for (int64_t left = count; left > 0 && !leave;) {
@@ -600,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 const int t = (lo + it) * kTile + token;
                 const bool edge = (lo + it + 1) * kTile > ctx;
                 const uint32_t s_addr = tmem + lanes + f * NR + col0;
-                uint8_t* pbuf = smem + C::OFF_P + f * C::P_SLABS * kSlab;
+                uint8_t* pbuf = smem + C::OFF_P + f * kSlab;
                 const int j = t - ctx;
                 // edge tiles: which of the thread's rows see its token, a node (drafted
                 // token, `group` rows) at a time
@@ -632,13 +277,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 auto weigh = [&](auto masked, float2 sign) {
                     uint32_t top = 0u;
                     uint32_t sb[2][CW];
-                    load_cols(s_addr, sb[0]);
+                    tmem_ld_32x32b_x16(s_addr, sb[0]);
 #pragma unroll
                     for (int c = 0; c < C::COLS; c += CW) {
                         uint32_t* s = sb[c / CW & 1];
                         tmem_ld_wait();
                         if (c + CW < C::COLS)
-                            load_cols(s_addr + c + CW, sb[(c / CW + 1) & 1]);
+                            tmem_ld_32x32b_x16(s_addr + c + CW, sb[(c / CW + 1) & 1]);
                         uint32_t w[CW / 2];
 #pragma unroll
                         for (int k = 0; k < CW; k += 4) {
@@ -702,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
 #pragma unroll 1
                 for (int step = it > 0 ? kFirst : kAgain;; ++step) {
                     if (step == kAgain) {
-                        float* top = scratch(pbuf);  // [4][COLS]
+                        float* top = scratch;  // [4][COLS]
                         float* factor = top + 4 * C::COLS;
                         named_barrier_sync(3 + half, 128);
                         if (edge)
@@ -791,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             // the unit's MMAs have read their operands: [4][NR] sums go to Q's place,
             // the rows of each half to one of P^T's buffers
             float* sums = reinterpret_cast<float*>(smem);
-            float* tile = reinterpret_cast<float*>(smem + C::OFF_P + (warp >> 2) * C::P_SLABS * kSlab);
-            static_assert(C::COLS * kDim * 4 <= C::P_SLABS * kSlab, "a half's outputs in one buffer");
+            float* tile = reinterpret_cast<float*>(smem + C::OFF_P + (warp >> 2) * kSlab);
+            static_assert(C::COLS * kDim * 4 <= kSlab, "a half's outputs in one buffer");
             // sums of the rows over the warp's tokens: each step sends half of the rows
             // away and adds the other half's, until a lane holds COLS / 32 rows (or two
             // lanes the same one)
@@ -841,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 const int r = i / (kDim / 8), d = (i - r * (kDim / 8)) * 8;
                 const float ls = sums[r] + sums[NR + r] + sums[2 * NR + r] + sums[3 * NR + r];
                 const float m = ref[r] == -kUnset ? -INFINITY : -ref[r];
-                const float* src = reinterpret_cast<const float*>(smem + C::OFF_P + (r >= C::COLS ? C::P_SLABS * kSlab : 0)) +
+                const float* src = reinterpret_cast<const float*>(smem + C::OFF_P + (r >= C::COLS ? kSlab : 0)) +
                                    (r >= C::COLS ? r - C::COLS : r) * kDim + d;
                 const float4 u = *reinterpret_cast<const float4*>(src);
                 const float4 v = *reinterpret_cast<const float4*>(src + 4);
@@ -887,101 +532,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
     }
 }
 
-// Joins the parts of the rows whose unit fell to several CTAs.
-template <int kDim, int NR, int kJoinWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_tile_join_kernel(const AttnParams p)
-{
-    __shared__ JoinScratch<kDim, kJoinWarps> scratch;
-    grid_dependency_wait();
-    launch_dependents();
-    const int64_t row = blockIdx.x;
-    const int tok = static_cast<int>(row / p.q_heads);
-    const int hq = static_cast<int>(row - static_cast<int64_t>(tok) * p.q_heads);
-    Walk<NR> w;
-    w.b = sequence_of(p, tok);
-    w.sequence(p);
-    const int head = hq / p.group;
-    const int r = (tok - w.q_start) * p.group + hq - head * p.group;  // of the head's rows
-    if (tok < w.q_start || tok >= w.q_start + w.n || r >= w.row_tiles * NR)
-        return;
-    const int64_t per = p.prefix[p.batch];
-    const int64_t from = p.prefix[w.b] + static_cast<int64_t>(head * w.row_tiles + r / NR) * (w.tiles + kUnitTiles) +
-                         kUnitTiles;
-    const int c0 = static_cast<int>(from / per), c1 = static_cast<int>((from + w.tiles - 1) / per);
-    if (c0 == c1)
-        return;  // written by its CTA
-    join_row<kDim, kJoinWarps>(p, &scratch, tok, hq, c1 - c0 + 1, [&](int s) -> int64_t {
-        return (2 * static_cast<int64_t>(c0) + (s == 0 ? 1 : 2 * s)) * NR + r % NR;
-    });
-}
-
-template <int kFmt, int kDim, int NR>
-cudaError_t launch_tile(const AttnParams& p, cudaStream_t stream)
-{
-    using C = TileCfg<kFmt, kDim, NR>;
-    auto kern = kv_attention_tile_kernel<kFmt, kDim, NR>;
-    // per device and context, once: the shared-memory opt-in and the register split
-    static std::mutex mu;
-    static unsigned long long configured[64] = {};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess || dev < 0 || dev >= 64)
-        return err != cudaSuccess ? err : cudaErrorInvalidDevice;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        const unsigned long long ctx = current_context_id();
-        if (configured[dev] == 0 || configured[dev] != ctx) {
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-            if (err != cudaSuccess)
-                return err;
-            // setmaxnreg.inc waits until the registers it asks for are free: never
-            // launch a split that the launch's allocation cannot cover
-            cudaFuncAttributes fa;
-            err = cudaFuncGetAttributes(&fa, kern);
-            if (err != cudaSuccess)
-                return err;
-            if (fa.numRegs * kThreads < C::REGS)
-                return cudaErrorInvalidConfiguration;
-            configured[dev] = ctx;
-        }
-    }
-    err = launch_pdl(kern, dim3(static_cast<unsigned>(sm_count())), dim3(kThreads), C::SMEM, stream, p);
-    if (err != cudaSuccess || p.whole)
-        return err;
-    // parts per unit: about the runs over the units
-    const bool few = 4 * static_cast<int64_t>(p.batch) * p.cache.heads * p.row_tiles >= sm_count();
-    return launch_pdl(few ? kv_attention_tile_join_kernel<kDim, NR, 1> : kv_attention_tile_join_kernel<kDim, NR, 4>,
-                      dim3(static_cast<unsigned>(p.T) * p.q_heads), dim3(few ? 32 : 128), 0, stream, p);
-}
-
 template <int kFmt, int kDim>
-cudaError_t launch_rows(const AttnParams& p, int rows, cudaStream_t stream)
+cudaError_t launch(const AttnParams& p, cudaStream_t stream)
 {
-    return rows == 32   ? launch_tile<kFmt, kDim, 32>(p, stream)
-           : rows == 64 ? launch_tile<kFmt, kDim, 64>(p, stream)
-                        : launch_tile<kFmt, kDim, 128>(p, stream);
+    using C = TileCfg<kFmt, kDim>;
+    return launch_runs<void (*)(AttnParams), kv_attention_tile_kernel<kFmt, kDim>, kDim, NR>(p, C::SMEM, C::REGS, stream);
 }
 
 }  // namespace
 
-// Two partial results per CTA, and the sequences' first tiles.
-size_t kv_attention_tile_workspace(int rows, int dim, int batch)
+cudaError_t launch_kv_attention_tile(const AttnParams& p, cudaStream_t stream)
 {
-    return static_cast<size_t>(2 * sm_count()) * rows * (dim + 2) * sizeof(float) + (static_cast<size_t>(batch) + 2) / 2 * 16;
-}
-
-cudaError_t launch_kv_attention_tile(const AttnParams& params, int rows, void* workspace, cudaStream_t stream)
-{
-    AttnParams p = params;
-    p.xscale *= kUnscale;  // scores come out of the MMA times 2^-64
-    const size_t part_rows = static_cast<size_t>(2 * sm_count()) * rows;
-    p.prefix = static_cast<int64_t*>(workspace);
-    p.part_o = reinterpret_cast<float*>(p.prefix + (params.batch + 2) / 2 * 2);
-    p.part_ml = p.part_o + part_rows * p.cache.dim;
     if (p.cache.format == kKvMxfp8)
-        return p.cache.dim == 128 ? launch_rows<kKvMxfp8, 128>(p, rows, stream)
-                                  : launch_rows<kKvMxfp8, 64>(p, rows, stream);
-    return p.cache.dim == 128 ? launch_rows<kKvMxfp4, 128>(p, rows, stream) : launch_rows<kKvMxfp4, 64>(p, rows, stream);
+        return p.cache.dim == 128 ? launch<kKvMxfp8, 128>(p, stream) : launch<kKvMxfp8, 64>(p, stream);
+    return p.cache.dim == 128 ? launch<kKvMxfp4, 128>(p, stream) : launch<kKvMxfp4, 64>(p, stream);
 }
 
 }  // namespace fp4lin
