@@ -600,8 +600,7 @@ FP4LIN_API fp4_status fp4_quant_weight_fp8_b128(const void* w_bf16, uint8_t* cod
  *                   + bias[n] ),  both sums in float32, one rounding.
  * The products sa * sb must be finite float32 (or NaN, which reaches every
  * output of its row or block column).  bias may be NULL.  All pointers
- * 16-byte aligned (sb: 4).  Weights stream through the tensor cores' M side;
- * no workspace.                                                             */
+ * 16-byte aligned (sb: 4).  No workspace.                                   */
 FP4LIN_API fp4_status fp4_gemm_fp8_b128(const uint8_t* a, const float* sa, const uint8_t* b,
                              const float* sb, const void* bias_bf16, void* out_bf16,
                              int64_t M, int64_t N, int64_t K, void* stream);

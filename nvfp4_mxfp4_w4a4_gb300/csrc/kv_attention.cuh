@@ -117,10 +117,8 @@ __device__ __forceinline__ int sequence_of(const AttnParams& p, int tok)
     return lo;
 }
 
-// Joining a row's parts: one CTA per row; its warps take the parts in turn,
-// and their sums are added in the warps' order.  Four warps for rows with many
-// parts, one where most rows have a few (their look-ups' latency, not the
-// bytes, sets the time: 6000 rows of three parts 13 us with four warps a row).
+// Joining a row's parts: one CTA per row, for rows with many parts; its warps
+// take the parts in turn, and their sums are added in the warps' order.
 template <int kDim, int kWarps>
 struct JoinScratch {
     float weight[kMaxSplits];
@@ -196,6 +194,45 @@ __device__ __forceinline__ void join_row(const AttnParams& p, JoinScratch<kDim, 
         *reinterpret_cast<uint32_t*>(p.out + tok * p.ot + hq * p.oh + d) = pack2(a0 * inv, a1 * inv);
     }
     if (threadIdx.x == 0 && p.lse != nullptr)
+        p.lse[static_cast<int64_t>(tok) * p.q_heads + hq] = (mx + log2f(ls)) * 0.69314718055994531f;
+}
+
+// The same by one warp, for rows with a few parts.
+template <int kDim, typename Index>
+__device__ __forceinline__ void join_row_warp(const AttnParams& p, int tok, int hq, int parts, Index index)
+{
+    const int lane = threadIdx.x & 31;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    float mx = -INFINITY;
+    for (int s = lane; s < parts; s += 32)
+        mx = fmaxf(mx, ml[index(s)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+    constexpr int W = kDim / 32;
+    float acc[W] = {}, ls = 0.0f;
+#pragma unroll 3
+    for (int s = 0; s < parts; ++s) {
+        const float2 v = ml[index(s)];
+        // a part without a visible token has m = -inf and zero sums (or NaN sums, which count)
+        const float f = v.x == -INFINITY ? 1.0f : exp2_approx(v.x - mx);
+        ls += f * v.y;
+        const float* src = p.part_o + index(s) * kDim + lane * W;
+        if constexpr (W == 4) {
+            const float4 o = *reinterpret_cast<const float4*>(src);
+            acc[0] += f * o.x, acc[1] += f * o.y, acc[2] += f * o.z, acc[3] += f * o.w;
+        } else {
+            const float2 o = *reinterpret_cast<const float2*>(src);
+            acc[0] += f * o.x, acc[1] += f * o.y;
+        }
+    }
+    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + tok * p.ot + hq * p.oh + lane * W);
+    if constexpr (W == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+    else
+        *dst = pack2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse != nullptr)
         p.lse[static_cast<int64_t>(tok) * p.q_heads + hq] = (mx + log2f(ls)) * 0.69314718055994531f;
 }
 

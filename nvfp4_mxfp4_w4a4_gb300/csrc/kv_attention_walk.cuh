@@ -383,14 +383,21 @@ __device__ __forceinline__ void convert_run(const AttnParams& p, Walk<kRows>& w,
     }
 }
 
-// Joins the parts of the rows whose unit fell to several CTAs.
-template <int kDim, int kRows, int kJoinWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_run_join_kernel(const AttnParams p)
+// Joins the parts of the rows whose unit fell to several CTAs: four warps for a
+// row with many parts, one where most rows have a few.  Those rows' look-ups set
+// the time, not the bytes, so all of them should be resident at once: 8 rows a
+// CTA and 32 registers, 64 rows per SM (32 trees of 31 tokens x 4 heads over up
+// to 2000 tokens of MXFP4: 70 us with the join; a CTA per row, 32 rows per SM, 84).
+constexpr int kJoinRows = 8;
+
+template <int kDim, int kRows, bool kFew>
+__global__ void __launch_bounds__(kFew ? kJoinRows * 32 : 128, 8) kv_attention_run_join_kernel(const AttnParams p)
 {
-    __shared__ JoinScratch<kDim, kJoinWarps> scratch;
     grid_dependency_wait();
     launch_dependents();
-    const int64_t row = blockIdx.x;
+    const int64_t row = kFew ? static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= static_cast<int64_t>(p.T) * p.q_heads)
+        return;
     const int tok = static_cast<int>(row / p.q_heads);
     const int hq = static_cast<int>(row - static_cast<int64_t>(tok) * p.q_heads);
     Walk<kRows> w;
@@ -406,9 +413,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_run_join_kernel(
     const int c0 = static_cast<int>(from / per), c1 = static_cast<int>((from + w.tiles - 1) / per);
     if (c0 == c1)
         return;  // written by its CTA
-    join_row<kDim, kJoinWarps>(p, &scratch, tok, hq, c1 - c0 + 1, [&](int s) -> int64_t {
+    auto index = [&](int s) -> int64_t {
         return (2 * static_cast<int64_t>(c0) + (s == 0 ? 1 : 2 * s)) * p.part_rows + r % kRows;
-    });
+    };
+    if constexpr (kFew) {
+        join_row_warp<kDim>(p, tok, hq, c1 - c0 + 1, index);
+    } else {
+        __shared__ JoinScratch<kDim, 4> scratch;
+        join_row<kDim, 4>(p, &scratch, tok, hq, c1 - c0 + 1, index);
+    }
 }
 
 // Launches a kernel of runs, whose registers after setmaxnreg are `regs` in all,
@@ -446,8 +459,10 @@ cudaError_t launch_runs(const AttnParams& p, int smem, int regs, cudaStream_t st
         return err;
     // parts per unit: about the runs over the units
     const bool few = 4 * static_cast<int64_t>(p.batch) * p.cache.heads * p.row_tiles >= sm_count();
-    return launch_pdl(few ? kv_attention_run_join_kernel<kDim, kRows, 1> : kv_attention_run_join_kernel<kDim, kRows, 4>,
-                      dim3(static_cast<unsigned>(p.T) * p.q_heads), dim3(few ? 32 : 128), 0, stream, p);
+    const unsigned rows = static_cast<unsigned>(p.T) * p.q_heads;
+    return few ? launch_pdl(kv_attention_run_join_kernel<kDim, kRows, true>, dim3((rows + kJoinRows - 1) / kJoinRows),
+                            dim3(kJoinRows * 32), 0, stream, p)
+               : launch_pdl(kv_attention_run_join_kernel<kDim, kRows, false>, dim3(rows), dim3(128), 0, stream, p);
 }
 
 }  // namespace fp4lin
