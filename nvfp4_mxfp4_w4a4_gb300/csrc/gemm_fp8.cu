@@ -189,8 +189,10 @@ struct SwapCfg {
     static constexpr int W_BYTES = 128 * kBlock;
     static constexpr int X_BYTES = NT * kBlock;
     static constexpr int OFF_X = STAGES * W_BYTES;
-    static constexpr int OFF_SUM = OFF_X + STAGES * X_BYTES;  // [splits][tokens of this CTA][128] floats
-    static constexpr int OFF_SA = OFF_SUM + NT * 128 * 4;
+    // [splits][tokens of this CTA][128] floats: up to 7 more than NT rows where the
+    // cluster's size does not divide the tokens
+    static constexpr int OFF_SUM = OFF_X + STAGES * X_BYTES;
+    static constexpr int OFF_SA = OFF_SUM + (NT + 7) * 128 * 4;
     static constexpr int OFF_BAR = OFF_SA + RING * SLOT * 4;
     static constexpr int NUM_BARS = 2 * STAGES;
     static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
@@ -873,9 +875,14 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t stream)
     // Split K as far as one wave of CTAs goes and every part keeps two blocks:
     // 64 x 14336 x 4096 (112 tiles, 304 slots) 23.7 / 16.8 / 22.8 us in 1 / 2 / 4
     // parts, 1 x 4096 x 4096 (32 tiles) 13.4 / 8.8 / 7.2 / 6.8 us in 1 / 2 / 4 / 8.
+    // Clusters of 3 and 6 leave places of a GPC empty: with the quantizer 64 x 11264
+    // x 4096 (88 tiles) 18.8 / 16.6 us in 2 / 3 parts, 128 x 5120 x 13824 (40 tiles,
+    // 152 slots) 31.6 / 25.1, but 64 x 12800 x 5120 (100 tiles) 21.5 / 26.8; 5 and 7
+    // parts were never faster than 4 (64 x 7680 x 4096, 60 tiles: 13.3 / 19.0 in 4 / 5).
     int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= slots && kb / (splits * 2) >= 2)
-        splits *= 2;
+    for (const int s : {2, 3, 4, 6, 8})
+        if (tiles * s <= (s % 3 ? slots : slots * 7 / 8) && kb / s >= 2)
+            splits = s;
     switch (nt) {
     case 16: return launch_swap<16>(a, splits, stream);
     case 32: return launch_swap<32>(a, splits, stream);

@@ -218,3 +218,10 @@ def test_many_calls_give_the_same_bits(L, M):
     codes, scales = _quant_act(L, bf16_bits_host(x))
     _check(bf16_bits_host(out[39]), R.fp8_values(host(codes), host(scales)[:, :M].T, 1), R.fp8_values(host(w), host(s), 128),
            None, K // 128)
+
+
+# clusters of 3 and 6 along K: tokens that they do not divide, blocks that they do not
+@pytest.mark.parametrize("M,N,K", [(1, 5000, 1680), (5, 5128, 1536), (13, 9992, 768), (16, 11008, 1040), (31, 5632, 2048),
+                                   (64, 10232, 896), (57, 5120, 1552), (128, 5120, 1024), (101, 4872, 784)])
+def test_clusters_that_do_not_divide(L, M, N, K):
+    test_linear_matches_the_formula(L, M, N, K, True)
