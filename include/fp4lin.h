@@ -750,7 +750,7 @@ typedef struct {
     int32_t batch;               /* 1 .. 65535 */
     int64_t tokens;
     int32_t q_heads;
-    int32_t max_draft;           /* bound of n_b (host), 1 .. 1024: tokens past it are not computed */
+    int32_t max_draft;           /* bound of n_b (host), 1 .. 1024: tokens past it give NaN (out and lse) */
     int64_t max_seq_len;         /* bound of context_lens[b] + n_b (host): longer contexts are cut */
     float softmax_scale;         /* > 0 */
 } fp4_kv_attention_args;

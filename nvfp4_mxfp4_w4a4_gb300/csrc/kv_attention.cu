@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
     const int row0 = (blockIdx.y - head * p.row_tiles) * ROWS;
     int q_start, n;
     group_rows(p.q_offsets, b, p.T, &q_start, &n);
-    if (row0 >= n * p.group)
+    const int live = min(n, p.max_draft) * p.group;  // the head's rows
+    if (row0 >= live)
         return;
     const int ctx = max(min(__ldg(p.context_lens + b), p.max_len - n), 0);
     const int len = min(ctx + n, p.max_len);
@@ -223,8 +224,10 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
     if (t_begin >= len)
         return;
     const int t_end = min(len, t_begin + p.chunk);
-    const int rows = min(ROWS, n * p.group - row0);
+    const int rows = min(ROWS, live - row0);
     const int splits = (len + p.chunk - 1) / p.chunk;
+    if (n > p.max_draft && blockIdx.x == 0 && row0 == 0)
+        void_rows(p, head, q_start, n, threadIdx.x, kWarps * 32);
 
     // this lane's share of Q: row g of each column tile, 8 elements of every
     // block, as f16 times a power of two of the row
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_attention_join_kernel(cons
     int q_start, n;
     const int b = sequence_of(p, tok);
     group_rows(p.q_offsets, b, p.T, &q_start, &n);
-    if (tok < q_start || tok >= q_start + n)
+    if (tok < q_start || tok >= q_start + min(n, p.max_draft))
         return;
     const int ctx = max(min(__ldg(p.context_lens + b), p.max_len - n), 0);
     const int splits = min((min(ctx + n, p.max_len) + p.chunk - 1) / p.chunk, kMaxSplits);
@@ -710,6 +713,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream)
     p.q_heads = a.q_heads;
     p.group = a.q_heads / a.cache.heads;
     p.row_tiles = pl.row_tiles;
+    p.max_draft = a.max_draft;
     p.chunk = pl.chunk;
     p.whole = a.max_seq <= 512;
     p.prefix = nullptr;

@@ -31,6 +31,7 @@ struct AttnParams {
     int q_heads;
     int group;
     int row_tiles;
+    int max_draft;  // drafted tokens of a sequence that are computed; those past it give NaN
     int chunk;      // tokens per split (stream kernel)
     DivMagic page_div;  // by the page size
     DivMagic group_div;  // by the query heads per key/value head
@@ -115,6 +116,24 @@ __device__ __forceinline__ int sequence_of(const AttnParams& p, int tok)
             hi = mid;
     }
     return lo;
+}
+
+// The rows of a key head of sequence tokens past the bound: NaN, so that a bound
+// which the caller's offsets exceed shows in the results.
+__device__ __forceinline__ void void_rows(const AttnParams& p, int head, int q_start, int n, int thread, int threads)
+{
+    const int vectors = p.cache.dim / 8;
+    const int64_t count = static_cast<int64_t>(n - p.max_draft) * p.group * vectors;
+#pragma unroll 1
+    for (int64_t i = thread; i < count; i += threads) {
+        const int64_t row = i / vectors;
+        const int d = static_cast<int>(i - row * vectors) * 8;
+        const int64_t tok = q_start + p.max_draft + row / p.group;
+        const int hq = head * p.group + static_cast<int>(row % p.group);
+        *reinterpret_cast<uint4*>(p.out + tok * p.ot + hq * p.oh + d) = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        if (d == 0 && p.lse != nullptr)
+            p.lse[tok * p.q_heads + hq] = __uint_as_float(0x7FC00000u);
+    }
 }
 
 // Joining a row's parts: one CTA per row, for rows with many parts; its warps

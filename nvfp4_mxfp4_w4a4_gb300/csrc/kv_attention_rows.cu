@@ -245,9 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const At
                 named_barrier_sync(1, kSoftmaxWarps * 32);
                 continue;
             }
-            const int head = wk.head, row0 = wk.row0(), n = wk.n, ctx = wk.ctx, len = wk.len, b = wk.b;
+            const int head = wk.head, row0 = wk.row0(), ctx = wk.ctx, len = wk.len, b = wk.b;
             const int q_start = wk.q_start, lo = wk.lo;
-            const int rows = min(p.part_rows, n * p.group - row0);
+            const int rows = min(p.part_rows, wk.rows(p) - row0);
             const int node = static_cast<int>(div_by_magic(row0 + r, p.group_div));  // of this thread's row
 
             // Q, in the stored order of a head's elements (rows past the last keep what is
@@ -451,6 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const At
                         p.lse[tok * p.q_heads + hq] = (ml + log2f(sum)) * 0.69314718055994531f;
                 }
             }
+            if (wk.n > p.max_draft && wk.lo == 0 && wk.row0() == 0)
+                void_rows(p, wk.head, wk.q_start, wk.n, threadIdx.x, kSoftmaxWarps * 32);
             g0 += tiles;
             // Q's place, O and the unit may be written again
             tc_fence_before_sync();

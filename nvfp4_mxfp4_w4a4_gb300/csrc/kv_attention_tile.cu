@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             }
             const int head = wk.head, row0 = wk.row0(), n = wk.n, ctx = wk.ctx, len = wk.len, b = wk.b;
             const int q_start = wk.q_start, lo = wk.lo;
-            const int rows = min(NR, n * p.group - row0);
+            const int rows = min(NR, wk.rows(p) - row0);
 
             // Q, in the stored order of a head's elements; fresh references
             for (int i = threadIdx.x; i < NR * (kDim / 8); i += kSoftmaxWarps * 32) {
@@ -519,6 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                         *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) = make_float2(m, ls);
                 }
             }
+            if (wk.n > p.max_draft && wk.lo == 0 && wk.row0() == 0)
+                void_rows(p, wk.head, wk.q_start, wk.n, threadIdx.x, kSoftmaxWarps * 32);
             // Q's and P^T's places and the unit may be written again
             named_barrier_sync(5, kSoftmaxWarps * 32);
             if (left > 0) {

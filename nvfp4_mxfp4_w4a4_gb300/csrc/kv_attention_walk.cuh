@@ -84,7 +84,7 @@ struct Walk {
         ctx = max(min(__ldg(p.context_lens + b), p.max_len - n), 0);
         len = min(ctx + n, p.max_len);
         tiles = (len + kTile - 1) / kTile;
-        row_tiles = min((n * p.group + kRows - 1) / kRows, p.row_tiles);
+        row_tiles = (rows(p) + kRows - 1) / kRows;
         units = row_tiles * p.cache.heads;
     }
     __device__ __forceinline__ void next(const AttnParams& p)
@@ -110,6 +110,8 @@ struct Walk {
         left -= lead + max(here, int64_t(0));
         return static_cast<int>(max(here, int64_t(0)));
     }
+    // of a key head: those of the drafted tokens within the bound
+    __device__ __forceinline__ int rows(const AttnParams& p) const { return min(n, p.max_draft) * p.group; }
     __device__ __forceinline__ int row0() const { return (unit - head * row_tiles) * kRows; }
 };
 
@@ -405,10 +407,10 @@ __global__ void __launch_bounds__(kFew ? kJoinRows * 32 : 128, 8) kv_attention_r
     Walk<kRows> w;
     w.b = sequence_of(p, tok);
     w.sequence(p);
+    if (tok < w.q_start || tok - w.q_start >= min(w.n, p.max_draft))
+        return;
     const int head = hq / p.group;
     const int r = (tok - w.q_start) * p.group + hq - head * p.group;  // of the head's rows
-    if (tok < w.q_start || tok >= w.q_start + w.n || r >= w.row_tiles * kRows || r % kRows >= p.part_rows)
-        return;
     const int64_t per = p.prefix[p.batch];
     const int64_t from = p.prefix[w.b] + static_cast<int64_t>(head * w.row_tiles + r / kRows) * (w.tiles + kUnitTiles) +
                          kUnitTiles;

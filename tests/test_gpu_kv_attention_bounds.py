@@ -1,0 +1,54 @@
+"""Attention with lengths that the host's bounds do not hold, or only just.
+
+A sequence with more drafted tokens than max_draft: the tokens up to the bound
+are computed as ever (bounds of test_gpu_kv_attention), those past it give NaN
+in the output and the log-sum, whatever the output and the workspace held."""
+import numpy as np
+import pytest
+
+import _layer_ref as R
+from _util import bf16_bits_host, bf16_bits_to_f64, dev, host, lib
+from test_gpu_kv_attention import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    return lib()
+
+
+def _attend(L, p, max_draft, max_seq, lens=None):
+    """The problem's call with bounds of the caller's, on buffers that hold plausible numbers."""
+    import torch
+
+    arrays = [dev(a) for a in p.arrays]
+    cache = L.kv_cache(*arrays, p.page, p.fmt)
+    q = p.q.cuda()
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((p.total, p.heads * p.group), 7.0, device="cuda")
+    need = L.fp4_kv_attention_workspace_size(len(p.lens), p.total, p.heads * p.group, p.heads, p.dim, max_seq, max_draft)
+    ws = torch.ones(max(need, 4) // 4, device="cuda")
+    ctx = dev(np.array([c for c, _ in p.lens], np.int32))
+    L.fp4_kv_attention(cache, q, out, dev(p.table), ctx, dev(p.cu), max_seq, max_draft, ws,
+                       tree_mask=dev(p.mask_bits().view(np.int32)) if p.tree else None, lse=lse, softmax_scale=p.scale)
+    assert L.fp4_get_device_status() == 0
+    return bf16_bits_to_f64(bf16_bits_host(out)), host(lse).astype(np.float64)
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.MXFP8])
+# heads of a key head, and the bound: kernels of 4, 8, 16, 32 and 128 rows and of two row tiles
+@pytest.mark.parametrize("group,bound", [(1, 3), (4, 1), (3, 2), (4, 4), (4, 7), (1, 20), (4, 9), (8, 20)])
+@pytest.mark.parametrize("ctx,max_seq", [(40, 400), (2300, 4000)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_tokens_past_the_bound_are_nan(L, fmt, group, bound, ctx, max_seq, tree):
+    over = bound + 5 if bound < 16 else bound + 41
+    p = Problem([(ctx, over), (11, bound), (ctx // 2, bound + 1), (3, 0)], 2, group, 64, 16, fmt, tree, seed=bound + group)
+    out, lse = _attend(L, p, bound, max_seq)
+    past = np.zeros(p.total, bool)
+    for b, (_, n) in enumerate(p.lens):
+        past[p.cu[b] + bound:p.cu[b] + max(n, bound)] = True
+    assert past.any() and np.isnan(out[past]).all() and np.isnan(lse[past]).all()
+    # the tokens up to the bound see what they saw
+    whole, wl = p.run(L)
+    p.check(np.where(past[:, None, None], whole, out), np.where(past[:, None], wl, lse))
