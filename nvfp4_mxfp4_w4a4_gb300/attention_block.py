@@ -80,10 +80,14 @@ class AttentionBlock:
         [tokens]; block_table: int32 [batch, pages]; context_lens: int32 [batch];
         q_offsets: int32 [batch + 1]; tree_mask: int32 [tokens, max_draft / 32,
         rounded up] or None.
-        Returns bf16 [tokens, hidden], a view of a buffer that the next step reuses."""
+        Returns bf16 [tokens, hidden], a view of a buffer that the next step reuses.
+        More than max_draft tokens of one sequence are an error: where the sum over
+        the sequences shows it, a ValueError, otherwise NaN in the rows past the bound."""
         T, hq, hkv, d = x.shape[0], self.q_heads, self.kv_heads, self.head_dim
         if T > self.max_tokens or block_table.shape[0] > self.max_batch:
             raise ValueError("more tokens or sequences than the block was made for")
+        if T > block_table.shape[0] * self.max_draft:
+            raise ValueError("more tokens than max_draft for each sequence")
         qkv = self.qkv(x, self.projected[:T], self.linear_ws)
         q = qkv[:, :hq * d].unflatten(1, (hq, d))
         k = qkv[:, hq * d:(hq + hkv) * d].unflatten(1, (hkv, d))
