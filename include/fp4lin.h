@@ -117,8 +117,9 @@ FP4LIN_API fp4_status fp4_get_device_status(void);
 
 /* Test hook for the bounded device waits (no counterpart on the pages: it
  * exists so that tests can drive the library's failure path without a GPU
- * fault).  Process-wide, read by each later GEMM call when it is enqueued:
- *   wait_limit_ns          limit of every bounded wait of the GEMM kernels
+ * fault).  Process-wide, read by each later GEMM or attention call when it is
+ * enqueued:
+ *   wait_limit_ns          limit of every bounded wait of their kernels
  *                          (0 restores the default of 1 s; otherwise
  *                          1e3 .. 1e10 ns);
  *   withhold_split_signal  1: in a split-K launch (see fp4_gemm_mxfp4_ws),
@@ -127,7 +128,12 @@ FP4LIN_API fp4_status fp4_get_device_status(void);
  *                          completes, its output is wrong, and
  *                          fp4_get_device_status() reports FP4_ERR_TIMEOUT;
  *                          the workspace counters are then left non-zero
- *                          (fp4_gemm_mxfp4_ws callers re-zero them).  0: off.
+ *                          (fp4_gemm_mxfp4_ws callers re-zero them).  In an
+ *                          fp4_kv_attention launch of more than 16 rows (drafted
+ *                          tokens x query heads of a key head), the first CTA
+ *                          leaves out its products with the values: its waits
+ *                          expire, what it would have written is not written,
+ *                          and the status is the same.  0: off.
  * Returns FP4_ERR_INVALID_ARG for other values.  Not for production use.    */
 FP4LIN_API fp4_status fp4_debug_set_wait_fault(uint64_t wait_limit_ns, int32_t withhold_split_signal);
 

@@ -131,6 +131,8 @@ int api_current_device(unsigned int** status) { return static_cast<int>(current_
 
 unsigned long long api_wait_limit_ns() { return g_wait_limit_ns.load(); }
 
+bool api_withhold_signal() { return g_withhold_split_signal.load() != 0; }
+
 }  // namespace fp4lin
 
 extern "C" {

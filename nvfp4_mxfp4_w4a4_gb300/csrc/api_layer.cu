@@ -381,6 +381,7 @@ fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_ar
     if ((st = device(&a.status)) != FP4_OK)
         return st;
     a.wait_ns = fp4lin::api_wait_limit_ns();
+    a.withhold = fp4lin::api_withhold_signal();
     a.q = args->q_bf16;
     a.out = args->out_bf16;
     a.lse = args->lse;

@@ -67,10 +67,12 @@ cudaError_t launch_coop(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sm
 unsigned long long current_context_id();
 
 // Shared by the C ABI translation units (api.cu): whether the current device
-// is supported and, optionally, its status word (an fp4_status value), and
-// the limit of bounded device waits now in force.
+// is supported and, optionally, its status word (an fp4_status value), the
+// limit of bounded device waits now in force, and whether the test hook
+// withholds a signal.
 int api_current_device(unsigned int** status);
 unsigned long long api_wait_limit_ns();
+bool api_withhold_signal();
 
 // Status word bits a kernel sets in the library-owned device status word.
 constexpr unsigned int kStatusTimeout = 1u;

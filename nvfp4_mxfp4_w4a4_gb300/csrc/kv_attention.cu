@@ -723,6 +723,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream)
     p.xscale = a.scale * 1.4426950408889634f;
     p.wait_ns = a.wait_ns;
     p.status = a.status;
+    p.withhold = a.withhold;
     p.part_rows = pl.part_rows;
     if (pl.tile) {
         p.xscale *= kUnscale;  // scores come out of the MMA times 2^-64

@@ -41,6 +41,7 @@ struct AttnParams {
     float* part_ml; // [splits][T * q_heads][2]
     unsigned long long wait_ns;  // limit of the bounded device waits, and where they report
     unsigned int* status;
+    bool withhold;  // test hook of the tile and row kernels: CTA 0 leaves out its second products
     // tile and row kernels: deal out whole units (short contexts) instead of tiles, and
     // where it leaves the sequences' first tiles and, behind them, a run's length
     bool whole;

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const At
                 mbar_arrive(&s_ready[1]);
             }
             __syncwarp();
-            for (uint32_t g = 0, end = *total_tiles; g < end; ++g) {
+            for (uint32_t g = 0, end = p.withhold && blockIdx.x == 0 ? 0u : *total_tiles; g < end; ++g) {
                 const uint32_t f = g & 1u;
                 ok = mbar_wait_bounded(&pv_ready[f], (g >> 1) & 1u, p.status, kStatusTimeout, limit);
                 if (!__all_sync(0xFFFFFFFFu, ok))

@@ -108,11 +108,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
     uint64_t* pv_done = pv_ready + 2;  // the tile is in O^T (the values' and P^T's buffers free)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
     volatile uint32_t* unit_start = tmem_slot + 1;  // by tile parity: the tile is its unit's first
-    volatile uint32_t* gave_up = tmem_slot + 3;     // by half and tile parity: a softmax wait of the tile ran out
+    volatile uint32_t* gave_up = tmem_slot + 3;     // a wait of the softmax ran out
     const uint32_t* total_tiles = tmem_slot + 7;    // of the run
 
     if (threadIdx.x == 0) {
-        gave_up[0] = gave_up[1] = gave_up[2] = gave_up[3] = 0u;
+        *gave_up = 0u;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_ready[i], 4 + kSoftmaxWarps);
             mbar_init(&s_done[i], 1);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             constexpr uint32_t idesc = idesc_bf16(128, NR, 1, 1);
             const uint64_t vd = smem_desc(smem_u32(smem + C::OFF_V), kSlab, 1024, 2);
             const uint64_t pd = smem_desc(smem_u32(smem + C::OFF_P), kSlab, 1024, 2);
-            for (uint32_t g = 0, end = *total_tiles; g < end; ++g) {
+            for (uint32_t g = 0, end = p.withhold && blockIdx.x == 0 ? 0u : *total_tiles; g < end; ++g) {
                 const uint32_t f = g & 1u;
                 ok = mbar_wait_bounded(&pv_ready[f], (g >> 1) & 1u, p.status, kStatusTimeout, limit);
                 if (!__all_sync(0xFFFFFFFFu, ok))
@@ -197,9 +197,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
         float* scratch = reinterpret_cast<float*>(smem + C::OFF_SCRATCH) + half * 5 * C::COLS;
         // the current unit stays in shared memory: one thread moves it on
         Walk<NR>& wk = places[0].walk;
+        // (once a wait has run out, the rest of the unit goes by without waiting; both halves
+        // leave together at its end)
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok)
+                ok = mbar_wait_bounded(bar, parity, p.status, kStatusTimeout, limit);
+        };
         uint32_t g = 0;
-        bool leave = false;
-        for (int64_t left = count; left > 0 && !leave;) {
+        for (int64_t left = count; left > 0;) {
             const int tiles = wk.run(p, left);
             if (tiles == 0) {
                 named_barrier_sync(5, kSoftmaxWarps * 32);  // everyone has read the unit
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             }
             fence_proxy_async_smem();
             named_barrier_sync(5, kSoftmaxWarps * 32);
-            if (lane == 0) {
+            if (ok && lane == 0) {
                 mbar_arrive(&s_ready[g & 1u]);
                 if (tiles > 1)
                     mbar_arrive(&s_ready[(g + 1u) & 1u]);
@@ -319,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                     }
                     return max(top & 0xFFFFu, top >> 16) > kSlackBits;
                 };
-                ok = mbar_wait_bounded(&s_done[f], ph, p.status, kStatusTimeout, limit) && ok;
+                wait(&s_done[f], ph);
                 // P^T's buffer is free when the tile before the last is in O^T
-                ok = mbar_wait_bounded(&pv_done[f], ph ^ 1, p.status, kStatusTimeout, limit) && ok;
+                wait(&pv_done[f], ph ^ 1);
                 __syncwarp();
                 tc_fence_after_sync();
                 auto tops = [&](auto masked, float* top) {
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
 #pragma unroll
                             for (int c = 0; c < C::COLS; ++c)
                                 l[c] *= factor[c];
-                            ok = mbar_wait_bounded(&pv_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u, p.status, kStatusTimeout, limit) && ok;
+                            wait(&pv_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u);
                             __syncwarp();
                             tc_fence_after_sync();
 #pragma unroll 1
@@ -392,20 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                     }
                     const float2 sign = step == kBack ? make_float2(-1.0f, -1.0f) : make_float2(1.0f, 1.0f);
                     const bool grow = edge ? weigh(std::true_type(), sign) : weigh(std::false_type(), sign);
-                    if (step == kAgain)
+                    if (step == kAgain || (step == kFirst && !named_barrier_or(1 + half, 128, grow)))
                         break;
-                    if (step == kFirst) {
-                        if (!ok)
-                            gave_up[2 * half + f] = 1u;
-                        __syncwarp();
-                        const bool rescale = named_barrier_or(1 + half, 128, grow);
-                        leave = gave_up[2 * half + f] != 0u;
-                        if (leave || !rescale)
-                            break;
-                    }
                 }
-                if (leave)
-                    break;  // all threads of the half at the same tile
                 if (edge && t < len) {
                     // a NaN value reaches exactly the rows that see its token
                     const int pi = static_cast<int>(div_by_magic(t, p.page_div));
@@ -427,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 __syncwarp();
                 if (threadIdx.x == 0)
                     unit_start[f] = it == 0;
-                if (lane == 0) {
+                if (ok && lane == 0) {
                     mbar_arrive(&pv_ready[f]);
                     if (it + 2 < tiles)
                         mbar_arrive(&s_ready[f]);
@@ -435,7 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             }
 
             // --------------------------------------------------- results
-            mbar_wait_bounded(&pv_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u, p.status, kStatusTimeout, limit);
+            wait(&pv_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u);
+            if (!ok)
+                *gave_up = 1u;
             __syncwarp();
             tc_fence_after_sync();
             // the unit's MMAs have read their operands: [4][NR] sums go to Q's place,
@@ -483,6 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             }
             tc_fence_before_sync();
             named_barrier_sync(5, kSoftmaxWarps * 32);
+            if (*gave_up)
+                break;
             // complete, or a part: of the unit that began before this run (slot 0), or of
             // the one that goes on after it (slot 1)
             const bool part = lo > 0 || tiles < wk.tiles;

@@ -73,6 +73,7 @@ struct KvAttentionArgs {
     void* workspace;
     unsigned int* status;
     unsigned long long wait_ns;
+    bool withhold;  // test hook
 };
 
 size_t kv_attention_workspace_bytes(int batch, int64_t T, int q_heads, int kv_heads, int dim, int64_t max_seq,
