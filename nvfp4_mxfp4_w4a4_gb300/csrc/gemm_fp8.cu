@@ -171,6 +171,9 @@ __global__ void __launch_bounds__(kThreadsQ) quant_weight_fp8_kernel(const __nv_
 //   warp 2  TMA of the tokens
 //   warp 3  a block's scales, to a ring in shared memory
 //   warps 4..  promotion: lane = weight row, NT / WGS columns per warp
+// Every wait that may last starts behind the grid dependency: its limit is for
+// this kernel's own copies and products, not for the kernel ahead, beside which
+// the CTA may already be resident.
 // A block has two barriers, `ready` (its operands and scales have landed and
 // its accumulator has been read) and `done` (its MMAs are complete), so that
 // the MMA thread, the one serial part, waits and commits once per block.
@@ -269,6 +272,8 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS, SwapCfg<NT>::CTAS)
             int it = 0;
             for (; it < nkb; ++it) {
                 const int s = it % C::STAGES;
+                if (it == C::STAGES && w && p.early_w)
+                    grid_dependency_wait();  // the first round of slots is free
                 // (a wait that gives up has given the copies in flight its whole limit to land)
                 if (!mbar_wait_bounded(&done[s], ((it / C::STAGES) & 1) ^ 1, p.status, kStatusTimeout, limit))
                     break;
@@ -279,6 +284,7 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS, SwapCfg<NT>::CTAS)
     } else if (warp == 1) {
         // ----------------------------------------------------- MMA issuer
         if (lane == 0) {
+            grid_dependency_wait();
             constexpr uint32_t idesc = idesc_e4m3(128, NT);
             const uint64_t wd = smem_desc(smem_u32(smem), 16, 1024, 2);
             const uint64_t xd = smem_desc(smem_u32(smem + C::OFF_X), 16, 1024, 2);
@@ -318,6 +324,7 @@ __global__ void __launch_bounds__(SwapCfg<NT>::THREADS, SwapCfg<NT>::CTAS)
         cp_async_wait_all();
     } else if (warp >= 4) {
         // ------------------------------------------------------ promotion
+        grid_dependency_wait();
         const int quad = warp & 3, col0 = ((warp - 4) >> 2) * C::COLS;
 #pragma unroll
         for (int j = 0; j < C::COLS; ++j)
