@@ -30,15 +30,25 @@ def allocate_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int,
 
 
 class Fp8Linear:
-    """y = x W^T (+ bias) with E4M3 weights and a scale per 128 x 128 block."""
+    """y = x W^T (+ bias) with E4M3 weights and a scale per 128 x 128 block: codes
+    [N, K] of one byte, scales float32 [N / 128, K / 128] rounded up, bias bf16 [N]."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None):
         self.codes, self.scales, self.bias = codes, scales, bias
         self.N, self.K = codes.shape
+        if codes.element_size() != 1 or not codes.is_contiguous() or not all(
+                t.is_cuda for t in (codes, scales, bias) if t is not None):
+            raise ValueError("codes are contiguous bytes [N, K]; all are device tensors")
+        if scales.dtype != torch.float32 or scales.shape != (-(-self.N // 128), -(-self.K // 128)) or not scales.is_contiguous():
+            raise ValueError("scales are contiguous float32, one for each 128 x 128 block")
+        if bias is not None and (bias.dtype != torch.bfloat16 or bias.shape != (self.N,) or not bias.is_contiguous()):
+            raise ValueError("bias is contiguous bf16 [N]")
 
     @classmethod
     def from_bf16(cls, w: torch.Tensor, bias: torch.Tensor | None = None) -> "Fp8Linear":
         N, K = w.shape
+        if w.dtype != torch.bfloat16 or not w.is_contiguous() or not w.is_cuda:
+            raise ValueError("w is a contiguous bf16 device tensor [N, K]")
         codes = torch.empty((N, K), dtype=torch.uint8, device=w.device)
         scales = torch.empty((-(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
         L.fp4_quant_weight_fp8_b128(w, codes, scales, N, K)
@@ -48,6 +58,10 @@ class Fp8Linear:
         return L.fp4_linear_fp8_b128_workspace_size(M, self.N, self.K)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor) -> torch.Tensor:
+        if x.dtype is not torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.K or not x.is_contiguous() or not x.is_cuda:
+            raise ValueError("x is a contiguous bf16 device tensor [M, K]")
+        if out.dtype is not torch.bfloat16 or out.shape != (x.shape[0], self.N) or not out.is_contiguous() or not out.is_cuda:
+            raise ValueError("out is a contiguous bf16 device tensor [M, N]")
         L.fp4_linear_fp8_b128(x, self.codes, self.scales, self.bias, out, x.shape[0], self.N, self.K, workspace)
         return out
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4lin.so")
@@ -103,6 +104,10 @@ class fp4_kv_attention_args(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float)]
 
 
+# the same layout in one step: the structure's constructor costs as much as the checks of a call
+_attention_args = struct.Struct("@PPPqqqqPqPPPiiqiiqf4x").pack
+
+
 _lib = None
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -171,7 +176,7 @@ def load(path: str = LIB_PATH):
                                              ctypes.POINTER(fp4_rope_params), _p, _p]),
             "fp4_kv_read": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), _p, _i64, _p, _i32, _i64, _p, _p, _p]),
             "fp4_kv_attention_workspace_size": (ctypes.c_size_t, [_i32, _i64, _i32, _i32, _i32, _i64, _i32]),
-            "fp4_kv_attention": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), ctypes.POINTER(fp4_kv_attention_args), _p,
+            "fp4_kv_attention": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), _p, _p,
                                                 ctypes.c_size_t, _p]),
             "fp4_linear_grouped_workspace_size": (ctypes.c_size_t, [_i64, _i32, _i64]),
             "fp4_linear_grouped": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _p, _p, _p, _i64, _i64, _p, ctypes.c_size_t,
@@ -492,10 +497,29 @@ def fp4_linear_fp8_b128(x_bf16, b, sb, bias_bf16, out_bf16, M, N, K, workspace, 
                                       _ptr(workspace), nbytes, _stream(stream)), "fp4_linear_fp8_b128")
 
 
+_torch = None  # set with the first rope_params, kv_cache or table, which the calls on tensors need
+
+
+def _need_torch():
+    global _torch
+    import torch as _torch
+
+
+def _expect(t, dtype, count, what):
+    """The kernels read these tensors by address alone: one of another type, with
+    gaps, too short or on the host is refused here."""
+    if t.dtype is not dtype or t.numel() < count or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s: a contiguous device tensor of %s with at least %d elements" % (what, dtype, count))
+
+
 class rope_params:
-    """fp4_rope_params of a table tensor [positions, rot_dim] (kept alive)."""
+    """fp4_rope_params of a float32 table tensor [positions, rot_dim] (kept alive)."""
 
     def __init__(self, table, rot_dim, layout=FP4_ROPE_HALF, inverse=False):
+        _need_torch()
+        if table.dim() != 2 or table.shape[1] != rot_dim:
+            raise ValueError("the table is [positions, rot_dim]")
+        _expect(table, _torch.float32, 0, "table")
         self.table = table
         self.struct = fp4_rope_params(table.data_ptr(), table.shape[0], rot_dim, layout,
                                       FP4_ROPE_INVERSE if inverse else 0)
@@ -503,40 +527,53 @@ class rope_params:
 
 
 class kv_cache:
-    """fp4_kv_cache of four uint8 tensors (kept alive): codes [pages, kv_heads,
-    page_size, head_dim or head_dim / 2], scales [pages, kv_heads, page_size,
-    head_dim / 32]."""
+    """fp4_kv_cache of four tensors of one byte per element (kept alive): codes
+    [pages, kv_heads, page_size, head_dim or head_dim / 2], scales [pages,
+    kv_heads, page_size, head_dim / 32]."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, page_size, format):
+        _need_torch()
         self.tensors = (k_codes, k_scales, v_codes, v_scales)
         for t in self.tensors:
-            if not t.is_contiguous():
-                raise ValueError("cache tensors are contiguous")
+            if not t.is_contiguous() or t.element_size() != 1 or not t.is_cuda:
+                raise ValueError("cache tensors are contiguous bytes on the device")
         pages, heads, page, width = k_codes.shape
         dim = width if format == FP4_ACT_MXFP8 else 2 * width
         if page != page_size or v_codes.shape != k_codes.shape or any(
                 s.shape != (pages, heads, page, dim // 32) for s in (k_scales, v_scales)):
             raise ValueError("cache tensors do not belong together")
+        self.heads, self.dim = heads, dim
         self.struct = fp4_kv_cache(*(t.data_ptr() for t in self.tensors), pages, page_size, heads, dim, format)
         self.ref = ctypes.byref(self.struct)
 
 
-def _strides(t):
-    """(token, head) strides of a [tokens, heads, dim] tensor with contiguous heads."""
-    a, b, c = t.stride()
-    if c != 1 and t.shape[2] != 1:
-        raise ValueError("the elements of a head are contiguous")
-    return a, b
+def _pair(a, b, what):
+    """The shape of two bf16 [tokens, heads, dim] tensors and their (token, head) strides."""
+    shape = a.shape
+    at, ah, ac = a.stride()
+    bt, bh, bc = b.stride()
+    kind = _torch.bfloat16
+    if b.shape != shape or a.dtype is not kind or b.dtype is not kind or not a.is_cuda or not b.is_cuda or (
+            (ac != 1 or bc != 1) and shape[2] != 1):
+        raise ValueError("%s: bf16 device tensors [tokens, heads, dim] of one shape with contiguous heads" % what)
+    return shape, at, ah, bt, bh
 
 
 def _table_stride(t):
-    """Row stride of a block table [batch, pages] (one row: its stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    """Rows and row stride of an int32 block table [batch, pages] (one row: its stride says nothing)."""
+    rows, width = t.shape
+    a, b = t.stride()
+    if t.dtype is not _torch.int32 or (b != 1 and width != 1) or not t.is_cuda:
+        raise ValueError("block_table: an int32 device tensor with contiguous rows")
+    return rows, a if rows > 1 else width
 
 
 def fp4_rope_table(table, positions, rot_dim, base, kind=FP4_ROPE_UNSCALED, factor=1.0, original_positions=0,
                    turns_fast=32.0, turns_slow=1.0, magnitude=1.0, stream=None):
     """Fills table float32 [positions, rot_dim] on the device."""
+    if not isinstance(table, int):
+        _need_torch()
+        _expect(table, _torch.float32, positions * rot_dim, "table")
     sc = fp4_rope_scaling(kind, factor, original_positions, turns_fast, turns_slow, magnitude)
     _check(load().fp4_rope_table(_ptr(table), positions, rot_dim, base, ctypes.byref(sc), _stream(stream)),
            "fp4_rope_table")
@@ -545,11 +582,8 @@ def fp4_rope_table(table, positions, rot_dim, base, kind=FP4_ROPE_UNSCALED, fact
 def fp4_rope(x, out, positions, rope, stream=None):
     """x, out: bf16 [tokens, heads, head_dim] with any token and head strides
     that are multiples of 8; positions: int32 [tokens]; rope: rope_params."""
-    tokens, heads, dim = x.shape
-    if out.shape != x.shape:
-        raise ValueError("x and out have one shape")
-    xt, xh = _strides(x)
-    ot, oh = _strides(out)
+    (tokens, heads, dim), xt, xh, ot, oh = _pair(x, out, "x, out")
+    _expect(positions, _torch.int32, tokens, "positions")
     _check(load().fp4_rope(x.data_ptr(), out.data_ptr(), positions.data_ptr(), rope.ref, tokens, heads, dim, xt, xh, ot,
                            oh, _stream(stream)), "fp4_rope")
 
@@ -557,23 +591,26 @@ def fp4_rope(x, out, positions, rope, stream=None):
 def fp4_kv_append(cache, k, v, slots, rope=None, positions=None, stream=None):
     """k, v: bf16 [tokens, kv_heads, head_dim]; slots: int64 [tokens]; with
     `rope` the keys are rotated first (positions: int32 [tokens])."""
-    s = cache.struct
-    if k.shape != v.shape or tuple(k.shape[1:]) != (s.kv_heads, s.head_dim):
+    (tokens, heads, dim), kt, kh, vt, vh = _pair(k, v, "k, v")
+    if heads != cache.heads or dim != cache.dim:
         raise ValueError("k and v are [tokens, kv_heads, head_dim] of the cache")
-    kt, kh = _strides(k)
-    vt, vh = _strides(v)
-    _check(load().fp4_kv_append(cache.ref, k.data_ptr(), v.data_ptr(), k.shape[0], kt, kh, vt, vh, slots.data_ptr(),
+    _expect(slots, _torch.int64, tokens, "slots")
+    if rope is not None and positions is not None:
+        _expect(positions, _torch.int32, tokens, "positions")
+    _check(load().fp4_kv_append(cache.ref, k.data_ptr(), v.data_ptr(), tokens, kt, kh, vt, vh, slots.data_ptr(),
                                 None if rope is None else rope.ref, _ptr(positions), _stream(stream)), "fp4_kv_append")
 
 
 def fp4_kv_read(cache, block_table, cu_lens, k_out, v_out, stream=None):
     """block_table: int32 [batch, pages]; cu_lens: int32 [batch + 1]; k_out,
     v_out: contiguous bf16 [rows, kv_heads, head_dim]."""
-    if not (k_out.is_contiguous() and v_out.is_contiguous()) or k_out.shape != v_out.shape:
-        raise ValueError("k_out and v_out are contiguous and have one shape")
-    _check(load().fp4_kv_read(cache.ref, block_table.data_ptr(), _table_stride(block_table), cu_lens.data_ptr(),
-                              block_table.shape[0], k_out.shape[0], k_out.data_ptr(), v_out.data_ptr(),
-                              _stream(stream)), "fp4_kv_read")
+    (rows, heads, dim), *_ = _pair(k_out, v_out, "k_out, v_out")
+    if heads != cache.heads or dim != cache.dim or not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError("k_out and v_out are contiguous [rows, kv_heads, head_dim] of the cache")
+    batch, stride = _table_stride(block_table)
+    _expect(cu_lens, _torch.int32, batch + 1, "cu_lens")
+    _check(load().fp4_kv_read(cache.ref, block_table.data_ptr(), stride, cu_lens.data_ptr(), batch, rows,
+                              k_out.data_ptr(), v_out.data_ptr(), _stream(stream)), "fp4_kv_read")
 
 
 def fp4_kv_attention_workspace_size(batch, tokens, q_heads, kv_heads, head_dim, max_seq_len, max_draft):
@@ -586,15 +623,24 @@ def fp4_kv_attention(cache, q, out, block_table, context_lens, q_offsets, max_se
     pages]; context_lens: int32 [batch]; q_offsets: int32 [batch + 1];
     tree_mask: int32 or uint32 [tokens, words] or None (causal); lse: float32
     [tokens, q_heads] or None; softmax_scale defaults to head_dim ** -0.5."""
-    tokens, heads, dim = q.shape
-    if out.shape != q.shape or dim != cache.struct.head_dim:
-        raise ValueError("q and out are [tokens, q_heads, head_dim]")
-    qt, qh = _strides(q)
-    ot, oh = _strides(out)
-    a = fp4_kv_attention_args(q.data_ptr(), out.data_ptr(), _ptr(lse), qt, qh, ot, oh, block_table.data_ptr(),
-                              _table_stride(block_table), context_lens.data_ptr(), q_offsets.data_ptr(), _ptr(tree_mask),
-                              0 if tree_mask is None else tree_mask.shape[1], block_table.shape[0], tokens, heads,
-                              max_draft, max_seq_len, dim ** -0.5 if softmax_scale is None else softmax_scale)
+    (tokens, heads, dim), qt, qh, ot, oh = _pair(q, out, "q, out")
+    if dim != cache.dim:
+        raise ValueError("q and out are [tokens, q_heads, head_dim] with the cache's head_dim")
+    batch, stride = _table_stride(block_table)
+    _expect(context_lens, _torch.int32, batch, "context_lens")
+    _expect(q_offsets, _torch.int32, batch + 1, "q_offsets")
+    words = mask = log_sum = 0
+    if tree_mask is not None:
+        _, words = tree_mask.shape
+        _expect(tree_mask, _torch.uint32 if tree_mask.dtype is _torch.uint32 else _torch.int32, tokens * words, "tree_mask")
+        mask = tree_mask.data_ptr()
+    if lse is not None:
+        _expect(lse, _torch.float32, tokens * heads, "lse")
+        log_sum = lse.data_ptr()
+    if workspace is not None and not (workspace.is_contiguous() and workspace.is_cuda):
+        raise ValueError("workspace: a contiguous device tensor")
+    a = _attention_args(q.data_ptr(), out.data_ptr(), log_sum, qt, qh, ot, oh, block_table.data_ptr(), stride,
+                        context_lens.data_ptr(), q_offsets.data_ptr(), mask, words, batch, tokens, heads, max_draft,
+                        max_seq_len, dim ** -0.5 if softmax_scale is None else softmax_scale)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().fp4_kv_attention(cache.ref, ctypes.byref(a), _ptr(workspace), nbytes, _stream(stream)),
-           "fp4_kv_attention")
+    _check(load().fp4_kv_attention(cache.ref, a, _ptr(workspace), nbytes, _stream(stream)), "fp4_kv_attention")
