@@ -37,7 +37,8 @@ constexpr int kLaunchRegs = 96;  // per thread, which setmaxnreg deals out anew
 // MXFP8, 158 / 158 / 161 / 161 us) and then its tiles.
 constexpr int kUnitTiles = 5;
 constexpr int kLeastRun = kUnitTiles + 4;
-constexpr float kUnset = -1e30f;  // a row's reference before its first visible token
+// a row's reference before its first visible token: the lowest float32, which no score lies under
+constexpr float kUnset = -3.402823466e38f;
 
 // d[0..1] = a[0..1] * m + c[0..1] in one instruction.
 __device__ __forceinline__ void fma_pair(float* d, float a0, float a1, float2 m, float c0, float c1)

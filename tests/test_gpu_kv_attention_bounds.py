@@ -52,3 +52,28 @@ def test_tokens_past_the_bound_are_nan(L, fmt, group, bound, ctx, max_seq, tree)
     # the tokens up to the bound see what they saw
     whole, wl = p.run(L)
     p.check(np.where(past[:, None, None], whole, out), np.where(past[:, None], wl, lse))
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.MXFP8])
+@pytest.mark.parametrize("group,draft", [(4, 1), (4, 4), (4, 8), (4, 31)])
+def test_scores_far_below_zero_still_count(L, fmt, group, draft):
+    """Equal keys, every score -2^103: the softmax is uniform over what a row sees,
+    however far below zero the scores lie."""
+    import torch
+
+    p = Problem([(200, draft), (0, draft)], 2, group, 64, 16, fmt, tree=False, seed=draft)
+    p.arrays[0][:] = 0x38 if fmt == R.MXFP8 else 0x22      # ones
+    p.arrays[1][:] = 127 + 50
+    p.q = torch.full_like(p.q, -2.0 ** 50)
+    score = -p.scale * 64 * 2.0 ** 100
+    out, lse = p.run(L)
+    for b, (ctx, n) in enumerate(p.lens):
+        t = np.arange(ctx + n)
+        pg, sl = p.table[b, t // p.page], t % p.page
+        v = R.mx_values(R.unpack(p.arrays[2][pg, :, sl], fmt), p.arrays[3][pg, :, sl], fmt)
+        for i in range(n):
+            ref = v[:ctx + i + 1].mean(0).repeat(group, 0)
+            mag = np.abs(v[:ctx + i + 1]).mean(0).repeat(group, 0)
+            bound = 1.01 * 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -19) * mag + (ctx + n) * 2.0 ** -61
+            assert np.all(np.abs(out[p.cu[b] + i] - ref) <= bound)
+            assert np.all(np.abs(lse[p.cu[b] + i] - score) <= (64 + 8) * 2.0 ** -23 * -score)
