@@ -264,10 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                     const int from = row0 + col0;  // of the head's rows
                     if (j < 0) {
                         vis = ~uint64_t(0);
-                    } else if (j < n && p.mask == nullptr) {
+                    } else if (j < len - ctx && p.mask == nullptr) {
                         const int c = max(j * p.group - from, 0);  // nodes from j on
                         vis = c < C::COLS ? ~uint64_t(0) << c : 0;
-                    } else if (j < n && (j >> 5) < p.mask_words) {
+                    } else if (j < len - ctx && (j >> 5) < p.mask_words) {
                         int node = static_cast<int>(div_by_magic(from, p.group_div));
                         const uint32_t* word = p.mask + static_cast<int64_t>(q_start + node) * p.mask_words + (j >> 5);
 #pragma unroll 4

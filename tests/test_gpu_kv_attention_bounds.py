@@ -77,3 +77,23 @@ def test_scores_far_below_zero_still_count(L, fmt, group, draft):
             bound = 1.01 * 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -19) * mag + (ctx + n) * 2.0 ** -61
             assert np.all(np.abs(out[p.cu[b] + i] - ref) <= bound)
             assert np.all(np.abs(lse[p.cu[b] + i] - score) <= (64 + 8) * 2.0 ** -23 * -score)
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.MXFP8])
+@pytest.mark.parametrize("group", [1, 4])
+def test_drafted_tokens_beyond_the_table_are_not_seen(L, fmt, group):
+    """20 drafted tokens over a table row of one page of 16: every row sees the tokens
+    that the table names, as if the cache ended there."""
+    p = Problem([(0, 20)], 2, group, 64, 16, fmt, tree=False, seed=group)
+    p.table = p.table[:, :1]
+    out, lse = _attend(L, p, 20, 20)
+    t = np.arange(16)
+    k, v = (R.mx_values(R.unpack(p.arrays[2 * i][p.table[0, 0], :, t], fmt), p.arrays[2 * i + 1][p.table[0, 0], :, t], fmt)
+            for i in range(2))
+    q, sees = p.q.double().numpy(), t[None] <= np.arange(20)[:, None]
+    for h in range(2 * group):
+        ref, rl, absv, mag = R.attend(q[:, h], k[:, h // group], v[:, h // group], sees, p.scale)
+        e = (64 + 8) * 2.0 ** -23 * mag
+        bound = 1.01 * 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[:, None] + 2.0 ** -19) * absv + 16 * 2.0 ** -61
+        assert np.all(np.abs(out[:, h] - ref) <= bound)
+        assert np.all(np.abs(lse[:, h] - rl) <= e + 2.0 ** -19 + 2.0 ** -22 * np.abs(rl))
