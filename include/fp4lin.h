@@ -650,7 +650,10 @@ typedef struct {
  *             magnitude.  The ramp's ends, as indexes, are
  *             rot_dim/2 * ln(original_positions / (2 pi turns)) / ln(base),
  *             rounded down (fast, at least 0) and up (slow, at most
- *             rot_dim/2 - 1).                                               */
+ *             rot_dim - 1: a ramp that ends past the last frequency, index
+ *             rot_dim/2 - 1, reaches it part of the way).  Where the slow end
+ *             does not lie above the fast one, every index above the slow end
+ *             is w_i / factor and the others are w_i.                       */
 typedef enum { FP4_ROPE_UNSCALED = 0, FP4_ROPE_LINEAR = 1, FP4_ROPE_BY_PARTS = 2 } fp4_rope_scaling_kind;
 typedef struct {
     int32_t kind;               /* fp4_rope_scaling_kind */

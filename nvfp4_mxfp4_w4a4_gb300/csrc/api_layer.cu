@@ -236,11 +236,12 @@ fp4_status fp4_rope_table(float* table, int64_t positions, int32_t rot_dim, doub
                 !std::isfinite(scaling->turns_fast) || scaling->original_positions <= 0 ||
                 !(scaling->magnitude > 0.0) || !std::isfinite(scaling->magnitude))
                 return FP4_ERR_INVALID_ARG;
-            // frequency index at which the original context holds a given number of turns
+            // frequency index at which the original context holds a given number of turns; the
+            // slow end may lie past the last frequency, rot_dim / 2 - 1
             const double half = rot_dim / 2;
             const double l = static_cast<double>(scaling->original_positions);
             f.low = std::fmax(std::floor(half * std::log(l / (scaling->turns_fast * kTwoPi)) / std::log(base)), 0.0);
-            f.high = std::fmin(std::ceil(half * std::log(l / (scaling->turns_slow * kTwoPi)) / std::log(base)), half - 1);
+            f.high = std::fmin(std::ceil(half * std::log(l / (scaling->turns_slow * kTwoPi)) / std::log(base)), rot_dim - 1.0);
             f.magnitude = scaling->magnitude;
         }
     }

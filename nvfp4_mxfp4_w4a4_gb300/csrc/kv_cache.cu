@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(float* __restrict_
         w = extrapolated / f.factor;
     } else if (f.scaling == kRopeByParts) {
         // frequencies that turn often within the original context stay, slow
-        // ones are interpolated, with a linear ramp between
-        const double t = f.high > f.low ? (j - f.low) / (f.high - f.low) : (j >= f.low ? 1.0 : 0.0);
+        // ones are interpolated, with a linear ramp between (a step behind `high` if it is empty)
+        const double t = f.high > f.low ? (j - f.low) / (f.high - f.low) : (j > f.high ? 1.0 : 0.0);
         const double ramp = fmin(fmax(t, 0.0), 1.0);
         w = extrapolated * (1.0 - ramp) + extrapolated / f.factor * ramp;
     }
