@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const At
             const int node = static_cast<int>(div_by_magic(row0 + r, p.group_div));  // of this thread's row
 
             // Q, in the stored order of a head's elements (rows past the last keep what is
-            // there: no row's results depend on another's)
+            // there; they have no say in when their warp's references move, so that nothing
+            // of it reaches the results)
             for (int i = threadIdx.x; i < rows * (kDim / 8); i += kSoftmaxWarps * 32) {
                 const int qr = i / (kDim / 8), c = i - qr * (kDim / 8);
                 const int qn = static_cast<int>(div_by_magic(row0 + qr, p.group_div));
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const At
                         return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.xscale;
                     };
                     const float now = edge ? top(std::true_type()) : top(std::false_type());
-                    if (__any_sync(0xFFFFFFFFu, now > m + kSlack)) {
+                    if (__any_sync(0xFFFFFFFFu, r < rows && now > m + kSlack)) {
                         const float next = fmaxf(m, now);
                         const float factor = exp2_approx(m - next);
                         m = next;
