@@ -172,31 +172,6 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The 16 visibility bits of row `node` for tokens base ... base + 15 relative
-// to the end of the context (negative: context tokens, always seen).
-__device__ __forceinline__ uint32_t visible16(const AttnParams& p, int64_t token, int node, int n, int base)
-{
-    uint32_t bits = 0;
-    const int lo = max(base, 0);
-    if (lo < n) {
-        if (p.mask != nullptr) {
-            const uint32_t* m = p.mask + token * p.mask_words;
-            const int w = lo >> 5;
-            const uint32_t w0 = w < p.mask_words ? __ldg(m + w) : 0u;
-            const uint32_t w1 = w + 1 < p.mask_words ? __ldg(m + w + 1) : 0u;
-            bits = __funnelshift_r(w0, w1, lo & 31);
-        } else {
-            const int k = node - lo;  // the row sees tokens up to itself
-            bits = k < 0 ? 0u : k >= 31 ? 0xFFFFFFFFu : (2u << k) - 1u;
-        }
-        if (n - lo < 32)
-            bits &= (1u << (n - lo)) - 1u;
-    }
-    if (base < 0)
-        bits = base <= -16 ? 0xFFFFu : (bits << -base) | ((1u << -base) - 1u);
-    return bits & 0xFFFFu;
-}
-
 // ROWS attention rows in COLS MMA columns; column c holds row c mod ROWS.
 template <int kFmt, int kDim, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_kernel(const AttnParams p)
@@ -211,12 +186,10 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, qd = lane & 3;
     const int b = blockIdx.z;
-    const int head = blockIdx.y / p.row_tiles;
-    const int row0 = (blockIdx.y - head * p.row_tiles) * ROWS;
+    const int head = blockIdx.y;
     int q_start, n;
     group_rows(p.q_offsets, b, p.T, &q_start, &n);
-    const int live = min(n, p.max_draft) * p.group;  // the head's rows
-    if (row0 >= live)
+    if (n == 0)
         return;
     const int ctx = max(min(__ldg(p.context_lens + b), p.max_len - n), 0);
     const int len = min(ctx + n, p.max_len);
@@ -224,9 +197,9 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
     if (t_begin >= len)
         return;
     const int t_end = min(len, t_begin + p.chunk);
-    const int rows = min(ROWS, live - row0);
+    const int rows = min(n, p.max_draft) * p.group;  // of the head, at most ROWS
     const int splits = (len + p.chunk - 1) / p.chunk;
-    if (n > p.max_draft && blockIdx.x == 0 && row0 == 0)
+    if (n > p.max_draft && blockIdx.x == 0)
         void_rows(p, head, q_start, n, threadIdx.x, kWarps * 32);
 
     // this lane's share of Q: row g of each column tile, 8 elements of every
@@ -236,11 +209,10 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int rr = (8 * nt + g) % ROWS;
-        const int r = row0 + rr;
         const bool live = rr < rows;
-        const int i = r / p.group;
+        const int i = rr / p.group;
         const __nv_bfloat16* src = p.q + static_cast<int64_t>(q_start + i) * p.qt +
-                                   static_cast<int64_t>(head * p.group + r - i * p.group) * p.qh + qd * 8;
+                                   static_cast<int64_t>(head * p.group + rr - i * p.group) * p.qh + qd * 8;
         uint32_t w[4 * S::SB];
         uint32_t am = 0;
 #pragma unroll
@@ -391,8 +363,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int rr = (8 * nt + 2 * qd + e) % ROWS;
-                    const int i = (row0 + rr) / p.group;
-                    vis[nt][e] = rr < rows ? visible16(p, q_start + i, i, n, t0 - ctx) : 0u;
+                    const int i = rr / p.group;
+                    vis[nt][e] = rr < rows ? visible32(p, q_start + i, i, n, t0 - ctx) : 0u;
                     if (t_end - t0 < kStep)
                         vis[nt][e] &= (1u << (t_end - t0)) - 1u;
                 }
@@ -555,9 +527,9 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS <= 8 ? 4 : 3) kv_attention_k
         }
         a0 *= kUnscale;
         a1 *= kUnscale;
-        const int ri = (row0 + r) / p.group;
+        const int ri = r / p.group;
         const int64_t tok = q_start + ri;
-        const int hq = head * p.group + row0 + r - ri * p.group;
+        const int hq = head * p.group + r - ri * p.group;
         if (splits == 1) {
             const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
             *reinterpret_cast<uint32_t*>(p.out + tok * p.ot + hq * p.oh + d) = pack2(a0 * inv, a1 * inv);
@@ -660,7 +632,7 @@ cudaError_t launch_stream(const AttnParams& p, const Plan& pl, cudaStream_t stre
             configured[dev] = ctx;
         }
     }
-    const dim3 grid(pl.splits, p.cache.heads * pl.row_tiles, p.batch);
+    const dim3 grid(pl.splits, p.cache.heads, p.batch);
     return launch_pdl(kern, grid, dim3(kWarps * 32), smem, stream, p);
 }
 

@@ -1,5 +1,6 @@
-// kv_attention.cuh -- what the two attention kernels over the MX-quantized
-// cache share: the launch's parameters and the exact bf16 form of a code.
+// kv_attention.cuh -- what the attention kernels over the MX-quantized cache
+// share: the launch's parameters, the exact bf16 form of a code, the tokens that
+// a row sees, and the joining of a row's parts.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,7 +31,7 @@ struct AttnParams {
     int T;
     int q_heads;
     int group;
-    int row_tiles;
+    int row_tiles;  // of a key head, at most (tile and row kernels)
     int max_draft;  // drafted tokens of a sequence that are computed; those past it give NaN
     int chunk;      // tokens per split (stream kernel)
     DivMagic page_div;  // by the page size
@@ -103,6 +104,32 @@ __device__ __forceinline__ void place_codes(uint32_t w, uint32_t* out)
         out[2] = ((w * 16u) & 0x80008000u) | ((w6 * 16u) & 0x01C001C0u);
         out[3] = (w & 0x80008000u) | (w6 & 0x01C001C0u);
     }
+}
+
+// The 32 visibility bits of row `node` for tokens base ... base + 31 relative
+// to the end of the context (negative: context tokens, always seen); n drafted
+// tokens are in the cache.
+__device__ __forceinline__ uint32_t visible32(const AttnParams& p, int64_t token, int node, int n, int base)
+{
+    uint32_t bits = 0;
+    const int lo = max(base, 0);
+    if (base > -32 && lo < n) {
+        if (p.mask != nullptr) {
+            const uint32_t* m = p.mask + token * p.mask_words;
+            const int w = lo >> 5;
+            const uint32_t w0 = w < p.mask_words ? __ldg(m + w) : 0u;
+            const uint32_t w1 = w + 1 < p.mask_words ? __ldg(m + w + 1) : 0u;
+            bits = __funnelshift_r(w0, w1, lo & 31);
+        } else {
+            const int k = node - lo;  // the row sees tokens up to itself
+            bits = k < 0 ? 0u : k >= 31 ? 0xFFFFFFFFu : (2u << k) - 1u;
+        }
+        if (n - lo < 32)
+            bits &= (1u << (n - lo)) - 1u;
+    }
+    if (base < 0)
+        bits = base <= -32 ? 0xFFFFFFFFu : (bits << -base) | ((1u << -base) - 1u);
+    return bits;
 }
 
 // The sequence that holds drafted token `tok`: the last that starts at or before it.

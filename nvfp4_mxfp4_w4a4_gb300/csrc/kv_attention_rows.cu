@@ -62,32 +62,6 @@ __device__ __forceinline__ float2 add_pair(float2 a, float b0, float b1)
     return r;
 }
 
-// The 32 visibility bits of row `node` for tokens base ... base + 31 relative
-// to the end of the context (negative: context tokens, always seen); n drafted
-// tokens are in the cache.
-__device__ __forceinline__ uint32_t visible32(const AttnParams& p, int64_t token, int node, int n, int base)
-{
-    uint32_t bits = 0;
-    const int lo = max(base, 0);
-    if (base > -32 && lo < n) {
-        if (p.mask != nullptr) {
-            const uint32_t* m = p.mask + token * p.mask_words;
-            const int w = lo >> 5;
-            const uint32_t w0 = w < p.mask_words ? __ldg(m + w) : 0u;
-            const uint32_t w1 = w + 1 < p.mask_words ? __ldg(m + w + 1) : 0u;
-            bits = __funnelshift_r(w0, w1, lo & 31);
-        } else {
-            const int k = node - lo;  // the row sees tokens up to itself
-            bits = k < 0 ? 0u : k >= 31 ? 0xFFFFFFFFu : (2u << k) - 1u;
-        }
-        if (n - lo < 32)
-            bits &= (1u << (n - lo)) - 1u;
-    }
-    if (base < 0)
-        bits = base <= -32 ? 0xFFFFFFFFu : (bits << -base) | ((1u << -base) - 1u);
-    return bits;
-}
-
 template <int kFmt, int kDim>
 struct RowsCfg {
     static constexpr int SLABS = kDim / 64;

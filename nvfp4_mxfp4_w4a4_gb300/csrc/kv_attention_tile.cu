@@ -62,7 +62,7 @@ __device__ __forceinline__ float warp_max(float x)
 template <int kFmt, int kDim>
 struct TileCfg {
     static constexpr int SLABS = kDim / 64;
-    static constexpr int COLS = NR / 2;  // rows per softmax thread
+    static constexpr int COLS = NR / 2;  // rows per softmax thread, one tensor memory load
     static constexpr int OFF_K = NR * 128 * SLABS;  // Q first
     static constexpr int OFF_V = OFF_K + 2 * SLABS * kSlab;
     static constexpr int OFF_P = OFF_V + 2 * SLABS * kSlab;
@@ -191,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
         const int quad = warp & 3, half = warp >> 2, col0 = half * C::COLS;
         const int token = quad * 32 + lane;  // of the tile
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-        constexpr int CW = 16;  // columns at a time
         const float2 xs = make_float2(p.xscale, p.xscale);
         // a half's memory for moving its references
         float* scratch = reinterpret_cast<float*>(smem + C::OFF_SCRATCH) + half * 5 * C::COLS;
@@ -259,68 +258,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 const int j = t - ctx;
                 // edge tiles: which of the thread's rows see its token, a node (drafted
                 // token, `group` rows) at a time
-                uint64_t vis = 0;
+                uint32_t vis = 0;
                 if (edge) {
                     const int from = row0 + col0;  // of the head's rows
                     if (j < 0) {
-                        vis = ~uint64_t(0);
+                        vis = 0xFFFFu;
                     } else if (j < len - ctx && p.mask == nullptr) {
                         const int c = max(j * p.group - from, 0);  // nodes from j on
-                        vis = c < C::COLS ? ~uint64_t(0) << c : 0;
+                        vis = c < C::COLS ? 0xFFFFu << c : 0u;
                     } else if (j < len - ctx && (j >> 5) < p.mask_words) {
                         int node = static_cast<int>(div_by_magic(from, p.group_div));
                         const uint32_t* word = p.mask + static_cast<int64_t>(q_start + node) * p.mask_words + (j >> 5);
 #pragma unroll 4
                         for (int c = node * p.group - from; c < C::COLS && node < n; c += p.group, ++node) {
-                            const uint64_t bit = (__ldg(word) >> (j & 31)) & 1u;
-                            const int end = min(c + p.group, 64), begin = max(c, 0);
-                            const uint64_t run = (end == 64 ? ~uint64_t(0) : (uint64_t(1) << end) - 1) >> begin << begin;
-                            vis |= bit ? run : 0;
+                            const uint32_t bit = (__ldg(word) >> (j & 31)) & 1u;
+                            const int end = min(c + p.group, C::COLS), begin = max(c, 0);
+                            vis |= bit ? ((1u << end) - 1u) >> begin << begin : 0u;
                             word += p.mask_words;
                         }
                     }
                 }
-                const uint32_t vis_lo = static_cast<uint32_t>(vis), vis_hi = static_cast<uint32_t>(vis >> 32);
                 // the scores' weights into P^T's buffer and the rows' sums; returns whether
                 // one is above 2^kSlack.  Edge tiles have code of their own (a branch per
                 // score would keep the compiler from overlapping them).
                 auto weigh = [&](auto masked, float2 sign) {
                     uint32_t top = 0u;
-                    uint32_t sb[2][CW];
-                    tmem_ld_32x32b_x16(s_addr, sb[0]);
+                    uint32_t s[C::COLS], w[C::COLS / 2];
+                    tmem_ld_32x32b_x16(s_addr, s);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < C::COLS; c += CW) {
-                        uint32_t* s = sb[c / CW & 1];
-                        tmem_ld_wait();
-                        if (c + CW < C::COLS)
-                            tmem_ld_32x32b_x16(s_addr + c + CW, sb[(c / CW + 1) & 1]);
-                        uint32_t w[CW / 2];
+                    for (int k = 0; k < C::COLS; k += 4) {
+                        const float4 r = *reinterpret_cast<const float4*>(ref + col0 + k);
+                        float x[4], e[4];
+                        fma_pair(x, __uint_as_float(s[k]), __uint_as_float(s[k + 1]), xs, r.x, r.y);
+                        fma_pair(x + 2, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]), xs, r.z, r.w);
 #pragma unroll
-                        for (int k = 0; k < CW; k += 4) {
-                            const float4 r = *reinterpret_cast<const float4*>(ref + col0 + c + k);
-                            float x[4], e[4];
-                            fma_pair(x, __uint_as_float(s[k]), __uint_as_float(s[k + 1]), xs, r.x, r.y);
-                            fma_pair(x + 2, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]), xs, r.z, r.w);
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                // finite however far the score lies above its reference
-                                e[h] = exp2_approx(min_nan(x[h], kCeiling));
-                                if constexpr (decltype(masked)::value)
-                                    e[h] = ((c + k + h < 32 ? vis_lo : vis_hi) >> ((c + k + h) & 31)) & 1u ? e[h] : 0.0f;
-                            }
-                            fma_pair(l + c + k, e[0], e[1], sign, l[c + k], l[c + k + 1]);
-                            fma_pair(l + c + k + 2, e[2], e[3], sign, l[c + k + 2], l[c + k + 3]);
-                            w[k / 2] = pack2(e[0], e[1]);
-                            w[k / 2 + 1] = pack2(e[2], e[3]);
-                            top = __vmaxu2(top, __vmaxu2(w[k / 2], w[k / 2 + 1]));
+                        for (int h = 0; h < 4; ++h) {
+                            // finite however far the score lies above its reference
+                            e[h] = exp2_approx(min_nan(x[h], kCeiling));
+                            if constexpr (decltype(masked)::value)
+                                e[h] = (vis >> (k + h)) & 1u ? e[h] : 0.0f;
                         }
+                        fma_pair(l + k, e[0], e[1], sign, l[k], l[k + 1]);
+                        fma_pair(l + k + 2, e[2], e[3], sign, l[k + 2], l[k + 3]);
+                        w[k / 2] = pack2(e[0], e[1]);
+                        w[k / 2 + 1] = pack2(e[2], e[3]);
+                        top = __vmaxu2(top, __vmaxu2(w[k / 2], w[k / 2 + 1]));
+                    }
 #pragma unroll
-                        for (int h = 0; h < CW / 8; ++h) {
-                            const int piece = (col0 + c) / 8 + h;
-                            *reinterpret_cast<uint4*>(pbuf + (piece >> 3) * kSlab + token * 128 +
-                                                      (((piece & 7) ^ (token & 7)) << 4)) =
-                                make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-                        }
+                    for (int h = 0; h < C::COLS / 8; ++h) {
+                        const int piece = col0 / 8 + h;
+                        *reinterpret_cast<uint4*>(pbuf + token * 128 + ((piece ^ (token & 7)) << 4)) =
+                            make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
                     }
                     return max(top & 0xFFFFu, top >> 16) > kSlackBits;
                 };
@@ -330,23 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                 __syncwarp();
                 tc_fence_after_sync();
                 auto tops = [&](auto masked, float* top) {
+                    uint32_t s[C::COLS];
+                    tmem_ld_32x32b_x16(s_addr, s);
+                    tmem_ld_wait();
+                    float mine = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < C::COLS; c += 16) {
-                        uint32_t s[16];
-                        tmem_ld_32x32b_x16(s_addr + c, s);
-                        tmem_ld_wait();
-                        float mine = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float x = __uint_as_float(s[k]) * p.xscale;
-                            if constexpr (decltype(masked)::value)
-                                x = ((c + k < 32 ? vis_lo : vis_hi) >> ((c + k) & 31)) & 1u ? x : -INFINITY;
-                            x = warp_max(x);
-                            mine = lane == k ? x : mine;
-                        }
-                        if (lane < 16)
-                            top[quad * C::COLS + c + lane] = mine;
+                    for (int k = 0; k < C::COLS; ++k) {
+                        float x = __uint_as_float(s[k]) * p.xscale;
+                        if constexpr (decltype(masked)::value)
+                            x = (vis >> k) & 1u ? x : -INFINITY;
+                        x = warp_max(x);
+                        mine = lane == k ? x : mine;
                     }
+                    if (lane < C::COLS)
+                        top[quad * C::COLS + lane] = mine;
                 };
                 // Weigh the tile; if a weight is too large, take its weights back, move the
                 // references to the rows' largest scores (per quadrant of tokens, by way of
@@ -381,16 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                             wait(&pv_done[(g - 1u) & 1u], ((g - 1u) >> 1) & 1u);
                             __syncwarp();
                             tc_fence_after_sync();
-#pragma unroll 1
-                            for (int c = 0; c < C::COLS; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(tmem_o + lanes + col0 + c, o);
-                                tmem_ld_wait();
+                            uint32_t o[C::COLS];
+                            tmem_ld_32x32b_x16(tmem_o + lanes + col0, o);
+                            tmem_ld_wait();
 #pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * factor[c + k]);
-                                tmem_st_32x32b_x16(tmem_o + lanes + col0 + c, o);
-                            }
+                            for (int k = 0; k < C::COLS; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * factor[k]);
+                            tmem_st_32x32b_x16(tmem_o + lanes + col0, o);
                             tmem_st_wait();
                             named_barrier_sync(3 + half, 128);  // the factors have been read
                         }
@@ -412,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                     for (int k = 0; k < C::SB; ++k)
                         bad |= __ldg(vs + k) == 0xFFu ? 1u << k : 0u;
                     if (bad)
+#pragma unroll 1
                         for (int c = 0; c < C::COLS; ++c)
                             if ((vis >> c) & 1u)
                                 atomicOr(&poison[col0 + c], bad);
@@ -440,8 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
             float* tile = reinterpret_cast<float*>(smem + C::OFF_P + (warp >> 2) * kSlab);
             static_assert(C::COLS * kDim * 4 <= kSlab, "a half's outputs in one buffer");
             // sums of the rows over the warp's tokens: each step sends half of the rows
-            // away and adds the other half's, until a lane holds COLS / 32 rows (or two
-            // lanes the same one)
+            // away and adds the other half's, until two lanes hold the same row
 #pragma unroll
             for (int d = 16, w = C::COLS / 2; d > 0; d >>= 1, w >>= 1) {
                 if (w > 0) {
@@ -456,26 +439,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                     l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], d);
                 }
             }
-            {
-                // the rows that the steps left: bit 4 of the lane chose the half, bit 3 the quarter, ...
-                constexpr int PER = C::COLS >= 32 ? C::COLS / 32 : 1;
-                const int r = C::COLS >= 32 ? lane * PER : lane >> 1;
-#pragma unroll
-                for (int c = 0; c < PER; ++c)
-                    sums[quad * NR + col0 + r + c] = l[c];
-            }
-            {
+            // (bit 4 of the lane chose the half of the rows, bit 3 the quarter, ...)
+            sums[quad * NR + col0 + (lane >> 1)] = l[0];
+            if (col0 < rows) {
                 const int d = element_at<kFmt>(token);  // TMEM lane = position in the head
-#pragma unroll 1
-                for (int c = 0; c < C::COLS && col0 + c < rows; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(tmem_o + lanes + col0 + c, o);
-                    tmem_ld_wait();
-                    if (token < kDim)
+                uint32_t o[C::COLS];
+                tmem_ld_32x32b_x16(tmem_o + lanes + col0, o);
+                tmem_ld_wait();
+                if (token < kDim)
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            tile[(c + k) * kDim + d] = __uint_as_float(o[k]);
-                }
+                    for (int k = 0; k < C::COLS; ++k)
+                        tile[k * kDim + d] = __uint_as_float(o[k]);
             }
             tc_fence_before_sync();
             named_barrier_sync(5, kSoftmaxWarps * 32);
