@@ -104,9 +104,6 @@ fp4_status check_attention_shape(int32_t batch, int64_t total, int32_t q_heads, 
         kv_heads <= 0 || q_heads % kv_heads != 0 || (dim != 64 && dim != 128) || max_seq_len <= 0 ||
         max_seq_len > (int64_t(1) << 30) || max_draft <= 0 || max_draft > 1024 || max_draft > max_seq_len)
         return FP4_ERR_SHAPE;
-    // row tiles of 8 rows and key heads share a grid dimension
-    if (static_cast<int64_t>(q_heads) * max_draft + kv_heads * int64_t(8) > 65535 * int64_t(8))
-        return FP4_ERR_SHAPE;
     return FP4_OK;
 }
 

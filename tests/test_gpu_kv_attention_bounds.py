@@ -97,3 +97,10 @@ def test_drafted_tokens_beyond_the_table_are_not_seen(L, fmt, group):
         bound = 1.01 * 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * e[:, None] + 2.0 ** -19) * absv + 16 * 2.0 ** -61
         assert np.all(np.abs(out[:, h] - ref) <= bound)
         assert np.all(np.abs(lse[:, h] - rl) <= e + 2.0 ** -19 + 2.0 ** -22 * np.abs(rl))
+
+
+@pytest.mark.parametrize("fmt", [R.MXFP4, R.MXFP8])
+def test_many_heads_with_the_largest_bound(L, fmt):
+    """768 query heads and a bound of 1024 drafted tokens: the bounds' product is no limit."""
+    p = Problem([(40, 2), (3, 1)], 8, 96, 64, 16, fmt, tree=False, seed=3)
+    p.check(*_attend(L, p, 1024, 2048))
