@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tile_kernel(const At
                     } else if (j < len - ctx && (j >> 5) < p.mask_words) {
                         int node = static_cast<int>(div_by_magic(from, p.group_div));
                         const uint32_t* word = p.mask + static_cast<int64_t>(q_start + node) * p.mask_words + (j >> 5);
-#pragma unroll 4
+#pragma unroll 2
                         for (int c = node * p.group - from; c < C::COLS && node < n; c += p.group, ++node) {
                             const uint32_t bit = (__ldg(word) >> (j & 31)) & 1u;
                             const int end = min(c + p.group, C::COLS), begin = max(c, 0);
