@@ -585,7 +585,8 @@ FP4LIN_API fp4_status fp4_gemm_mxfp4_grouped(const uint8_t* a, const uint8_t* sa
  *   weights      codes [N, K] u8, scales [ceil(N/128)][ceil(K/128)] float32
  *   activations  codes [M, K] u8, scales [ceil(K/128)][Mp] float32,
  *                Mp = M rounded up to 4 (fp4_fp8_act_scale_bytes bytes)
- * Value of an element: E4M3(code) * scale of its block.
+ * Value of an element: E4M3(code) * scale of its block (a weight with one scale
+ * for the whole tensor has it in every block's place).
  * K must be a multiple of 16 (the last block may be short), N of 8.         */
 
 /* Bytes of the activation scales (0 for an invalid shape). */

@@ -31,7 +31,8 @@ def allocate_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int,
 
 class Fp8Linear:
     """y = x W^T (+ bias) with E4M3 weights and a scale per 128 x 128 block: codes
-    [N, K] of one byte, scales float32 [N / 128, K / 128] rounded up, bias bf16 [N]."""
+    [N, K] of one byte, scales float32 [N / 128, K / 128] rounded up, bias bf16 [N].
+    A layer with one scale for its whole weight has that scale in every block."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None):
         self.codes, self.scales, self.bias = codes, scales, bias
@@ -68,7 +69,10 @@ class Fp8Linear:
 
 class AttentionBlock:
     """qkv: Fp8Linear [(q_heads + 2 kv_heads) head_dim, hidden]; o: Fp8Linear
-    [hidden, q_heads head_dim]; cache: allocate_cache(...); rope: fp4lin.rope_params."""
+    [hidden, q_heads head_dim]; cache: allocate_cache(...); rope: fp4lin.rope_params.
+    max_draft and max_seq_len choose the attention kernel and the cut of the
+    contexts: a block for pieces of a prompt decodes single tokens slower than one
+    made for them, which may share its cache, weights and rope."""
 
     def __init__(self, qkv: Fp8Linear, o: Fp8Linear, cache: L.kv_cache, rope: L.rope_params, q_heads: int,
                  max_tokens: int, max_batch: int, max_seq_len: int, max_draft: int):

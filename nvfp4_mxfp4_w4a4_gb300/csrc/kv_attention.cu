@@ -586,10 +586,10 @@ Plan make_plan(int batch, int kv_heads, int group, int64_t max_seq, int max_draf
     Plan pl;
     const int rows = group * max_draft;
     // Up to 32 rows the tile kernel: 8 tokens x 4 heads over 4000 tokens, 64
-    // sequences, 147 us with MXFP4 and 163 with MXFP8 (the row kernel 162 and 179).
-    // Above that the row kernel: 31 tokens over 16001, 8 sequences, 80 and 85 us
-    // (units of 128 rows in the tile kernel 113 and 140); 15 tokens 71 and 76
-    // (units of 64 rows 78 and 125).
+    // sequences, 141 us with MXFP4 and 156 with MXFP8 (the row kernel 164 and 168).
+    // Above that the row kernel: 31 tokens over 16001, 8 sequences, 78 and 84 us
+    // (a tile kernel with units of 128 rows 113 and 140); 15 tokens 72 and 77
+    // (with units of 64 rows 78 and 125).
     pl.rows = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
     pl.row_tiles = (rows + pl.rows - 1) / pl.rows;
     pl.tile = pl.rows > 16;

@@ -19,7 +19,8 @@
 //
 // Numbers: as in kv_attention.cu (exact bf16 elements with a multiplier that
 // carries 2^-64, probabilities rounded to bf16, everything else fp32), keys
-// included.  Elements of a group of 4 (E4M3) or 8 (E2M1) are stored in the
+// included.  (The rounding is relative 2^-8 at most, the size of the output's own;
+// what a product with its rest too would cost here was not measured.)  Elements of a group of 4 (E4M3) or 8 (E2M1) are stored in the
 // order in which their bits come out of a word; Q is stored in that order too,
 // and the output's elements are put back at the end.
 //
@@ -31,7 +32,7 @@
 // S are double-buffered, and the converters run ahead into the CTA's next unit.
 //
 // Measured: 8 trees of 31 tokens x 4 heads over up to 16001 tokens, 8 key heads
-// of 128: 80 us with MXFP4, 85 with MXFP8 (456 and 428 TFLOPS of the two
+// of 128: 78 us with MXFP4, 84 with MXFP8 (464 and 432 TFLOPS of the two
 // products; with the tokens on the M side and P in shared memory as in
 // kv_attention_tile.cu 113 and 140).  A tile takes about 1.05 us, of which the
 // MMAs are 0.5 and the issue slots 0.6: what bounds it is the way of a group's

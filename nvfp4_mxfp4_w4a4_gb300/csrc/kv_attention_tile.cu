@@ -19,7 +19,8 @@
 //
 // Numbers: as in kv_attention.cu (exact bf16 elements with a multiplier that
 // carries 2^-64, probabilities rounded to bf16, everything else fp32), keys
-// included.  Elements of a group of 4 (E4M3) or 8 (E2M1) are stored in the
+// included.  (The rounding is relative 2^-8 at most, the size of the output's own;
+// what a product with its rest too would cost here was not measured.)  Elements of a group of 4 (E4M3) or 8 (E2M1) are stored in the
 // order in which their bits come out of a word; Q is stored in that order too,
 // and the output's rows are put back at the end.
 //
@@ -32,8 +33,8 @@
 // ahead into the CTA's next unit.
 //
 // Measured: 4 tokens x 8 heads over 262139 of MXFP8, 8 key heads of 128: 172 us
-// (3.2 TB/s); 64 sequences of 8 tokens x 4 heads over 4000: 144 us with MXFP4,
-// 159 with MXFP8.  The converters' instructions bound it (92 of the 172 us of
+// (3.2 TB/s); 64 sequences of 8 tokens x 4 heads over 4000: 141 us with MXFP4,
+// 156 with MXFP8.  The converters' instructions bound it (92 of the 172 us of
 // every issue slot), then the latency between a tile's steps.
 #include "kv_attention_walk.cuh"
 
