@@ -761,7 +761,8 @@ typedef struct {
     int64_t tokens;
     int32_t q_heads;
     int32_t max_draft;           /* bound of n_b (host), 1 .. 1024: tokens past it give NaN (out and lse) */
-    int64_t max_seq_len;         /* bound of context_lens[b] + n_b (host): longer contexts are cut */
+    int64_t max_seq_len;         /* bound of context_lens[b] + n_b (host): a longer context is cut to it,
+                                  * which gives that sequence wrong numbers */
     float softmax_scale;         /* > 0 */
 } fp4_kv_attention_args;
 

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsQ) quant_weight_fp8_kernel(const __nv_
 //   warps 4..  promotion: lane = weight row, NT / WGS columns per warp
 // Every wait that may last starts behind the grid dependency: its limit is for
 // this kernel's own copies and products, not for the kernel ahead, beside which
-// the CTA may already be resident.
+// the CTA may already be resident (1 x 4096 x 4096: 7.78 us, 7.63 without).
 // A block has two barriers, `ready` (its operands and scales have landed and
 // its accumulator has been read) and `done` (its MMAs are complete), so that
 // the MMA thread, the one serial part, waits and commits once per block.
