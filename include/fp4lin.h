@@ -775,6 +775,157 @@ FP4LIN_API size_t fp4_kv_attention_workspace_size(int32_t batch, int64_t tokens,
 FP4LIN_API fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_args* args,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------- norms of queries and keys, with rotation */
+
+/* Every head x of the queries and of the keys of a token becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ * with a weight [head_dim] of its own for queries and keys, and is then
+ * rotated as by fp4_rope: float32 throughout, one rounding to bf16.  One
+ * launch for both.  With `rope` NULL there is no rotation (positions is not
+ * read).  Only the norm where there are no keys: kv_heads = 0, k and k_out
+ * NULL (and k_weight).
+ * head_dim 64, 128 or 256; strides in elements, multiples of 8; pointers
+ * 16-byte aligned.  An output may be its own input (same strides) and must
+ * not overlap an input otherwise.                                           */
+typedef struct {
+    const void* q_bf16;          /* [tokens][q_heads][head_dim] */
+    const void* k_bf16;          /* [tokens][kv_heads][head_dim] */
+    void* q_out_bf16;
+    void* k_out_bf16;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+    const void* q_weight_bf16;   /* [head_dim] */
+    const void* k_weight_bf16;
+    const int32_t* positions;    /* [tokens] */
+    int64_t tokens;
+    int32_t q_heads, kv_heads, head_dim;
+    float eps;                   /* >= 0, finite */
+} fp4_qk_norm_args;
+
+FP4LIN_API fp4_status fp4_qk_norm_rope(const fp4_qk_norm_args* args, const fp4_rope_params* rope, void* stream);
+
+/* ---------------------------------------- attention over whole prompts */
+
+/* Softmax attention of packed sequences, all in bf16: sequence b has the
+ * queries q_offsets[b] ... q_offsets[b + 1] - 1 (n of them) and the keys
+ * k_offsets[b] ... k_offsets[b + 1] - 1 (m of them).  Causal: query i sees the
+ * keys j <= i + m - n, so that the last query sees them all: m = n for whole
+ * prompts, m > n for a piece behind a context (whose keys and values
+ * fp4_kv_read gives back), m < n leaves the first n - m queries without keys.
+ * Not causal: every query sees all m keys.  Query head h reads key/value head
+ * h / (q_heads / kv_heads).
+ *   out  bf16: sum over the seen keys of softmax(softmax_scale q . k) v, zeros
+ *        for a query that sees none; the weights are rounded to bf16 for the
+ *        product with v, sums are float32
+ *   lse  float32 [tokens][q_heads] or NULL: log of the sum of
+ *        exp(softmax_scale q . k); -inf for a query that sees no key
+ * What a query does not see has no influence on it, NaN and Inf included.
+ * Queries behind the last sequence are not written.  Offsets are clamped to
+ * [0, tokens] (and each end to its start), so that wrong ones give wrong
+ * numbers but no access outside the tensors.
+ * head_dim 64 or 128; strides in elements, multiples of 8, those of k and v
+ * positive; pointers 16-byte aligned.  out must not overlap an input.       */
+typedef struct {
+    const void* q_bf16;          /* [tokens][q_heads][head_dim] */
+    const void* k_bf16;          /* [key_tokens][kv_heads][head_dim] */
+    const void* v_bf16;          /* the same shape */
+    void* out_bf16;              /* the shape of q */
+    float* lse;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+    const int32_t* q_offsets;    /* [batch + 1], ascending from 0 */
+    const int32_t* k_offsets;    /* [batch + 1]; may be q_offsets */
+    int64_t tokens, key_tokens;  /* below 2^31 - 256; key_tokens may be 0 (k, v NULL) */
+    int32_t batch;               /* 1 .. 65535 */
+    int32_t q_heads, kv_heads, head_dim;
+    int32_t causal;              /* 0 or 1 */
+    float softmax_scale;         /* > 0 */
+} fp4_prompt_attention_args;
+
+/* workspace: 256-byte aligned, at least the bytes that the size function
+ * gives for the same shape (0: NULL will do), no initialization needed;
+ * calls that share one must not overlap in time.                            */
+FP4LIN_API size_t fp4_prompt_attention_workspace_size(int32_t batch, int64_t tokens, int64_t key_tokens,
+                                           int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+FP4LIN_API fp4_status fp4_prompt_attention(const fp4_prompt_attention_args* args, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* ============================ around the FP4 weights: few rows, and experts */
+
+/* --------------------- matrix-vector products with 4-bit weights
+ *
+ * out[m, n] = bf16( sum_k x[m, k] W[n, k] + bias[n] ) for 1 to 8 rows of bf16
+ * activations that are not quantized, and the prepared weights of the GEMMs:
+ *   fp4_gemv_mxfp4  MXFP4 codes [N, K/2], SWIZZLED E8M0 scales per 32
+ *   fp4_gemv_nvfp4  NVFP4 codes [N, K/2], SWIZZLED E4M3 scales per 16 (as
+ *                   fp4_quant_nvfp4_ex writes and fp4_gemm_nvfp4 reads), times
+ *                   w_global
+ * Products of codes and activations are exact, sums are float32, one rounding.
+ * (Activations below 2^-31 of the largest of their block of 32 are rounded to
+ * multiples of 2^-38 of it; sums below 2^-126 may become zero.)  A NaN scale or
+ * a NaN or Inf activation reaches the outputs that it is a part of.
+ * M 0 .. 8 (0: nothing to do); N up to 2^24, K a multiple of 32 up to 65536;
+ * x, w, sw and out 16-byte aligned, bias (or NULL) 2-byte.  No workspace.    */
+FP4LIN_API fp4_status fp4_gemv_mxfp4(const void* x_bf16, const uint8_t* w, const uint8_t* sw, const void* bias_bf16,
+                          void* out_bf16, int64_t M, int64_t N, int64_t K, void* stream);
+FP4LIN_API fp4_status fp4_gemv_nvfp4(const void* x_bf16, const uint8_t* w, const uint8_t* sw, float w_global,
+                          const void* bias_bf16, void* out_bf16, int64_t M, int64_t N, int64_t K,
+                          void* stream);
+
+/* The same with an expert of its own for every row (a few tokens' MoE layer
+ * without sorting): out[r] = W_e x[r / rows_per_x] + bias_e, e = expert_ids[r].
+ * With the expert ids [tokens][top_k] of fp4_moe_dispatch as the rows,
+ * rows_per_x = top_k is the first projection (every choice reads its token) and
+ * rows_per_x = 1 the next one; fp4_moe_combine with row_of NULL adds them up.
+ * An id outside [0, E) gives a row of zeros.
+ *   x           [rows / rows_per_x, rounded up][K] bf16
+ *   expert_ids  int32 [rows] (device)
+ *   w, sw, bias [E][N][K/2], E consecutive SWIZZLED arrays, [E][N] or NULL, as
+ *               for fp4_gemm_mxfp4_grouped
+ * rows 0 .. 65535, 1 <= E <= 1024, rows_per_x >= 1; otherwise as above.      */
+FP4LIN_API fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* expert_ids, int32_t E, int64_t rows,
+                                  int32_t rows_per_x, const uint8_t* w, const uint8_t* sw,
+                                  const void* bias_bf16, void* out_bf16, int64_t N, int64_t K, void* stream);
+
+/* ------------------------------- tokens sorted by expert, and back
+ *
+ * The (token, choice) pairs of a MoE layer as rows grouped by expert, which
+ * fp4_linear_grouped and fp4_gemm_mxfp4_grouped take, and the way back.
+ *   expert_ids   int32 [tokens][top_k]: the expert of each choice; ids outside
+ *                [0, E) have no row (padding tokens, experts of other devices)
+ *   row_offsets  int32 [E + 1]: first row of each expert, then the rows in all
+ *   row_of       int32 [tokens][top_k]: the row of each choice, -1 for none
+ * Rows of one expert are in the order of (token, choice).  tokens * top_k below
+ * 2^31 - 256, top_k 1 .. 64, 1 <= E <= 1024, width a multiple of 8 up to 2^20; strides in
+ * elements, multiples of 8; bf16 pointers 16-byte aligned, others 4-byte.    */
+
+/* Fills row_offsets and row_of, and copies every choice's token to its row of
+ * sorted [tokens * top_k][width].  Rows from row_offsets[E] on are not written
+ * (the grouped calls take total_M = tokens * top_k and leave them alone).    */
+FP4LIN_API fp4_status fp4_moe_dispatch(const void* x_bf16, const int32_t* expert_ids, int64_t tokens, int32_t top_k,
+                            int32_t E, int64_t width, int64_t x_token_stride, void* sorted_bf16,
+                            int32_t* row_offsets, int32_t* row_of, void* stream);
+
+/* out[t] = bf16( sum_j weights[t, j] y[row_of[t, j]] ), float32, j ascending.
+ * y [rows][width]; choices whose row lies outside [0, rows) add nothing.
+ * row_of NULL: row t * top_k + j (fp4_gemv_mxfp4_experts).  weights float32
+ * [tokens][top_k], NULL: all 1 (the gradient of fp4_moe_dispatch).           */
+FP4LIN_API fp4_status fp4_moe_combine(const void* y_bf16, const int32_t* row_of, const float* weights, int64_t tokens,
+                           int32_t top_k, int64_t rows, int64_t width, void* out_bf16, int64_t out_token_stride,
+                           void* stream);
+
+/* The gradient of fp4_moe_combine: for every choice with a row
+ *   grad_y[row] = bf16( weights[t, j] grad_out[t] )
+ *   grad_weights[t, j] = sum over the width of grad_out[t] y[row]   (float32;
+ *                        0 for a choice without a row)
+ * No two choices may have the same row.  Rows of grad_y without a choice are
+ * not written.  weights NULL: all 1.  grad_weights NULL: not computed (y may
+ * then be NULL too).                                                         */
+FP4LIN_API fp4_status fp4_moe_combine_backward(const void* grad_out_bf16, const void* y_bf16, const int32_t* row_of,
+                                    const float* weights, int64_t tokens, int32_t top_k, int64_t rows,
+                                    int64_t width, int64_t grad_out_token_stride, void* grad_y_bf16,
+                                    float* grad_weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,10 +20,10 @@ LIB_PEAK = os.path.join(HERE, "libfp4peak.so")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["api.cu", "api_layer.cu", "quant.cu", "gemm.cu", "gemm_pair.cu", "gemm_noalloc.cu", "gemm_fp8.cu",
            "kv_cache.cu", "kv_attention.cu", "kv_attention_tile.cu",
-           "kv_attention_rows.cu"]
+           "kv_attention_rows.cu", "head_norm.cu", "prompt_attention.cu", "gemv.cu", "moe.cu"]
 PEAK_SOURCES = ["mma_peak.cu"]
 HEADERS = ["ptx.cuh", "formats.cuh", "internal.h", "gemm_fp8.h", "kv_cache.h", "kv_attention.cuh",
-           "kv_attention_walk.cuh"]
+           "kv_attention_walk.cuh", "rope.cuh", "decoder_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -1,6 +1,8 @@
 // api_layer.cu -- the extern "C" entry points of the operators around the FP4
 // linear layer: the FP8 linear layer, rotary positions, the MX-quantized
-// key/value cache and attention over it.  Same rules as api.cu: arguments are
+// key/value cache and attention over it, norms of queries and keys, attention
+// over whole prompts, matrix-vector products with 4-bit weights, and the way of
+// tokens to their experts and back.  Same rules as api.cu: arguments are
 // checked on the host before anything is enqueued, nothing is allocated,
 // nothing synchronizes.
 #include <cuda_runtime.h>
@@ -8,6 +10,7 @@
 #include <cmath>
 
 #include "../../include/fp4lin.h"
+#include "decoder_ops.h"
 #include "gemm_fp8.h"
 #include "internal.h"
 #include "kv_cache.h"
@@ -105,6 +108,53 @@ fp4_status check_attention_shape(int32_t batch, int64_t total, int32_t q_heads, 
         max_seq_len > (int64_t(1) << 30) || max_draft <= 0 || max_draft > 1024 || max_draft > max_seq_len)
         return FP4_ERR_SHAPE;
     return FP4_OK;
+}
+
+fp4_status check_prompt_shape(int32_t batch, int64_t tokens, int64_t keys, int32_t q_heads, int32_t kv_heads, int32_t dim)
+{
+    if (batch <= 0 || batch > 65535 || tokens < 0 || tokens >= kMaxDim - 256 || keys < 0 || keys >= kMaxDim - 256 ||
+        q_heads <= 0 || q_heads > 4096 || kv_heads <= 0 || q_heads % kv_heads != 0 || (dim != 64 && dim != 128) ||
+        tokens * (q_heads / kv_heads) >= kMaxDim - 256)
+        return FP4_ERR_SHAPE;
+    return FP4_OK;
+}
+
+// ------------------------------------------------------ products, experts
+
+fp4_status check_gemv(const void* x, const void* w, const void* sw, const void* bias, const void* out, int64_t N, int64_t K)
+{
+    if (N <= 0 || N > (int64_t(1) << 24) || K <= 0 || K % 32 != 0 || K > 65536)
+        return FP4_ERR_SHAPE;
+    if (!x || !w || !sw || !out)
+        return FP4_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(sw, 16) || !aligned(out, 16) || !aligned(bias, 2))
+        return FP4_ERR_ALIGNMENT;
+    return FP4_OK;
+}
+
+fp4_status gemv(const void* x, const uint8_t* w, const uint8_t* sw, float w_global, const void* bias, void* out, int64_t M,
+                int64_t N, int64_t K, bool nv, void* stream)
+{
+    if (M < 0 || M > 8)
+        return FP4_ERR_SHAPE;
+    if (M == 0)
+        return FP4_OK;
+    fp4_status st = check_gemv(x, w, sw, bias, out, N, K);
+    if (st != FP4_OK || (st = device()) != FP4_OK)
+        return st;
+    fp4lin::GemvArgs a = {};
+    a.x = x, a.w = w, a.sw = sw, a.bias = bias, a.out = out;
+    a.M = static_cast<int>(M), a.N = N, a.K = K;
+    a.nv = nv, a.w_global = w_global;
+    return from_cuda(fp4lin::launch_gemv(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status check_choices(int64_t tokens, int32_t top_k, int64_t width, int64_t stride)
+{
+    if (tokens < 0 || top_k <= 0 || top_k > 64 || tokens >= kMaxDim || tokens * top_k >= kMaxDim - 256 || width <= 0 ||
+        width % 8 != 0 || width > (int64_t(1) << 20) || stride < 0)
+        return FP4_ERR_SHAPE;
+    return stride % 8 == 0 ? FP4_OK : FP4_ERR_ALIGNMENT;
 }
 
 }  // namespace
@@ -401,6 +451,202 @@ fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_attention_ar
     a.scale = args->softmax_scale;
     a.workspace = workspace;
     return from_cuda(fp4lin::launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_qk_norm_rope(const fp4_qk_norm_args* args, const fp4_rope_params* rope, void* stream)
+{
+    if (!args)
+        return FP4_ERR_INVALID_ARG;
+    const fp4_qk_norm_args& g = *args;
+    if (g.tokens < 0 || g.tokens >= kMaxDim || g.q_heads <= 0 || g.q_heads > 65536 || g.kv_heads < 0 || g.kv_heads > 65536 ||
+        (g.head_dim != 64 && g.head_dim != 128 && g.head_dim != 256) ||
+        g.tokens * (g.q_heads + g.kv_heads) * (g.head_dim / 16) >= (int64_t(1) << 32) - 1024)
+        return FP4_ERR_SHAPE;  // 32-bit indexes of 16-element units
+    if (!(g.eps >= 0.0f) || !std::isfinite(g.eps))
+        return FP4_ERR_INVALID_ARG;
+    if (g.tokens == 0)
+        return FP4_OK;
+    if (!g.q_bf16 || !g.q_out_bf16 || !g.q_weight_bf16 || (g.kv_heads > 0 && (!g.k_bf16 || !g.k_out_bf16 || !g.k_weight_bf16)))
+        return FP4_ERR_INVALID_ARG;
+    fp4lin::HeadNormArgs a = {};
+    fp4_status st;
+    if (rope && (st = check_rope(rope, g.positions, g.head_dim, &a.rope)) != FP4_OK)
+        return st;
+    if ((st = check_strides(g.q_bf16, g.q_token_stride, g.q_head_stride)) != FP4_OK ||
+        (st = check_strides(g.q_out_bf16, g.q_out_token_stride, g.q_out_head_stride)) != FP4_OK)
+        return st;
+    if (g.kv_heads > 0 && ((st = check_strides(g.k_bf16, g.k_token_stride, g.k_head_stride)) != FP4_OK ||
+                           (st = check_strides(g.k_out_bf16, g.k_out_token_stride, g.k_out_head_stride)) != FP4_OK))
+        return st;
+    if (!aligned(g.q_weight_bf16, 16) || (g.kv_heads > 0 && !aligned(g.k_weight_bf16, 16)))
+        return FP4_ERR_ALIGNMENT;
+    if ((st = device()) != FP4_OK)
+        return st;
+    a.part[0] = {g.q_bf16, g.q_out_bf16, g.q_weight_bf16, g.q_token_stride, g.q_head_stride, g.q_out_token_stride, g.q_out_head_stride};
+    a.part[1] = {g.k_bf16, g.k_out_bf16, g.k_weight_bf16, g.k_token_stride, g.k_head_stride, g.k_out_token_stride, g.k_out_head_stride};
+    a.T = g.tokens;
+    a.q_heads = g.q_heads, a.kv_heads = g.kv_heads, a.dim = g.head_dim;
+    a.eps = g.eps;
+    return from_cuda(fp4lin::launch_head_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp4_prompt_attention_workspace_size(int32_t batch, int64_t tokens, int64_t key_tokens, int32_t q_heads,
+                                           int32_t kv_heads, int32_t head_dim)
+{
+    if (check_prompt_shape(batch, tokens, key_tokens, q_heads, kv_heads, head_dim) != FP4_OK || tokens == 0)
+        return 0;
+    return fp4lin::prompt_attention_workspace_bytes(batch, tokens, key_tokens, q_heads, kv_heads, head_dim);
+}
+
+fp4_status fp4_prompt_attention(const fp4_prompt_attention_args* args, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!args)
+        return FP4_ERR_INVALID_ARG;
+    const fp4_prompt_attention_args& g = *args;
+    fp4_status st = check_prompt_shape(g.batch, g.tokens, g.key_tokens, g.q_heads, g.kv_heads, g.head_dim);
+    if (st != FP4_OK)
+        return st;
+    if ((g.causal != 0 && g.causal != 1) || !(g.softmax_scale > 0.0f) || !std::isfinite(g.softmax_scale))
+        return FP4_ERR_INVALID_ARG;
+    if (g.tokens == 0)
+        return FP4_OK;
+    if (!g.q_bf16 || !g.out_bf16 || !g.q_offsets || !g.k_offsets || (g.key_tokens > 0 && (!g.k_bf16 || !g.v_bf16)))
+        return FP4_ERR_INVALID_ARG;
+    if ((st = check_strides(g.q_bf16, g.q_token_stride, g.q_head_stride)) != FP4_OK ||
+        (st = check_strides(g.out_bf16, g.out_token_stride, g.out_head_stride)) != FP4_OK)
+        return st;
+    if (g.key_tokens > 0) {
+        if ((st = check_strides(g.k_bf16, g.k_token_stride, g.k_head_stride)) != FP4_OK ||
+            (st = check_strides(g.v_bf16, g.v_token_stride, g.v_head_stride)) != FP4_OK)
+            return st;
+        // (strides of tensor maps; a dimension of one element has none)
+        constexpr int64_t kMaxStride = int64_t(1) << 38;
+        if ((g.key_tokens > 1 && (g.k_token_stride <= 0 || g.v_token_stride <= 0)) ||
+            (g.kv_heads > 1 && (g.k_head_stride <= 0 || g.v_head_stride <= 0)) || g.k_token_stride > kMaxStride ||
+            g.v_token_stride > kMaxStride || g.k_head_stride > kMaxStride || g.v_head_stride > kMaxStride)
+            return FP4_ERR_SHAPE;
+    }
+    const size_t need = fp4lin::prompt_attention_workspace_bytes(g.batch, g.tokens, g.key_tokens, g.q_heads, g.kv_heads, g.head_dim);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return FP4_ERR_INVALID_ARG;
+    if (!aligned(g.q_offsets, 4) || !aligned(g.k_offsets, 4) || !aligned(g.lse, 4) || (need > 0 && !aligned(workspace, 256)))
+        return FP4_ERR_ALIGNMENT;
+    fp4lin::PromptArgs a = {};
+    if ((st = device(&a.status)) != FP4_OK)
+        return st;
+    a.q = g.q_bf16, a.k = g.k_bf16, a.v = g.v_bf16, a.out = g.out_bf16, a.lse = g.lse;
+    a.qt = g.q_token_stride, a.qh = g.q_head_stride, a.kt = g.k_token_stride, a.kh = g.k_head_stride;
+    a.vt = g.v_token_stride, a.vh = g.v_head_stride, a.ot = g.out_token_stride, a.oh = g.out_head_stride;
+    a.q_offsets = g.q_offsets, a.k_offsets = g.k_offsets;
+    a.T = g.tokens, a.keys = g.key_tokens;
+    a.batch = g.batch, a.q_heads = g.q_heads, a.kv_heads = g.kv_heads, a.dim = g.head_dim;
+    a.causal = g.causal;
+    a.scale = g.softmax_scale;
+    a.workspace = workspace;
+    a.wait_ns = fp4lin::api_wait_limit_ns();
+    a.withhold = fp4lin::api_withhold_signal();
+    return from_cuda(fp4lin::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_gemv_mxfp4(const void* x_bf16, const uint8_t* w, const uint8_t* sw, const void* bias_bf16, void* out_bf16,
+                          int64_t M, int64_t N, int64_t K, void* stream)
+{
+    return gemv(x_bf16, w, sw, 1.0f, bias_bf16, out_bf16, M, N, K, false, stream);
+}
+
+fp4_status fp4_gemv_nvfp4(const void* x_bf16, const uint8_t* w, const uint8_t* sw, float w_global, const void* bias_bf16,
+                          void* out_bf16, int64_t M, int64_t N, int64_t K, void* stream)
+{
+    return gemv(x_bf16, w, sw, w_global, bias_bf16, out_bf16, M, N, K, true, stream);
+}
+
+fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* expert_ids, int32_t E, int64_t rows, int32_t rows_per_x,
+                                  const uint8_t* w, const uint8_t* sw, const void* bias_bf16, void* out_bf16, int64_t N,
+                                  int64_t K, void* stream)
+{
+    if (E <= 0 || E > fp4lin::kMaxGroupedExperts || rows < 0 || rows > 65535 || rows_per_x <= 0)
+        return FP4_ERR_SHAPE;
+    if (rows == 0)
+        return FP4_OK;
+    fp4_status st = check_gemv(x_bf16, w, sw, bias_bf16, out_bf16, N, K);
+    if (st != FP4_OK)
+        return st;
+    if (!expert_ids)
+        return FP4_ERR_INVALID_ARG;
+    if (!aligned(expert_ids, 4))
+        return FP4_ERR_ALIGNMENT;
+    if ((st = device()) != FP4_OK)
+        return st;
+    fp4lin::GemvArgs a = {};
+    a.x = x_bf16, a.w = w, a.sw = sw, a.bias = bias_bf16, a.out = out_bf16;
+    a.M = static_cast<int>(rows), a.N = N, a.K = K;
+    a.w_global = 1.0f;
+    a.expert_ids = expert_ids, a.E = E, a.rows_per_x = rows_per_x;
+    return from_cuda(fp4lin::launch_gemv(a, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_moe_dispatch(const void* x_bf16, const int32_t* expert_ids, int64_t tokens, int32_t top_k, int32_t E,
+                            int64_t width, int64_t x_token_stride, void* sorted_bf16, int32_t* row_offsets, int32_t* row_of,
+                            void* stream)
+{
+    fp4_status st = check_choices(tokens, top_k, width, x_token_stride);
+    if (st != FP4_OK)
+        return st;
+    if (E <= 0 || E > fp4lin::kMaxGroupedExperts)
+        return FP4_ERR_SHAPE;
+    // (no tokens: the offsets are still written)
+    if (!row_offsets || (tokens > 0 && (!x_bf16 || !expert_ids || !sorted_bf16 || !row_of)))
+        return FP4_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || !aligned(sorted_bf16, 16) || !aligned(expert_ids, 4) || !aligned(row_offsets, 4) ||
+        !aligned(row_of, 4))
+        return FP4_ERR_ALIGNMENT;
+    if ((st = device()) != FP4_OK)
+        return st;
+    return from_cuda(fp4lin::launch_moe_dispatch(x_bf16, expert_ids, tokens, top_k, E, width, x_token_stride, sorted_bf16,
+                                                 row_offsets, row_of, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_moe_combine(const void* y_bf16, const int32_t* row_of, const float* weights, int64_t tokens, int32_t top_k,
+                           int64_t rows, int64_t width, void* out_bf16, int64_t out_token_stride, void* stream)
+{
+    fp4_status st = check_choices(tokens, top_k, width, out_token_stride);
+    if (st != FP4_OK)
+        return st;
+    if (rows < 0 || rows >= kMaxDim)
+        return FP4_ERR_SHAPE;
+    if (tokens == 0)
+        return FP4_OK;
+    if (!out_bf16 || (rows > 0 && !y_bf16))
+        return FP4_ERR_INVALID_ARG;
+    if (!aligned(y_bf16, 16) || !aligned(out_bf16, 16) || !aligned(row_of, 4) || !aligned(weights, 4))
+        return FP4_ERR_ALIGNMENT;
+    if ((st = device()) != FP4_OK)
+        return st;
+    return from_cuda(fp4lin::launch_moe_combine(y_bf16, row_of, weights, tokens, top_k, rows, width, out_bf16,
+                                                out_token_stride, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_moe_combine_backward(const void* grad_out_bf16, const void* y_bf16, const int32_t* row_of,
+                                    const float* weights, int64_t tokens, int32_t top_k, int64_t rows, int64_t width,
+                                    int64_t grad_out_token_stride, void* grad_y_bf16, float* grad_weights, void* stream)
+{
+    fp4_status st = check_choices(tokens, top_k, width, grad_out_token_stride);
+    if (st != FP4_OK)
+        return st;
+    if (rows < 0 || rows >= kMaxDim)
+        return FP4_ERR_SHAPE;
+    if (tokens == 0)
+        return FP4_OK;
+    if (!grad_out_bf16 || (rows > 0 && (!grad_y_bf16 || (grad_weights && !y_bf16))))
+        return FP4_ERR_INVALID_ARG;
+    if (!aligned(grad_out_bf16, 16) || !aligned(y_bf16, 16) || !aligned(grad_y_bf16, 16) || !aligned(row_of, 4) ||
+        !aligned(weights, 4) || !aligned(grad_weights, 4))
+        return FP4_ERR_ALIGNMENT;
+    if ((st = device()) != FP4_OK)
+        return st;
+    return from_cuda(fp4lin::launch_moe_combine_backward(grad_out_bf16, y_bf16, row_of, weights, tokens, top_k, rows, width,
+                                                         grad_out_token_stride, grad_y_bf16, grad_weights,
+                                                         static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,320 @@
+// moe.cu -- the (token, choice) pairs of a mixture-of-experts layer as rows
+// grouped by expert, and back: the steps before and behind the grouped GEMM.
+//
+//   dispatch   a stable counting sort of the pairs by expert (row_offsets,
+//              row_of), then every token's vector to the rows of its choices
+//   combine    out[t] = sum_j w[t, j] y[row_of[t, j]]
+//   backward   grad_y[row_of[t, j]] = w[t, j] grad[t],
+//              grad_w[t, j] = <grad[t], y[row_of[t, j]]>
+//
+// All are bound by HBM but for the smallest calls, where the launches count.
+// Nothing is added by atomics: every result has one order.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "decoder_ops.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace fp4lin {
+namespace {
+
+// ---------------------------------------------------------------- sorting
+
+// One cluster sorts all pairs.  A warp owns a run of them and counts its experts
+// (lanes of one expert find one another by __match_any_sync, their first lane
+// adds); sums over the warps, over the cluster's CTAs (through their shared
+// memory) and over the experts then give each warp the row at which its pairs
+// of an expert begin.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSortThreads) moe_sort_kernel(const int32_t* __restrict__ ids, int pairs, int E,
+                                                                int32_t* __restrict__ row_offsets,
+                                                                int32_t* __restrict__ row_of)
+{
+    extern __shared__ uint32_t smem[];
+    uint32_t* hist = smem;                    // [kSortWarps][E]
+    uint32_t* total = hist + kSortWarps * E;  // [E] of this CTA
+    uint32_t* base = total + E;               // [E] first row of this CTA's pairs of an expert
+    __shared__ uint32_t warp_sum[kSortWarps];
+    grid_dependency_wait();
+    launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int ctas = gridDim.x;
+    // runs of whole warps' widths
+    const int steps = (pairs + ctas * kSortThreads - 1) / (ctas * kSortThreads);
+    const int first = (static_cast<int>(rank) * kSortWarps + warp) * steps * 32;
+    for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads)
+        hist[i] = 0;
+    __syncthreads();
+    uint32_t* mine = hist + warp * E;
+    for (int s = 0; s < steps; ++s) {
+        const int i = first + s * 32 + lane;
+        const int e = i < pairs ? __ldg(ids + i) : -1;
+        const bool live = e >= 0 && e < E;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, live ? e : -1);
+        if (live && lane == __ffs(same) - 1)
+            mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // counts -> those of the warps before, and the CTA's sums
+    for (int e = threadIdx.x; e < E; e += kSortThreads) {
+        uint32_t sum = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t n = hist[w * E + e];
+            hist[w * E + e] = sum;
+            sum += n;
+        }
+        total[e] = sum;
+    }
+    cluster_sync_all();
+    // (E <= kSortThreads: a thread per expert)
+    const int e = threadIdx.x;
+    uint32_t before = 0, all = 0;
+    if (e < E) {
+        for (int r = 0; r < ctas; ++r) {
+            const uint32_t n = ld_cluster_u32(mapa_shared(smem_u32(total + e), r));
+            before += r < static_cast<int>(rank) ? n : 0u;
+            all += n;
+        }
+    }
+    uint32_t x = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        x += lane >= d ? y : 0u;
+    }
+    if (lane == 31)
+        warp_sum[warp] = x;
+    __syncthreads();
+    uint32_t offset = x - all;
+    for (int w = 0; w < warp; ++w)
+        offset += warp_sum[w];
+    if (e < E) {
+        base[e] = offset + before;
+        if (rank == 0) {
+            row_offsets[e] = static_cast<int32_t>(offset);
+            if (e == E - 1)
+                row_offsets[E] = static_cast<int32_t>(offset + all);
+        }
+    }
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        const int i = first + s * 32 + lane;
+        const int ex = i < pairs ? __ldg(ids + i) : -1;
+        const bool live = ex >= 0 && ex < E;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, live ? ex : -1);
+        if (i < pairs)
+            row_of[i] = live ? static_cast<int32_t>(base[ex] + mine[ex] + __popc(same & ((1u << lane) - 1u))) : -1;
+        __syncwarp();
+        if (live && lane == __ffs(same) - 1)
+            mine[ex] += __popc(same);
+        __syncwarp();
+    }
+    cluster_sync_all();  // the others may still read this CTA's sums
+}
+
+// ---------------------------------------------------------------- vectors
+
+// Threads of a block: `across` (a power of two) vectors of 8 of a token, and as
+// many tokens as fit.
+constexpr int kThreads = 128;
+
+struct Shape {
+    int across_log;
+    dim3 grid;
+};
+
+Shape shape_of(int64_t tokens, int64_t width)
+{
+    Shape s;
+    s.across_log = 0;
+    while ((1 << s.across_log) < kThreads && (int64_t(8) << s.across_log) < width)
+        ++s.across_log;
+    const int64_t down = kThreads >> s.across_log;
+    s.grid = dim3(static_cast<unsigned>((tokens + down - 1) / down),
+                  static_cast<unsigned>((width / 8 + (int64_t(1) << s.across_log) - 1) >> s.across_log));
+    return s;
+}
+
+struct Place {
+    int64_t token;
+    int64_t at;  // first element of the vector
+};
+
+__device__ __forceinline__ Place place_of(int across_log)
+{
+    const int across = 1 << across_log;
+    return {static_cast<int64_t>(blockIdx.x) * (kThreads >> across_log) + (threadIdx.x >> across_log),
+            (static_cast<int64_t>(blockIdx.y) * across + (threadIdx.x & (across - 1))) * 8};
+}
+
+__global__ void __launch_bounds__(kThreads) moe_gather_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ row_of,
+                                                              int64_t tokens, int top_k, int64_t width, int64_t xt,
+                                                              __nv_bfloat16* __restrict__ sorted, int across_log)
+{
+    const Place p = place_of(across_log);
+    grid_dependency_wait();
+    launch_dependents();
+    if (p.token >= tokens || p.at >= width)
+        return;
+    const uint4 v = *reinterpret_cast<const uint4*>(x + p.token * xt + p.at);
+    for (int j = 0; j < top_k; ++j) {
+        const int64_t row = row_of[p.token * top_k + j];
+        if (row >= 0)
+            *reinterpret_cast<uint4*>(sorted + row * width + p.at) = v;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) moe_combine_kernel(const __nv_bfloat16* __restrict__ y, const int32_t* __restrict__ row_of,
+                                                               const float* __restrict__ weights, int64_t tokens, int top_k,
+                                                               int64_t rows, int64_t width, __nv_bfloat16* __restrict__ out,
+                                                               int64_t ot, int across_log)
+{
+    const Place p = place_of(across_log);
+    grid_dependency_wait();
+    launch_dependents();
+    if (p.token >= tokens || p.at >= width)
+        return;
+    float sum[8] = {};
+#pragma unroll 4
+    for (int j = 0; j < top_k; ++j) {
+        const int64_t pair = p.token * top_k + j;
+        const int64_t row = row_of != nullptr ? __ldg(row_of + pair) : pair;
+        if (row < 0 || row >= rows)
+            continue;
+        const float w = weights != nullptr ? __ldg(weights + pair) : 1.0f;
+        float f[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(y + row * width + p.at)), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum[i] += w * f[i];
+    }
+    *reinterpret_cast<uint4*>(out + p.token * ot + p.at) = pack8(sum);
+}
+
+// A warp per choice; the choices of a token share its gradient through L1.
+__global__ void __launch_bounds__(256) moe_combine_backward_kernel(const __nv_bfloat16* __restrict__ grad,
+                                                                   const __nv_bfloat16* __restrict__ y,
+                                                                   const int32_t* __restrict__ row_of,
+                                                                   const float* __restrict__ weights, int64_t pairs, int top_k,
+                                                                   int64_t rows, int64_t width, int64_t gt,
+                                                                   __nv_bfloat16* __restrict__ grad_y,
+                                                                   float* __restrict__ grad_w)
+{
+    grid_dependency_wait();
+    launch_dependents();
+    const int64_t pair = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (pair >= pairs)
+        return;
+    const int64_t row = row_of != nullptr ? __ldg(row_of + pair) : pair;
+    float dot = 0.0f;
+    if (row >= 0 && row < rows) {
+        const float w = weights != nullptr ? __ldg(weights + pair) : 1.0f;
+        const __nv_bfloat16* g = grad + pair / top_k * gt;
+        for (int64_t at = lane * 8; at < width; at += 256) {
+            float f[8];
+            unpack8(__ldg(reinterpret_cast<const uint4*>(g + at)), f);
+            if (grad_w != nullptr) {
+                float v[8];
+                unpack8(__ldg(reinterpret_cast<const uint4*>(y + row * width + at)), v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dot += f[i] * v[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] *= w;
+            *reinterpret_cast<uint4*>(grad_y + row * width + at) = pack8(f);
+        }
+    }
+    if (grad_w != nullptr) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+        if (lane == 0)
+            grad_w[pair] = dot;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t tokens, int top_k, int E, int64_t width, int64_t xt,
+                                void* sorted, int32_t* row_offsets, int32_t* row_of, cudaStream_t stream)
+{
+    // per device and context, once: the shared-memory opt-in
+    static std::mutex mu;
+    static unsigned long long configured[64] = {};
+    constexpr int kMaxSmem = (kSortWarps + 2) * kMaxGroupedExperts * 4;
+    static_assert(kMaxSmem <= 232448 - 1024 && kMaxGroupedExperts <= kSortThreads, "a thread per expert");
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || dev < 0 || dev >= 64)
+        return err != cudaSuccess ? err : cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const unsigned long long ctx = current_context_id();
+        if (configured[dev] == 0 || configured[dev] != ctx) {
+            err = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+            if (err != cudaSuccess)
+                return err;
+            configured[dev] = ctx;
+        }
+    }
+    const int64_t pairs = tokens * top_k;
+    const int ctas = pairs <= kSortThreads ? 1 : kSortCluster;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(kSortWarps + 2) * E * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, moe_sort_kernel, ids, static_cast<int>(pairs), E, row_offsets, row_of);
+    if (err != cudaSuccess || tokens == 0)
+        return err;
+    const Shape s = shape_of(tokens, width);
+    return launch_pdl(moe_gather_kernel, s.grid, dim3(kThreads), 0, stream, static_cast<const __nv_bfloat16*>(x), row_of, tokens,
+                      top_k, width, xt, static_cast<__nv_bfloat16*>(sorted), s.across_log);
+}
+
+cudaError_t launch_moe_combine(const void* y, const int32_t* row_of, const float* weights, int64_t tokens, int top_k,
+                               int64_t rows, int64_t width, void* out, int64_t ot, cudaStream_t stream)
+{
+    const Shape s = shape_of(tokens, width);
+    return launch_pdl(moe_combine_kernel, s.grid, dim3(kThreads), 0, stream, static_cast<const __nv_bfloat16*>(y), row_of,
+                      weights, tokens, top_k, rows, width, static_cast<__nv_bfloat16*>(out), ot, s.across_log);
+}
+
+cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const int32_t* row_of, const float* weights,
+                                        int64_t tokens, int top_k, int64_t rows, int64_t width, int64_t gt, void* grad_y,
+                                        float* grad_weights, cudaStream_t stream)
+{
+    const int64_t pairs = tokens * top_k;
+    return launch_pdl(moe_combine_backward_kernel, dim3(static_cast<unsigned>((pairs + 7) / 8)), dim3(256), 0, stream,
+                      static_cast<const __nv_bfloat16*>(grad), static_cast<const __nv_bfloat16*>(y), row_of, weights, pairs,
+                      top_k, rows, width, gt, static_cast<__nv_bfloat16*>(grad_y), grad_weights);
+}
+
+}  // namespace fp4lin

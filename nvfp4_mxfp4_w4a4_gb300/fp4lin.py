@@ -44,6 +44,9 @@ SYMBOLS = (
     "fp4_linear_fp8_b128_workspace_size", "fp4_linear_fp8_b128", "fp4_rope_table", "fp4_rope",
     "fp4_kv_code_bytes", "fp4_kv_scale_bytes", "fp4_kv_append", "fp4_kv_read",
     "fp4_kv_attention_workspace_size", "fp4_kv_attention",
+    "fp4_qk_norm_rope", "fp4_prompt_attention_workspace_size", "fp4_prompt_attention",
+    "fp4_gemv_mxfp4", "fp4_gemv_nvfp4", "fp4_gemv_mxfp4_experts",
+    "fp4_moe_dispatch", "fp4_moe_combine", "fp4_moe_combine_backward",
 )
 
 
@@ -104,8 +107,33 @@ class fp4_kv_attention_args(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float)]
 
 
+class fp4_qk_norm_args(ctypes.Structure):
+    _fields_ = [("q_bf16", ctypes.c_void_p), ("k_bf16", ctypes.c_void_p), ("q_out_bf16", ctypes.c_void_p),
+                ("k_out_bf16", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+                ("k_out_token_stride", ctypes.c_int64), ("k_out_head_stride", ctypes.c_int64),
+                ("q_weight_bf16", ctypes.c_void_p), ("k_weight_bf16", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class fp4_prompt_attention_args(ctypes.Structure):
+    _fields_ = [("q_bf16", ctypes.c_void_p), ("k_bf16", ctypes.c_void_p), ("v_bf16", ctypes.c_void_p),
+                ("out_bf16", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("q_offsets", ctypes.c_void_p), ("k_offsets", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("key_tokens", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
+
+
 # the same layout in one step: the structure's constructor costs as much as the checks of a call
 _attention_args = struct.Struct("@PPPqqqqPqPPPiiqiiqf4x").pack
+_norm_args = struct.Struct("@PPPPqqqqqqqqPPPqiiif").pack
+_prompt_args = struct.Struct("@PPPPPqqqqqqqqPPqqiiiiif").pack
 
 
 _lib = None
@@ -178,6 +206,15 @@ def load(path: str = LIB_PATH):
             "fp4_kv_attention_workspace_size": (ctypes.c_size_t, [_i32, _i64, _i32, _i32, _i32, _i64, _i32]),
             "fp4_kv_attention": (ctypes.c_int, [ctypes.POINTER(fp4_kv_cache), _p, _p,
                                                 ctypes.c_size_t, _p]),
+            "fp4_qk_norm_rope": (ctypes.c_int, [_p, ctypes.POINTER(fp4_rope_params), _p]),
+            "fp4_prompt_attention_workspace_size": (ctypes.c_size_t, [_i32, _i64, _i64, _i32, _i32, _i32]),
+            "fp4_prompt_attention": (ctypes.c_int, [_p, _p, ctypes.c_size_t, _p]),
+            "fp4_gemv_mxfp4": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
+            "fp4_gemv_nvfp4": (ctypes.c_int, [_p, _p, _p, ctypes.c_float, _p, _p, _i64, _i64, _i64, _p]),
+            "fp4_gemv_mxfp4_experts": (ctypes.c_int, [_p, _p, _i32, _i64, _i32, _p, _p, _p, _p, _i64, _i64, _p]),
+            "fp4_moe_dispatch": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i64, _i64, _p, _p, _p, _p]),
+            "fp4_moe_combine": (ctypes.c_int, [_p, _p, _p, _i64, _i32, _i64, _i64, _p, _i64, _p]),
+            "fp4_moe_combine_backward": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i32, _i64, _i64, _i64, _p, _p, _p]),
             "fp4_linear_grouped_workspace_size": (ctypes.c_size_t, [_i64, _i32, _i64]),
             "fp4_linear_grouped": (ctypes.c_int, [_p, _p, _i32, _i64, _p, _p, _p, _p, _i64, _i64, _p, ctypes.c_size_t,
                                                   ctypes.POINTER(fp4_quant_opts), _p]),
@@ -644,3 +681,177 @@ def fp4_kv_attention(cache, q, out, block_table, context_lens, q_offsets, max_se
                         max_seq_len, dim ** -0.5 if softmax_scale is None else softmax_scale)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().fp4_kv_attention(cache.ref, a, _ptr(workspace), nbytes, _stream(stream)), "fp4_kv_attention")
+
+
+def _vector(t, count, what):
+    _expect(t, _torch.bfloat16, count, what)
+    return t.data_ptr()
+
+
+def fp4_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, eps=1e-6, positions=None, rope=None, stream=None):
+    """q, q_out: bf16 [tokens, q_heads, head_dim]; k, k_out: bf16 [tokens,
+    kv_heads, head_dim] or None; q_weight, k_weight: bf16 [head_dim]; with `rope`
+    the heads are rotated after their norm (positions: int32 [tokens])."""
+    _need_torch()
+    (tokens, heads, dim), qt, qh, qot, qoh = _pair(q, q_out, "q, q_out")
+    kv = kt = kh = kot = koh = kp = ko = kw = 0
+    if k is not None:
+        (kv_tokens, kv, kv_dim), kt, kh, kot, koh = _pair(k, k_out, "k, k_out")
+        if kv_tokens != tokens or kv_dim != dim:
+            raise ValueError("q and k have the same tokens and head_dim")
+        kp, ko, kw = k.data_ptr(), k_out.data_ptr(), _vector(k_weight, dim, "k_weight")
+    if rope is not None:
+        _expect(positions, _torch.int32, tokens, "positions")
+    a = _norm_args(q.data_ptr(), kp, q_out.data_ptr(), ko, qt, qh, kt, kh, qot, qoh, kot, koh,
+                   _vector(q_weight, dim, "q_weight"), kw, 0 if rope is None else positions.data_ptr(), tokens, heads, kv,
+                   dim, eps)
+    _check(load().fp4_qk_norm_rope(a, None if rope is None else rope.ref, _stream(stream)), "fp4_qk_norm_rope")
+
+
+def fp4_prompt_attention_workspace_size(batch, tokens, key_tokens, q_heads, kv_heads, head_dim):
+    return load().fp4_prompt_attention_workspace_size(batch, tokens, key_tokens, q_heads, kv_heads, head_dim)
+
+
+def fp4_prompt_attention(q, k, v, out, q_offsets, k_offsets=None, workspace=None, causal=True, lse=None,
+                         softmax_scale=None, stream=None):
+    """q, out: bf16 [tokens, q_heads, head_dim]; k, v: bf16 [key_tokens, kv_heads,
+    head_dim]; q_offsets, k_offsets: int32 [batch + 1] (k_offsets None: the same);
+    lse: float32 [tokens, q_heads] or None; softmax_scale defaults to
+    head_dim ** -0.5."""
+    _need_torch()
+    (tokens, heads, dim), qt, qh, ot, oh = _pair(q, out, "q, out")
+    if k.numel() == 0 and k.shape == v.shape:  # (no keys: such tensors may have any strides)
+        (keys, kv, kv_dim), kt, kh, vt, vh = k.shape, 0, 0, 0, 0
+    else:
+        (keys, kv, kv_dim), kt, kh, vt, vh = _pair(k, v, "k, v")
+    if kv_dim != dim:
+        raise ValueError("q and k have the same head_dim")
+    batch = q_offsets.numel() - 1
+    _expect(q_offsets, _torch.int32, 2, "q_offsets")
+    if k_offsets is None:
+        k_offsets = q_offsets
+    else:
+        _expect(k_offsets, _torch.int32, batch + 1, "k_offsets")
+    log_sum = 0
+    if lse is not None:
+        _expect(lse, _torch.float32, tokens * heads, "lse")
+        log_sum = lse.data_ptr()
+    if workspace is not None and not (workspace.is_contiguous() and workspace.is_cuda):
+        raise ValueError("workspace: a contiguous device tensor")
+    a = _prompt_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), log_sum, qt, qh, kt, kh, vt, vh, ot, oh,
+                     q_offsets.data_ptr(), k_offsets.data_ptr(), tokens, keys, batch, heads, kv, dim, int(bool(causal)),
+                     dim ** -0.5 if softmax_scale is None else softmax_scale)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().fp4_prompt_attention(a, _ptr(workspace), nbytes, _stream(stream)), "fp4_prompt_attention")
+
+
+# ------------------------------------- around the FP4 weights: few rows, experts
+
+
+def _packed(w, sw, count, N, K, group):
+    """The addresses of `count` packed weights [N, K / 2] and their swizzled scales."""
+    need = count * -(-N // 128) * -(-K // (4 * group)) * 512
+    for t, n, what in ((w, count * N * K // 2, "w"), (sw, need, "sw")):
+        if t.element_size() != 1 or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError("%s: a contiguous device tensor of bytes with at least %d elements" % (what, n))
+    return w.data_ptr(), sw.data_ptr()
+
+
+def _gemv(x, w, sw, bias, out, M, N, K, group):
+    _need_torch()
+    at = _packed(w, sw, 1, N, K, group)
+    return (_vector(x, M * K, "x"), *at), (None if bias is None else _vector(bias, N, "bias"), _vector(out, M * N, "out"))
+
+
+def fp4_gemv_mxfp4(x_bf16, w, sw, bias_bf16, out_bf16, M, N, K, stream=None):
+    """bf16 rows [M, K] x MXFP4 weights, M up to 8, activations not quantized."""
+    a, b = _gemv(x_bf16, w, sw, bias_bf16, out_bf16, M, N, K, 32)
+    _check(load().fp4_gemv_mxfp4(*a, *b, M, N, K, _stream(stream)), "fp4_gemv_mxfp4")
+
+
+def fp4_gemv_nvfp4(x_bf16, w, sw, w_global, bias_bf16, out_bf16, M, N, K, stream=None):
+    """bf16 rows [M, K] x NVFP4 weights (swizzled E4M3 scales, times w_global)."""
+    a, b = _gemv(x_bf16, w, sw, bias_bf16, out_bf16, M, N, K, 16)
+    _check(load().fp4_gemv_nvfp4(*a, w_global, *b, M, N, K, _stream(stream)), "fp4_gemv_nvfp4")
+
+
+def fp4_gemv_mxfp4_experts(x_bf16, expert_ids, E, rows, rows_per_x, w, sw, bias_bf16, out_bf16, N, K, stream=None):
+    """out[r] = W[expert_ids[r]] x[r // rows_per_x] (+ bias of the expert); expert_ids: int32 [rows]."""
+    _need_torch()
+    wp, sp = _packed(w, sw, E, N, K, 32)
+    _expect(expert_ids, _torch.int32, rows, "expert_ids")
+    x = _vector(x_bf16, -(-rows // max(rows_per_x, 1)) * K, "x")
+    bias = None if bias_bf16 is None else _vector(bias_bf16, E * N, "bias")
+    _check(load().fp4_gemv_mxfp4_experts(x, expert_ids.data_ptr(), E, rows, rows_per_x, wp, sp, bias,
+                                         _vector(out_bf16, rows * N, "out"), N, K, _stream(stream)),
+           "fp4_gemv_mxfp4_experts")
+
+
+def _matrix(t, what, contiguous=False):
+    """Rows, width and row stride of a bf16 device matrix with contiguous rows."""
+    rows, width = t.shape
+    a, b = t.stride()
+    if t.dtype is not _torch.bfloat16 or (b != 1 and width != 1) or not t.is_cuda or (contiguous and not t.is_contiguous()):
+        raise ValueError("%s: a bf16 device tensor with %s" % (what, "no gaps" if contiguous else "contiguous rows"))
+    return rows, width, a if rows > 1 else width
+
+
+def _choices(row_of, weights, top_k, tokens):
+    if row_of is not None:
+        top_k = row_of.shape[-1]
+        _expect(row_of, _torch.int32, tokens * top_k, "row_of")
+    if weights is not None:
+        top_k = weights.shape[-1] if top_k is None else top_k
+        _expect(weights, _torch.float32, tokens * top_k, "weights")
+    if top_k is None:
+        raise ValueError("top_k: needed without row_of and weights")
+    return top_k
+
+
+def fp4_moe_dispatch(x, expert_ids, E, sorted_x, row_offsets, row_of, stream=None):
+    """x: bf16 [tokens, width]; expert_ids, row_of: int32 [tokens, top_k];
+    sorted_x: bf16 [tokens * top_k, width]; row_offsets: int32 [E + 1]."""
+    _need_torch()
+    tokens, width, xt = _matrix(x, "x")
+    if expert_ids.dim() != 2 or expert_ids.shape[0] != tokens:
+        raise ValueError("expert_ids are [tokens, top_k]")
+    top_k = expert_ids.shape[1]
+    _expect(expert_ids, _torch.int32, tokens * top_k, "expert_ids")
+    _expect(row_of, _torch.int32, tokens * top_k, "row_of")
+    _expect(row_offsets, _torch.int32, E + 1, "row_offsets")
+    rows, sorted_width, _ = _matrix(sorted_x, "sorted_x", True)
+    if rows < tokens * top_k or sorted_width != width:
+        raise ValueError("sorted_x is [tokens * top_k, width]")
+    _check(load().fp4_moe_dispatch(x.data_ptr(), expert_ids.data_ptr(), tokens, top_k, E, width, xt, sorted_x.data_ptr(),
+                                   row_offsets.data_ptr(), row_of.data_ptr(), _stream(stream)), "fp4_moe_dispatch")
+
+
+def fp4_moe_combine(y, row_of, weights, out, top_k=None, stream=None):
+    """y: bf16 [rows, width]; row_of: int32 [tokens, top_k] or None (row t * top_k
+    + j); weights: float32 [tokens, top_k] or None (1); out: bf16 [tokens, width]."""
+    _need_torch()
+    rows, width, _ = _matrix(y, "y", True)
+    tokens, out_width, ot = _matrix(out, "out")
+    if out_width != width:
+        raise ValueError("y and out have the same width")
+    top_k = _choices(row_of, weights, top_k, tokens)
+    _check(load().fp4_moe_combine(y.data_ptr(), _ptr(row_of), _ptr(weights), tokens, top_k, rows, width, out.data_ptr(), ot,
+                                  _stream(stream)), "fp4_moe_combine")
+
+
+def fp4_moe_combine_backward(grad_out, y, row_of, weights, grad_y, grad_weights=None, top_k=None, stream=None):
+    """grad_out: bf16 [tokens, width]; y, grad_y: bf16 [rows, width] (y None where
+    grad_weights is); grad_weights: float32 [tokens, top_k]."""
+    _need_torch()
+    tokens, width, gt = _matrix(grad_out, "grad_out")
+    rows, grad_width, _ = _matrix(grad_y, "grad_y", True)
+    if grad_width != width:
+        raise ValueError("grad_out and grad_y have the same width")
+    top_k = _choices(row_of, weights, top_k, tokens)
+    if grad_weights is not None:
+        _expect(grad_weights, _torch.float32, tokens * top_k, "grad_weights")
+        if _matrix(y, "y", True)[:2] != (rows, width):
+            raise ValueError("y and grad_y have the same shape")
+    _check(load().fp4_moe_combine_backward(grad_out.data_ptr(), _ptr(y), _ptr(row_of), _ptr(weights), tokens, top_k, rows,
+                                           width, gt, grad_y.data_ptr(), _ptr(grad_weights), _stream(stream)),
+           "fp4_moe_combine_backward")
