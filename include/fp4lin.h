@@ -823,7 +823,7 @@ FP4LIN_API fp4_status fp4_qk_norm_rope(const fp4_qk_norm_args* args, const fp4_r
  * Queries behind the last sequence are not written.  Offsets are clamped to
  * [0, tokens] (and each end to its start), so that wrong ones give wrong
  * numbers but no access outside the tensors.
- * head_dim 64 or 128; strides in elements, multiples of 8, those of k and v
+ * head_dim 64 or 128; strides in elements, multiples of 8, those of q, k and v
  * positive; pointers 16-byte aligned.  out must not overlap an input.       */
 typedef struct {
     const void* q_bf16;          /* [tokens][q_heads][head_dim] */

@@ -119,6 +119,13 @@ fp4_status check_prompt_shape(int32_t batch, int64_t tokens, int64_t keys, int32
     return FP4_OK;
 }
 
+// Strides of a tensor map's dimensions (one of a single element has none).
+bool map_strides_ok(int64_t tokens, int64_t heads, int64_t token, int64_t head)
+{
+    constexpr int64_t kMaxStride = int64_t(1) << 38;
+    return (tokens <= 1 || (token > 0 && token <= kMaxStride)) && (heads <= 1 || (head > 0 && head <= kMaxStride));
+}
+
 // ------------------------------------------------------ products, experts
 
 fp4_status check_gemv(const void* x, const void* w, const void* sw, const void* bias, const void* out, int64_t N, int64_t K)
@@ -515,15 +522,14 @@ fp4_status fp4_prompt_attention(const fp4_prompt_attention_args* args, void* wor
     if ((st = check_strides(g.q_bf16, g.q_token_stride, g.q_head_stride)) != FP4_OK ||
         (st = check_strides(g.out_bf16, g.out_token_stride, g.out_head_stride)) != FP4_OK)
         return st;
+    if (!map_strides_ok(g.tokens, g.q_heads, g.q_token_stride, g.q_head_stride))
+        return FP4_ERR_SHAPE;
     if (g.key_tokens > 0) {
         if ((st = check_strides(g.k_bf16, g.k_token_stride, g.k_head_stride)) != FP4_OK ||
             (st = check_strides(g.v_bf16, g.v_token_stride, g.v_head_stride)) != FP4_OK)
             return st;
-        // (strides of tensor maps; a dimension of one element has none)
-        constexpr int64_t kMaxStride = int64_t(1) << 38;
-        if ((g.key_tokens > 1 && (g.k_token_stride <= 0 || g.v_token_stride <= 0)) ||
-            (g.kv_heads > 1 && (g.k_head_stride <= 0 || g.v_head_stride <= 0)) || g.k_token_stride > kMaxStride ||
-            g.v_token_stride > kMaxStride || g.k_head_stride > kMaxStride || g.v_head_stride > kMaxStride)
+        if (!map_strides_ok(g.key_tokens, g.kv_heads, g.k_token_stride, g.k_head_stride) ||
+            !map_strides_ok(g.key_tokens, g.kv_heads, g.v_token_stride, g.v_head_stride))
             return FP4_ERR_SHAPE;
     }
     const size_t need = fp4lin::prompt_attention_workspace_bytes(g.batch, g.tokens, g.key_tokens, g.q_heads, g.kv_heads, g.head_dim);

@@ -1064,18 +1064,22 @@ bool make_output_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, i
 }
 
 // bf16 [tokens][heads][dim] with strides in elements, boxes of 64 elements of
-// `box_tokens` tokens of one head, 128-byte swizzle.
+// `box_heads` heads of `box_tokens` tokens, 128-byte swizzle.  Coordinates:
+// element, token, head, or with `heads_inside` element, head, token.
 bool make_heads_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride,
-                    int64_t head_stride, int box_tokens)
+                    int64_t head_stride, int box_tokens, int box_heads, bool heads_inside)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn)
         return false;
     // (a dimension of one element may have any stride: it gets one that the map takes)
-    const int64_t ts = tokens > 1 ? token_stride : dim, hs = heads > 1 ? head_stride : dim;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(tokens), static_cast<cuuint64_t>(heads)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ts * 2), static_cast<cuuint64_t>(hs * 2)};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_tokens), 1};
+    const cuuint64_t ts = static_cast<cuuint64_t>(tokens > 1 ? token_stride : dim) * 2;
+    const cuuint64_t hs = static_cast<cuuint64_t>(heads > 1 ? head_stride : dim) * 2;
+    const cuuint64_t nt = static_cast<cuuint64_t>(tokens), nh = static_cast<cuuint64_t>(heads);
+    const cuuint32_t bt = static_cast<cuuint32_t>(box_tokens), bh = static_cast<cuuint32_t>(box_heads);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), heads_inside ? nh : nt, heads_inside ? nt : nh};
+    const cuuint64_t strides[2] = {heads_inside ? hs : ts, heads_inside ? ts : hs};
+    const cuuint32_t box[3] = {64, heads_inside ? bh : bt, heads_inside ? bt : bh};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -170,7 +170,7 @@ bool make_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t 
 bool make_output_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int box_cols, int box_rows,
                      CUtensorMapSwizzle swizzle);
 bool make_heads_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t heads, int64_t dim, int64_t token_stride,
-                    int64_t head_stride, int box_tokens);
+                    int64_t head_stride, int box_tokens, int box_heads, bool heads_inside);
 int sm_count();
 
 // Host-side argument checks of the GEMM entry points; returns an fp4_status

@@ -4,12 +4,12 @@
 //
 //   S [rows x keys] = Q K^T,  P = exp2(S scale log2(e) - m),  O += P V
 //
-// A unit is 256 rows of a key/value head: the queries' heads that read it side by
-// side, (token, head) pairs in the tokens' order, as two halves of 128 rows.  The
-// halves' tiles of 128 keys take turns: while the MMAs of one half run, the other
-// half's scores are weighed.  A softmax thread is one row: the tile's 128 scores
-// are in its registers at once, maximum and sum stay there, and the
-// probabilities (bf16) go back to tensor memory over the scores.  The row's
+// A unit is two halves of up to 128 rows of a key/value head: a few tokens with
+// the query heads that read it, side by side.  The halves' tiles of 128 keys take
+// turns: while the MMAs of one half run, the other half's scores are weighed.  A
+// softmax thread is one row: the tile's 128 scores are in its registers at once,
+// maximum (a by-product of their load from tensor memory) and sum stay there, and
+// the probabilities (bf16) go back to tensor memory over the scores.  The row's
 // reference m moves only when a score passes it by 2^8, so most tiles leave O as
 // it is.
 //
@@ -25,8 +25,8 @@
 // second kernel joins.  Where all units are short, they are dealt out whole.
 //
 // Warps: 0-3 and 4-7 the softmax of the halves (they also write the results), 8
-// loads keys and values (TMA), 9 issues the MMAs, 10 and 11 load the queries and
-// look through the values.
+// goes over the run's units and loads queries, keys and values (TMA), 9 and 10
+// issue the MMAs of the halves, 11 looks through values.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -42,7 +42,7 @@
 namespace fp4lin {
 namespace {
 
-constexpr int kHalf = 128;           // rows of a half
+constexpr int kHalf = 128;           // rows of a half, at most
 constexpr int kRows = 2 * kHalf;     // of a unit
 constexpr int kTile = 128;           // keys of a tile
 constexpr int kSlab = 128 * 128;     // bytes of 64 bf16 elements of 128 rows or keys
@@ -50,6 +50,7 @@ constexpr int kThreads = 384;
 constexpr int kUnitPlaces = 3;       // of a unit's start and end on the line
 constexpr int kLeastRun = kUnitPlaces + 4;
 constexpr int kWholeTiles = 8;       // units of at most so many tiles are never cut
+constexpr int kParts = 4;            // of the run whose descriptions are in shared memory
 constexpr int kWarpSequences = 96;   // up to so many sequences, a warp adds one up
 constexpr float kSlack = 8.0f;       // a score this far above its reference moves it
 // a row's reference before its first seen key: the lowest float32, which no score lies under
@@ -69,8 +70,10 @@ struct Cut {
 
 struct PromptParams {
     PromptArgs a;
-    DivMagic group_div;
-    int group;
+    int heads;      // query heads of a half's token: all of a key head's, or 128 of them
+    int chunks;     // such groups of a key head
+    int tokens;     // of a half
+    DivMagic heads_div;
     float xscale;   // scale * log2(e)
     float* part_o;  // [CTA][2][kRows][dim]
     float2* part_ml;
@@ -125,28 +128,24 @@ __device__ __forceinline__ void set_registers()
 // A place on the line: one unit after the other, by sequence, key head and block
 // of rows.
 struct Walk {
-    int b, head, block, blocks;  // blocks of the sequence
+    int b, head, block, blocks;  // head: key head and chunk; blocks of the sequence
     int q0, n, k0, m;
 
     __device__ __forceinline__ void sequence(const PromptParams& p)
     {
         group_rows(p.a.q_offsets, b, static_cast<int>(p.a.T), &q0, &n);
         group_rows(p.a.k_offsets, b, static_cast<int>(p.a.keys), &k0, &m);
-        blocks = static_cast<int>((static_cast<uint32_t>(n) * p.group + kRows - 1) / kRows);
+        blocks = (n + 2 * p.tokens - 1) / (2 * p.tokens);
     }
-    // Keys that row r (of the sequence's rows) sees.
-    __device__ __forceinline__ int limit(const PromptParams& p, int r) const
+    // Keys that query i of the sequence sees.
+    __device__ __forceinline__ int limit(const PromptParams& p, int i) const
     {
-        if (!p.a.causal)
-            return m;
-        const int i = min(static_cast<int>(div_by_magic(r, p.group_div)), n - 1);
-        return max(min(i + 1 + m - n, m), 0);
+        return p.a.causal ? max(min(i + 1 + m - n, m), 0) : m;
     }
-    __device__ __forceinline__ int first_row(int half) const { return block * kRows + half * kHalf; }
     __device__ __forceinline__ int tiles(const PromptParams& p, int half) const
     {
-        const int r0 = first_row(half), rows = n * p.group;
-        return r0 >= rows ? 0 : (limit(p, min(r0 + kHalf, rows) - 1) + kTile - 1) / kTile;
+        const int i = (2 * block + half) * p.tokens;
+        return i >= n ? 0 : (limit(p, min(i + p.tokens, n) - 1) + kTile - 1) / kTile;
     }
     __device__ __forceinline__ int tiles(const PromptParams& p) const { return max(tiles(p, 0), tiles(p, 1)); }
     __device__ __forceinline__ void next(const PromptParams& p)
@@ -154,7 +153,7 @@ struct Walk {
         if (++block < blocks)
             return;
         block = 0;
-        if (++head < p.a.kv_heads)
+        if (++head < p.a.kv_heads * p.chunks)
             return;
         head = 0;
         blocks = 0;
@@ -275,7 +274,7 @@ __device__ bool find_run(const PromptParams& p, uint8_t* scratch, Run* shared)
         *before = base + x - v;
         return total;
     };
-    const int heads = p.a.kv_heads;
+    const int heads = p.a.kv_heads * p.chunks;
     int64_t total = 0, before = 0, mine = 0;
     for (int i = 0; i < batch; i += kThreads) {
         mine = weight(i + threadIdx.x);
@@ -348,19 +347,34 @@ __device__ bool find_run(const PromptParams& p, uint8_t* scratch, Run* shared)
 
 // ------------------------------------------------------------------ kernel
 
+// A part of the run, as the warps see it.
+struct alignas(16) Part {
+    int lo, hi;      // tiles; lo < 0: the run has ended
+    int end[2];      // the halves' own tiles end here
+    int token;       // first query of the unit
+    int tokens;      // of the sequence from there on
+    int first_seen;  // keys seen by that query, before they are clamped to [0, m]
+    int m;
+    int key_head, q_head, q_heads;  // the chunk's first query head, and how many
+    int slot;        // of the partial results, -1: the part is the whole unit
+    int masked;      // first tile in which some row sees not all keys
+};
+
 template <int kDim>
 struct Cfg {
     static constexpr int SLABS = kDim / 64;
     static constexpr int TILE = SLABS * kSlab;  // bytes of a tile of K or V, or of a half's Q
     static constexpr int STAGES = kDim == 128 ? 2 : 4;
-    static constexpr int OFF_K = 2 * TILE;  // Q first
+    static constexpr int QBUFS = kDim == 128 ? 1 : 2;  // of a half's Q
+    static constexpr int OFF_K = 2 * QBUFS * TILE;  // Q first
     static constexpr int OFF_V = OFF_K + STAGES * TILE;
     static constexpr int OFF_BAD = OFF_V + STAGES * TILE;  // int [2][3][kDim]: first keys whose value is inf, -inf, NaN
     static constexpr int OFF_BAR = OFF_BAD + 2 * 3 * kDim * 4;
-    static constexpr int BARS = 4 * STAGES + 4 + 2 * 7 + 1;
+    static constexpr int BARS = 4 * STAGES + 4 + 4 * QBUFS + 2 * 6 + 2 * kParts + 2;
     static constexpr int OFF_SLOT = OFF_BAR + BARS * 8;  // TMEM address, flags
     static constexpr int OFF_RUN = (OFF_SLOT + 32 + 15) / 16 * 16;
-    static constexpr int SMEM = OFF_RUN + 128 + 1024;  // + alignment slack
+    static constexpr int OFF_PARTS = OFF_RUN + 128;
+    static constexpr int SMEM = OFF_PARTS + kParts * static_cast<int>(sizeof(Part)) + 1024;  // + alignment slack
     static constexpr int TMEM_COLS = 512;  // S of the halves, then O
     static constexpr int TMEM_O = 2 * kTile;
     static_assert(sizeof(Run) <= 128, "");
@@ -369,52 +383,65 @@ struct Cfg {
 
 template <int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map)
+    prompt_attention_kernel(const PromptParams p, const __grid_constant__ CUtensorMap q_map,
+                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map)
 {
     using C = Cfg<kDim>;
-    constexpr int STAGES = C::STAGES;
+    constexpr int STAGES = C::STAGES, QBUFS = C::QBUFS;
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* k_full = bars;              // [STAGES] a tile has landed
-    uint64_t* k_free = k_full + STAGES;   // [STAGES] and is multiplied
-    uint64_t* v_full = k_free + STAGES;   // [STAGES]
-    uint64_t* v_free = v_full + STAGES;   // [STAGES]
-    uint64_t* v_seen = v_free + STAGES;   // [4] a masked tile's values are looked through
-    uint64_t* q_full = v_seen + 4;        // [2] by half
-    uint64_t* q_free = q_full + 2;        // [2]
-    uint64_t* s_full = q_free + 2;        // [2] scores are complete (and the tile before is in O)
-    uint64_t* p_full = s_full + 2;        // [2] probabilities are in tensor memory
-    uint64_t* o_full = p_full + 2;        // [2] the part's last tile is in O
-    uint64_t* bad_full = o_full + 2;      // [2] by part: its masked tiles are looked through
-    uint64_t* bad_free = bad_full + 2;    // [2] and what was found is read
-    uint64_t* drained = bad_free + 2;     // every MMA has ended
+    uint64_t* k_full = bars;               // [STAGES] a tile has landed
+    uint64_t* k_free = k_full + STAGES;    // [STAGES] both halves' products with it have ended
+    uint64_t* v_full = k_free + STAGES;    // [STAGES]
+    uint64_t* v_free = v_full + STAGES;    // [STAGES]
+    uint64_t* v_seen = v_free + STAGES;    // [4] a masked tile's values are looked through
+    uint64_t* q_full = v_seen + 4;         // [QBUFS][2] by half
+    uint64_t* q_free = q_full + 2 * QBUFS; // [QBUFS][2]
+    uint64_t* s_full = q_free + 2 * QBUFS; // [2] scores are complete (and the tile before is in O)
+    uint64_t* p_half = s_full + 2;         // [2] probabilities of half the keys are in tensor memory
+    uint64_t* p_full = p_half + 2;         // [2] and of the others
+    uint64_t* o_full = p_full + 2;         // [2] the part's last tile is in O
+    uint64_t* bad_full = o_full + 2;       // [2] by part: its masked tiles are looked through
+    uint64_t* bad_free = bad_full + 2;     // [2] and what was found is read
+    uint64_t* part_full = bad_free + 2;    // [kParts] a part is described
+    uint64_t* part_free = part_full + kParts;  // [kParts] and done with
+    uint64_t* drained = part_free + kParts;    // [2] every MMA of a half has ended
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
     volatile uint32_t* any_bad = tmem_slot + 1;  // [2] by part
     Run* run = reinterpret_cast<Run*>(smem + C::OFF_RUN);
+    volatile Part* parts = reinterpret_cast<Part*>(smem + C::OFF_PARTS);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_free[i], 1);
+            mbar_init(&k_free[i], 2);
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_free[i], 1);
+            mbar_init(&v_free[i], 2);
         }
         for (int i = 0; i < 4; ++i)
-            mbar_init(&v_seen[i], 2);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 2);
+            mbar_init(&v_seen[i], 1);
+        for (int i = 0; i < 2 * QBUFS; ++i) {
+            mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
-            mbar_init(&bad_full[i], 2);
+            mbar_init(&bad_full[i], 1);
             mbar_init(&bad_free[i], 8);
+            mbar_init(&drained[i], 1);
             any_bad[i] = 0u;
         }
-        mbar_init(drained, 1);
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&part_full[i], 1);
+            mbar_init(&part_free[i], 8 + 2 + 1);
+        }
         fence_mbar_init();
+        tma_prefetch_map(&q_map);
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
     }
@@ -440,247 +467,252 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, wait_one(bar, parity));
         return ok;
     };
-    Cut cut = {};
-    cut.open = 0;
+    // the next part's description, or nullptr at the end of the run
+    uint32_t part_count = 0;
+    auto next_part = [&]() -> volatile Part* {
+        const uint32_t i = part_count % kParts;
+        if (!wait(&part_full[i], part_count / kParts) || parts[i].lo < 0)
+            return nullptr;
+        return &parts[i];
+    };
+    auto part_done = [&]() {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&part_free[part_count % kParts]);
+        ++part_count;
+    };
 
     if (warp >= 8) {
         set_registers<kOtherRegs>();
         if (!have) {
+            if (p.may_cut && warp == 8 && lane == 0)
+                p.cuts[blockIdx.x] = Cut{};
         } else if (warp == 8) {
-            // ------------------------------------------------ keys and values
+            // ------------------------------- the run; queries, keys and values
             if (lane == 0) {
                 Run r = *run;
-                bool started = false;
-                uint32_t g = 0;  // tiles so far
-                auto landed = [&](uint64_t* full, uint32_t slot, uint32_t phase) {
-                    mbar_wait_bounded(&full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
-                };
-                while (ok && r.part(p, started)) {
+                bool started = false, more = true;
+                Cut cut = {};
+                uint32_t g = 0, queries[2] = {0, 0};  // tiles, and a half's Q, so far
+                while (ok) {
+                    // the part's description
+                    const uint32_t i = part_count % kParts;
+                    more = r.part(p, started);
+                    if (!wait_one(&part_free[i], (part_count / kParts) ^ 1u))
+                        break;
+                    volatile Part& d = parts[i];
+                    if (!more) {
+                        d.lo = -1;
+                        mbar_arrive(&part_full[i]);
+                        break;
+                    }
+                    const Walk& w = r.w;
+                    const int key_head = w.head / p.chunks, chunk = w.head - key_head * p.chunks;
+                    const int first = 2 * w.block * p.tokens;
+                    const int group = p.a.q_heads / p.a.kv_heads;
+                    const int q_head = key_head * group + chunk * kHalf;
+                    const int end[2] = {max(r.lo, min(r.hi, w.tiles(p, 0))), max(r.lo, min(r.hi, w.tiles(p, 1)))};
+                    d.lo = r.lo, d.hi = r.hi;
+                    d.end[0] = end[0], d.end[1] = end[1];
+                    d.token = w.q0 + first;
+                    d.tokens = w.n - first;
+                    d.first_seen = p.a.causal ? first + 1 + w.m - w.n : w.m;
+                    d.m = w.m;
+                    d.key_head = key_head, d.q_head = q_head;
+                    d.q_heads = min(p.heads, group - chunk * kHalf);
+                    d.slot = r.lo == 0 && r.hi == r.tiles ? -1 : r.lo > 0 ? 0 : 1;
+                    d.masked = w.limit(p, first) / kTile;
+                    mbar_arrive(&part_full[i]);
+                    ++part_count;
+                    if (r.hi < r.tiles) {
+                        if (r.lo > 0)
+                            cut.through = 1;
+                        else
+                            cut.open = 1, cut.b = w.b, cut.head = w.head, cut.block = w.block;
+                    }
+                    // its tiles; the queries behind the first keys, whose place is free earlier
                     for (int j = r.lo; ok && j < r.hi; ++j, ++g) {
                         const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1u;
-                        const int at = r.w.k0 + j * kTile;
+                        const int at = w.k0 + j * kTile;
                         if (!wait_one(&k_free[slot], phase ^ 1u))
                             break;
                         mbar_arrive_expect_tx(&k_full[slot], C::TILE);
 #pragma unroll
                         for (int s = 0; s < C::SLABS; ++s)
-                            tma_load_3d(smem + C::OFF_K + slot * C::TILE + s * kSlab, &k_map, &k_full[slot], s * 64, at, r.w.head);
+                            tma_load_3d(smem + C::OFF_K + slot * C::TILE + s * kSlab, &k_map, &k_full[slot], s * 64, at, key_head);
+                        if (j == r.lo) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (end[h] == r.lo)
+                                    continue;
+                                const uint32_t buf = (queries[h] % QBUFS) * 2 + h;
+                                if (!wait_one(&q_free[buf], (queries[h] / QBUFS) ^ 1u))
+                                    break;
+                                ++queries[h];
+                                mbar_arrive_expect_tx(&q_full[buf], p.tokens * p.heads * kDim * 2);
+#pragma unroll
+                                for (int s = 0; s < C::SLABS; ++s)
+                                    tma_load_3d(smem + buf * C::TILE + s * kSlab, &q_map, &q_full[buf], s * 64, q_head,
+                                                w.q0 + first + h * p.tokens);
+                            }
+                        }
                         if (!wait_one(&v_free[slot], phase ^ 1u)) {
-                            landed(k_full, slot, phase);
+                            mbar_wait_bounded(&k_full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
                             break;
                         }
                         mbar_arrive_expect_tx(&v_full[slot], C::TILE);
 #pragma unroll
                         for (int s = 0; s < C::SLABS; ++s)
-                            tma_load_3d(smem + C::OFF_V + slot * C::TILE + s * kSlab, &v_map, &v_full[slot], s * 64, at, r.w.head);
+                            tma_load_3d(smem + C::OFF_V + slot * C::TILE + s * kSlab, &v_map, &v_full[slot], s * 64, at, key_head);
                     }
                 }
+                if (p.may_cut)
+                    p.cuts[blockIdx.x] = cut;
                 // nothing of this CTA may be in flight when it ends
-                for (uint32_t i = 0; i < STAGES && i < g; ++i) {
-                    const uint32_t last = g - 1 - i;
-                    landed(k_full, last % STAGES, (last / STAGES) & 1u);
-                    landed(v_full, last % STAGES, (last / STAGES) & 1u);
+                for (uint32_t i = 1; i <= STAGES && i <= g; ++i) {
+                    const uint32_t slot = (g - i) % STAGES, phase = ((g - i) / STAGES) & 1u;
+                    mbar_wait_bounded(&k_full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
+                    mbar_wait_bounded(&v_full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
                 }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    for (uint32_t i = 1; i <= QBUFS && i <= queries[h]; ++i) {
+                        const uint32_t use = queries[h] - i;
+                        mbar_wait_bounded(&q_full[(use % QBUFS) * 2 + h], (use / QBUFS) & 1u, p.a.status, kStatusTimeout, limit_ns);
+                    }
             }
-        } else if (warp == 9) {
-            // ------------------------------------------------------------ MMAs
+        } else if (warp < 11) {
+            // ---------------------------------------------- MMAs of one half
+            // (the whole warp walks the loop and one elected lane issues: the operands
+            // of the MMAs then stay in uniform registers)
+            const int h = warp - 9;
             constexpr uint32_t idesc_s = idesc_bf16(kHalf, kTile, 0, 0);
             constexpr uint32_t idesc_o = idesc_bf16(kHalf, kDim, 0, 1);
-            const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2);
             const uint64_t kd = smem_desc(smem_u32(smem + C::OFF_K), 16, 1024, 2);
             const uint64_t vd = smem_desc(smem_u32(smem + C::OFF_V), kSlab, 1024, 2);
-            // a step is a tile of the run: the tiles of each half in its part
-            struct Step {
-                bool live, masked;
-                bool has[2], first[2], last[2];
-            };
-            Run r = *run;
-            bool started = false, more = true;
-            int j = 0, end[2] = {0, 0}, free_keys = 0;
-            r.hi = 0;
-            auto next_step = [&]() {
-                Step s = {};
-                if (++j >= r.hi) {
-                    do
-                        more = more && r.part(p, started);
-                    while (more && r.hi == r.lo);
-                    if (!more)
-                        return s;
-                    j = r.lo;
-                    end[0] = min(r.hi, r.w.tiles(p, 0));
-                    end[1] = min(r.hi, r.w.tiles(p, 1));
-                    free_keys = r.w.limit(p, r.w.first_row(0));
-                }
-                s.live = true;
-                s.masked = (j + 1) * kTile > free_keys;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    s.has[h] = j < end[h];
-                    s.first[h] = j == r.lo;
-                    s.last[h] = j == end[h] - 1;
-                }
-                return s;
-            };
-            uint32_t uses[2] = {0, 0};   // of a half's Q
-            uint32_t turns[2] = {0, 0};  // of a half's probabilities
-            uint32_t seen = 0;           // masked tiles
-            auto scores = [&](const Step& s, int h, uint32_t g) {
-                // S of the half; Q's place is free after the part's last tile
-                if (!s.has[h])
-                    return;
-                if (s.first[h] && !wait(&q_full[h], uses[h]++))
-                    return;
-                tc_fence_after_sync();
-                const uint64_t q = qd + ((h * C::TILE) >> 4), k = kd + (((g % STAGES) * C::TILE) >> 4);
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < kDim / 16; ++i) {
-                        const uint64_t at = ((i >> 2) * kSlab + 32 * (i & 3)) >> 4;
-                        tc_mma_f16(tmem + h * kTile, q + at, k + at, idesc_s, i != 0);
+            const uint32_t s_tmem = tmem + h * kTile, o_tmem = tmem + C::TMEM_O + h * kDim;
+            const bool withhold = p.a.withhold && blockIdx.x == 0;
+            uint32_t g = 0, turns = 0, queries = 0, seen = 0;
+            while (volatile Part* d = next_part()) {
+                const int lo = d->lo, hi = d->hi, end = d->end[h], masked = d->masked;
+                const uint32_t buf = (queries % QBUFS) * 2 + h;
+                const uint64_t qd = smem_desc(smem_u32(smem + buf * C::TILE), 16, 1024, 2);
+                // S of the half with tile j, the run's tile `tile`
+                auto scores = [&](int j, uint32_t tile) {
+                    const uint32_t slot = tile % STAGES;
+                    if (!wait(&k_full[slot], tile / STAGES))
+                        return;
+                    if (j >= end) {
+                        if (lane == 0)
+                            mbar_arrive(&k_free[slot]);
+                        return;
                     }
-                    tc_commit(&s_full[h]);
-                    if (s.last[h])
-                        tc_commit(&q_free[h]);
-                }
-                __syncwarp();
-            };
-            auto free_slot = [&](uint64_t* bar) {
-                if (elect_one())
-                    tc_commit(bar);
-                __syncwarp();
-            };
-            Step now = next_step();
-            if (now.live && wait(&k_full[0], 0)) {
-                scores(now, 0, 0);
-                scores(now, 1, 0);
-                if (ok)
-                    free_slot(&k_free[0]);
-            }
-            for (uint32_t g = 0; now.live && ok; ++g) {
-                const Step then = next_step();
-                const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1u;
-                if (!wait(&v_full[slot], phase))
-                    break;
-                if (now.masked) {
-                    if (!wait(&v_seen[seen & 3u], seen >> 2))
-                        break;
-                    ++seen;
-                }
-                if (then.live && !wait(&k_full[(g + 1) % STAGES], (g + 1) / STAGES))
-                    break;
-                const uint64_t v = vd + ((slot * C::TILE) >> 4);
+                    tc_fence_after_sync();
+                    const uint64_t k = kd + ((slot * C::TILE) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (now.has[h]) {
-                        if (!wait(&p_full[h], turns[h]++))
-                            break;
-                        tc_fence_after_sync();
-                        if (elect_one() && !(p.a.withhold && blockIdx.x == 0)) {
-#pragma unroll
-                            for (int i = 0; i < kTile / 16; ++i)
-                                tc_mma_f16_ts(tmem + C::TMEM_O + h * kDim, tmem + h * kTile + 8 * i, v + ((2048 * i) >> 4),
-                                              idesc_o, i != 0 || !now.first[h]);
-                            if (now.last[h])
-                                tc_commit(&o_full[h]);
+                        for (int i = 0; i < kDim / 16; ++i) {
+                            const uint64_t at = ((i >> 2) * kSlab + 32 * (i & 3)) >> 4;
+                            tc_mma_f16(s_tmem, qd + at, k + at, idesc_s, i != 0);
                         }
-                        __syncwarp();
+                        tc_commit(&s_full[h]);
+                        tc_commit(&k_free[slot]);
+                        if (j == end - 1)
+                            tc_commit(&q_free[buf]);
                     }
-                    if (then.live)
-                        scores(then, h, g + 1);
-                    if (!ok)
+                    __syncwarp();
+                };
+                if (end > lo) {
+                    wait(&q_full[buf], queries / QBUFS);
+                    ++queries;
+                }
+                if (ok && hi > lo)
+                    scores(lo, g);
+                for (int j = lo; ok && j < hi; ++j, ++g) {
+                    const uint32_t slot = g % STAGES;
+                    if (!wait(&v_full[slot], g / STAGES))
                         break;
+                    if (j >= masked) {
+                        if (!wait(&v_seen[seen & 3u], seen >> 2))
+                            break;
+                        ++seen;
+                    }
+                    if (j >= end) {
+                        if (lane == 0)
+                            mbar_arrive(&v_free[slot]);
+                    } else {
+                        const uint64_t v = vd + ((slot * C::TILE) >> 4);
+                        // half of the keys after the other, as their probabilities come
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            if (!wait(part == 0 ? &p_half[h] : &p_full[h], turns))
+                                break;
+                            tc_fence_after_sync();
+                            if (elect_one() && !withhold) {
+#pragma unroll
+                                for (int i = part * 4; i < part * 4 + 4; ++i)
+                                    tc_mma_f16_ts(o_tmem, s_tmem + 8 * i, v + ((2048 * i) >> 4), idesc_o, i != 0 || j != lo);
+                                if (part == 1) {
+                                    tc_commit(&v_free[slot]);
+                                    if (j == end - 1)
+                                        tc_commit(&o_full[h]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        ++turns;
+                    }
+                    if (ok && j + 1 < hi)
+                        scores(j + 1, g + 1);
                 }
                 if (!ok)
                     break;
-                free_slot(&v_free[slot]);
-                if (then.live)
-                    free_slot(&k_free[(g + 1) % STAGES]);
-                now = then;
+                part_done();
             }
             // whatever was issued has ended before tensor and shared memory go
             if (elect_one())
-                tc_commit(drained);
+                tc_commit(&drained[h]);
             __syncwarp();
-            mbar_wait_bounded(drained, 0, p.a.status, kStatusTimeout, limit_ns);
+            mbar_wait_bounded(&drained[h], 0, p.a.status, kStatusTimeout, limit_ns);
         } else {
-            // ----------------------------------- queries; looks through values
-            const int t = threadIdx.x - 320;
-            // a wait of both warps, which go on or end together
-            auto wait_both = [&](uint64_t* bar, uint32_t parity) {
-                ok = !named_barrier_or(1, 64, !wait_one(bar, parity));
-                return ok;
-            };
-            Run r = *run;
-            bool started = false;
-            uint32_t uses[2] = {0, 0}, g = 0, seen = 0, parts = 0;
-            while (ok && r.part(p, started)) {
-                const int rows = r.w.n * p.group;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (r.lo >= min(r.hi, r.w.tiles(p, h)))
-                        continue;
-                    if (!wait_both(&q_free[h], (uses[h] & 1u) ^ 1u))
-                        break;
-                    ++uses[h];
-                    constexpr int VECS = kDim / 8, PER = 64 / VECS;  // vectors of a row, rows of a round
-                    const int c = t % VECS;
-                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + c * 8;
-#pragma unroll 4
-                    for (int i = 0; i < kHalf / PER; ++i) {
-                        const int row = i * PER + t / VECS, at = r.w.first_row(h) + row;
-                        const int tok = static_cast<int>(div_by_magic(at, p.group_div));
-                        const bool live = at < rows;
-                        const __nv_bfloat16* src = q + static_cast<int64_t>(r.w.q0 + tok) * p.a.qt +
-                                                   static_cast<int64_t>(r.w.head * p.group + at - tok * p.group) * p.a.qh;
-                        cp_async_16(smem + h * C::TILE + (c >> 3) * kSlab + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                                    live ? src : p.a.q, live);
-                    }
-                    cp_async_wait_all();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&q_full[h]);
-                }
-                if (!ok)
-                    break;
-                // the part's masked tiles
-                const uint32_t par = parts & 1u;
-                if (!wait_both(&bad_free[par], ((parts >> 1) & 1u) ^ 1u))
+            // ------------------------------------------- looks through values
+            uint32_t g = 0, seen = 0;
+            while (volatile Part* d = next_part()) {
+                const int lo = d->lo, hi = d->hi, masked = d->masked;
+                const uint32_t par = part_count & 1u;
+                if (!wait(&bad_free[par], (part_count >> 1) ^ 1u))
                     break;
                 int* bad = reinterpret_cast<int*>(smem + C::OFF_BAD) + par * 3 * kDim;
-                const int free_keys = r.w.limit(p, r.w.first_row(0));
-                if (t == 0)
+                if (lane == 0)
                     any_bad[par] = 0u;
                 bool cleared = false;
-                for (int j = r.lo; ok && j < r.hi; ++j) {
-                    if ((j + 1) * kTile <= free_keys)
-                        continue;
-                    const uint32_t tile = g + (j - r.lo), slot = tile % STAGES;
-                    if (!wait_both(&v_full[slot], tile / STAGES))
+                for (int j = max(lo, masked); j < hi; ++j) {
+                    const uint32_t tile = g + (j - lo), slot = tile % STAGES;
+                    if (!wait(&v_full[slot], tile / STAGES))
                         break;
                     uint8_t* v = smem + C::OFF_V + slot * C::TILE;
-                    bool found = false;
-                    constexpr int PIECES = C::TILE / 16 / 64;
+                    constexpr int PIECES = C::TILE / 16 / 32;
+                    __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
 #pragma unroll 8
                     for (int i = 0; i < PIECES; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 64 + t) * 16);
+                        const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            found |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                            top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
                     }
-                    // (both warps decide together: they write the same list)
-                    if (named_barrier_or(1, 64, found)) {
+                    const bool found = !(__bfloat162float(top.x) < INFINITY && __bfloat162float(top.y) < INFINITY);
+                    if (__any_sync(0xFFFFFFFFu, found)) {
                         if (!cleared) {
-                            for (int i = t; i < 3 * kDim; i += 64)
+                            for (int i = lane; i < 3 * kDim; i += 32)
                                 bad[i] = 0x7FFFFFFF;
-                            if (t == 0)
+                            if (lane == 0)
                                 any_bad[par] = 1u;
                             cleared = true;
                         }
-                        named_barrier_sync(1, 64);
+                        __syncwarp();
                         for (int i = 0; i < PIECES; ++i) {
-                            const int piece = i * 64 + t, in_slab = piece % (kSlab / 16), key = in_slab / 8;
+                            const int piece = i * 32 + lane, in_slab = piece % (kSlab / 16), key = in_slab / 8;
                             const int d0 = piece / (kSlab / 16) * 64 + ((in_slab & 7) ^ (key & 7)) * 8;
                             uint16_t* e = reinterpret_cast<uint16_t*>(v + piece * 16);
                             for (int k = 0; k < 8; ++k) {
@@ -698,11 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(&v_seen[seen & 3u]);
                     ++seen;
                 }
+                if (!ok)
+                    break;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bad_full[par]);
-                g += r.hi - r.lo;
-                ++parts;
+                g += hi - lo;
+                part_done();
             }
         }
     } else {
@@ -710,6 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_registers<kSoftmaxRegs>();
         const int h = warp >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;  // of the half
+        const int of_half = static_cast<int>(div_by_magic(row, p.heads_div));  // its token
+        const int head = row - of_half * p.heads;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const uint32_t s_addr = tmem + lanes + h * kTile, o_addr = tmem + lanes + C::TMEM_O + h * kDim;
         const float2 xs = make_float2(p.xscale, p.xscale);
@@ -718,47 +754,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             return ok;
         };
-        uint32_t turns = 0, uses = 0, parts = 0;
-        Run r = *run;
-        bool started = false;
-        while (have && ok && r.part(p, started)) {
-            const int at = r.w.first_row(h) + row;  // row of the sequence's key head
-            const int rows = r.w.n * p.group;
-            const int mine = min(r.hi, r.w.tiles(p, h));  // this half's tiles end here
-            const int limit = r.w.limit(p, at);
-            const int free_keys = r.w.limit(p, r.w.first_row(h));
+        uint32_t turns = 0, uses = 0;
+        while (have) {
+            volatile Part* d = next_part();
+            if (d == nullptr)
+                break;
+            const int lo = d->lo, end = d->end[h];
+            const int tok = h * p.tokens + of_half;  // of the unit
+            // (rows without a query have no say in when their warp's references move, so that
+            // nothing of them reaches the results)
+            const bool live = of_half < p.tokens && tok < d->tokens && head < d->q_heads;
+            int limit, free_keys;  // keys that this row sees, and the half's first one
+            {
+                const int m = d->m, seen = d->first_seen;
+                limit = p.a.causal ? max(min(seen + tok, m), 0) : m;
+                free_keys = p.a.causal ? max(min(seen + h * p.tokens, m), 0) : m;
+            }
             float m = kUnset;
             float2 l = make_float2(0.0f, 0.0f);
-            for (int j = r.lo; j < mine; ++j) {
+            for (int j = lo; j < end; ++j) {
                 if (!wait_all(&s_full[h], turns))
                     break;
                 ++turns;
-                float s[kTile];
+                float s[kTile], mx[4];
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32)
-                    tmem_ld_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s + c));
+                    mx[c / 32] = tmem_ld_max_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s + c));
                 tmem_ld_wait();
                 if ((j + 1) * kTile > free_keys) {
                     const int seen = limit - j * kTile;
+                    mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
+                    for (int c = 0; c < kTile; ++c) {
                         s[c] = c < seen ? s[c] : -INFINITY;
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < kTile; c += 8) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx[k] = fmaxf(mx[k], fmaxf(s[c + k], s[c + k + 4]));
+                        mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                    }
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.xscale;
-                if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+                if (__any_sync(0xFFFFFFFFu, live && top > m + kSlack)) {
                     const float next = fmaxf(m, top);
                     const float factor = exp2_approx(m - next);
                     m = next;
                     l.x *= factor;
                     l.y *= factor;
-                    if (j > r.lo) {  // (the part's tiles so far are in O: this one's S came after them)
+                    if (j > lo) {  // (the part's tiles so far are in O: this one's S came after them)
 #pragma unroll 1
                         for (int c = 0; c < kDim; c += 16) {
                             uint32_t o[16];
@@ -772,44 +811,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float minus = -m;
+                // half of the keys after the other: the MMAs begin with the first
 #pragma unroll
                 for (int c = 0; c < kTile; c += 64) {
                     uint32_t w[32];
 #pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        float x[2];
-                        fma_pair(x, s[c + k], s[c + k + 1], xs, minus);
-                        x[0] = exp2_approx(x[0]);
-                        x[1] = exp2_approx(x[1]);
-                        l = add_pair(l, x[0], x[1]);
-                        w[k / 2] = pack2(x[0], x[1]);
+                    for (int k = c; k < c + 64; k += 2) {
+                        fma_pair(s + k, s[k], s[k + 1], xs, minus);
+                        s[k] = exp2_approx(s[k]);
+                        s[k + 1] = exp2_approx(s[k + 1]);
+                        w[(k - c) / 2] = pack2(s[k], s[k + 1]);
                     }
                     tmem_st_32x32b_x32(s_addr + c / 2, w);
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(c == 0 ? &p_half[h] : &p_full[h]);
                 }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&p_full[h]);
+                // (the sum while the MMAs run)
+                float2 more = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < kTile; k += 4) {
+                    l = add_pair(l, s[k], s[k + 1]);
+                    more = add_pair(more, s[k + 2], s[k + 3]);
+                }
+                l = add_pair(l, more.x, more.y);
             }
             // ------------------------------------------------------- results
-            const bool some = mine > r.lo;
+            const bool some = end > lo;
             if (ok && some) {
                 wait_all(&o_full[h], uses);
                 ++uses;
             }
             if (ok)
-                wait_all(&bad_full[parts & 1u], parts >> 1);
+                wait_all(&bad_full[part_count & 1u], part_count >> 1);
             if (!ok)
                 break;
-            const bool whole = r.lo == 0 && r.hi == r.tiles;
-            const int* bad = any_bad[parts & 1u] ? reinterpret_cast<const int*>(smem + C::OFF_BAD) + (parts & 1u) * 3 * kDim : nullptr;
+            const int slot = d->slot;
+            const int* bad = any_bad[part_count & 1u] ? reinterpret_cast<const int*>(smem + C::OFF_BAD) + (part_count & 1u) * 3 * kDim : nullptr;
             const float sum = l.x + l.y;
-            const float scale = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int tok = static_cast<int>(div_by_magic(at, p.group_div));
-            const int64_t token = r.w.q0 + tok;
-            const int hq = r.w.head * p.group + at - tok * p.group;
-            const int64_t part_row = (2 * static_cast<int64_t>(blockIdx.x) + (r.lo > 0 ? 0 : 1)) * kRows + h * kHalf + row;
+            const float scale = slot >= 0 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int64_t token = d->token + static_cast<int64_t>(tok);
+            const int hq = d->q_head + head;
+            const int64_t part_row = (2 * static_cast<int64_t>(blockIdx.x) + slot) * kRows + h * kHalf + row;
 #pragma unroll 1
             for (int c = 0; c < kDim; c += 32) {
                 float x[32];
@@ -837,8 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[k] += add;
                     }
                 }
-                if (at < rows) {
-                    if (whole) {
+                if (live) {
+                    if (slot < 0) {
                         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + token * p.a.ot + hq * p.a.oh + c);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -851,31 +896,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (at < rows) {
-                if (!whole)
+            if (live) {
+                if (slot >= 0)
                     p.part_ml[part_row] = make_float2(m, sum);
                 else if (p.a.lse != nullptr)
                     p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
-            }
-            if (r.hi < r.tiles) {
-                if (r.lo > 0) {
-                    cut.through = 1;
-                } else {
-                    cut.open = 1;
-                    cut.b = r.w.b, cut.head = r.w.head, cut.block = r.w.block;
-                }
             }
             // O, and what was found in the values, may be written again
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&bad_free[parts & 1u]);
-            ++parts;
-        }
-        if (threadIdx.x == 0 && p.may_cut) {
-            if (!ok)
-                cut.open = cut.through = 0;
-            p.cuts[blockIdx.x] = cut;
+                mbar_arrive(&bad_free[part_count & 1u]);
+            part_done();
         }
     }
     __syncwarp();
@@ -904,8 +936,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const Prom
     Walk w;
     w.b = cut.b;
     w.sequence(p);
-    const int at = cut.block * kRows + row;
-    if (at >= w.n * p.group)
+    const int half = row / kHalf, of_half = static_cast<int>(div_by_magic(row - half * kHalf, p.heads_div));
+    const int tok = (2 * cut.block + half) * p.tokens + of_half;
+    const int group = p.a.q_heads / p.a.kv_heads;
+    const int key_head = cut.head / p.chunks, of_group = (cut.head - key_head * p.chunks) * kHalf + row - half * kHalf - of_half * p.heads;
+    if (of_half >= p.tokens || tok >= w.n || of_group >= group)
         return;
     // the unit's parts: this one, those that it runs through, and the one behind
     int parts = 2;
@@ -952,9 +987,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const Prom
         }
     }
     const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int tok = static_cast<int>(div_by_magic(at, p.group_div));
     const int64_t token = w.q0 + tok;
-    const int hq = cut.head * p.group + at - tok * p.group;
+    const int hq = key_head * group + of_group;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.out) + token * p.a.ot + hq * p.a.oh + lane * W);
 #pragma unroll
     for (int k = 0; k < W / 2; ++k)
@@ -994,12 +1028,13 @@ cudaError_t launch(const PromptParams& p, cudaStream_t stream)
     }
     // (without keys nothing is loaded: the maps only have to be valid)
     const bool keys = p.a.keys > 0;
-    CUtensorMap k_map, v_map;
-    if (!make_heads_map(&k_map, keys ? p.a.k : p.a.q, std::max<int64_t>(p.a.keys, 1), keys ? p.a.kv_heads : 1, kDim, p.a.kt, p.a.kh, kTile) ||
-        !make_heads_map(&v_map, keys ? p.a.v : p.a.q, std::max<int64_t>(p.a.keys, 1), keys ? p.a.kv_heads : 1, kDim, p.a.vt, p.a.vh, kTile))
+    CUtensorMap q_map, k_map, v_map;
+    if (!make_heads_map(&q_map, p.a.q, p.a.T, p.a.q_heads, kDim, p.a.qt, p.a.qh, p.tokens, p.heads, true) ||
+        !make_heads_map(&k_map, keys ? p.a.k : p.a.q, std::max<int64_t>(p.a.keys, 1), keys ? p.a.kv_heads : 1, kDim, p.a.kt, p.a.kh, kTile, 1, false) ||
+        !make_heads_map(&v_map, keys ? p.a.v : p.a.q, std::max<int64_t>(p.a.keys, 1), keys ? p.a.kv_heads : 1, kDim, p.a.vt, p.a.vh, kTile, 1, false))
         return cudaErrorInvalidValue;
     const unsigned ctas = static_cast<unsigned>(sm_count());
-    err = launch_pdl(prompt_attention_kernel<kDim>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p, k_map, v_map);
+    err = launch_pdl(prompt_attention_kernel<kDim>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p, q_map, k_map, v_map);
     if (err != cudaSuccess || !p.may_cut)
         return err;
     return launch_pdl(prompt_join_kernel<kDim>, dim3(ctas, kRows / kJoinWarps), dim3(kJoinWarps * 32), 0, stream, p);
@@ -1032,8 +1067,11 @@ cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t stream)
 {
     PromptParams p = {};
     p.a = a;
-    p.group = a.q_heads / a.kv_heads;
-    p.group_div = div_magic(p.group);
+    const int group = a.q_heads / a.kv_heads;
+    p.heads = std::min(group, kHalf);
+    p.chunks = (group + kHalf - 1) / kHalf;
+    p.tokens = kHalf / p.heads;
+    p.heads_div = div_magic(p.heads);
     p.xscale = a.scale * 1.44269504088896341f;
     p.may_cut = a.keys > kWholeTiles * kTile;
     if (p.may_cut) {
