@@ -25,8 +25,9 @@
 // second kernel joins.  Where all units are short, they are dealt out whole.
 //
 // Warps: 0-3 and 4-7 the softmax of the halves (they also write the results), 8
-// goes over the run's units and loads queries, keys and values (TMA), 9 and 10
-// issue the MMAs of the halves, 11 looks through values.
+// goes over the run's units and loads queries, keys and values (TMA), 9 issues the
+// MMAs, 10 looks through values and sees to their loads (11 fills the register
+// group).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -75,8 +76,8 @@ struct PromptParams {
     int tokens;     // of a half
     DivMagic heads_div;
     float xscale;   // scale * log2(e)
-    float* part_o;  // [CTA][2][kRows][dim]
-    float2* part_ml;
+    float* part_o;  // [CTA][2][half][dim / 4][kHalf][4]
+    float2* part_ml;  // [CTA][2][half][kHalf]
     Cut* cuts;      // [CTA]
     bool may_cut;
 };
@@ -113,6 +114,8 @@ __device__ __forceinline__ float2 add_pair(float2 a, float b0, float b1)
         : "f"(a.x), "f"(a.y), "f"(b0), "f"(b1));
     return r;
 }
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
 template <int kRegs>
 __device__ __forceinline__ void set_registers()
@@ -369,8 +372,9 @@ struct Cfg {
     static constexpr int OFF_K = 2 * QBUFS * TILE;  // Q first
     static constexpr int OFF_V = OFF_K + STAGES * TILE;
     static constexpr int OFF_BAD = OFF_V + STAGES * TILE;  // int [2][3][kDim]: first keys whose value is inf, -inf, NaN
-    static constexpr int OFF_BAR = OFF_BAD + 2 * 3 * kDim * 4;
-    static constexpr int BARS = 4 * STAGES + 4 + 4 * QBUFS + 2 * 6 + 2 * kParts + 2;
+    static constexpr int OFF_OUT = OFF_BAD + 2 * 3 * kDim * 4;  // [8 warps] 32 elements of 32 rows
+    static constexpr int OFF_BAR = OFF_OUT + 8 * 2048;
+    static constexpr int BARS = 4 * STAGES + 4 * QBUFS + 2 * 6 + 2 * kParts + 1;
     static constexpr int OFF_SLOT = OFF_BAR + BARS * 8;  // TMEM address, flags
     static constexpr int OFF_RUN = (OFF_SLOT + 32 + 15) / 16 * 16;
     static constexpr int OFF_PARTS = OFF_RUN + 128;
@@ -396,18 +400,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* k_free = k_full + STAGES;    // [STAGES] both halves' products with it have ended
     uint64_t* v_full = k_free + STAGES;    // [STAGES]
     uint64_t* v_free = v_full + STAGES;    // [STAGES]
-    uint64_t* v_seen = v_free + STAGES;    // [4] a masked tile's values are looked through
-    uint64_t* q_full = v_seen + 4;         // [QBUFS][2] by half
+    uint64_t* q_full = v_free + STAGES;       // [QBUFS][2] by half
     uint64_t* q_free = q_full + 2 * QBUFS; // [QBUFS][2]
     uint64_t* s_full = q_free + 2 * QBUFS; // [2] scores are complete (and the tile before is in O)
-    uint64_t* p_half = s_full + 2;         // [2] probabilities of half the keys are in tensor memory
-    uint64_t* p_full = p_half + 2;         // [2] and of the others
+    uint64_t* p_half = s_full + 2;         // [2] half the probabilities are in tensor memory, the values and the next keys have landed
+    uint64_t* p_full = p_half + 2;         // [2] and the other half
     uint64_t* o_full = p_full + 2;         // [2] the part's last tile is in O
     uint64_t* bad_full = o_full + 2;       // [2] by part: its masked tiles are looked through
     uint64_t* bad_free = bad_full + 2;     // [2] and what was found is read
     uint64_t* part_full = bad_free + 2;    // [kParts] a part is described
     uint64_t* part_free = part_full + kParts;  // [kParts] and done with
-    uint64_t* drained = part_free + kParts;    // [2] every MMA of a half has ended
+    uint64_t* drained = part_free + kParts;    // every MMA has ended
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
     volatile uint32_t* any_bad = tmem_slot + 1;  // [2] by part
     Run* run = reinterpret_cast<Run*>(smem + C::OFF_RUN);
@@ -416,30 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_free[i], 2);
+            mbar_init(&k_free[i], 1);
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_free[i], 2);
+            mbar_init(&v_free[i], 1);
         }
-        for (int i = 0; i < 4; ++i)
-            mbar_init(&v_seen[i], 1);
         for (int i = 0; i < 2 * QBUFS; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_half[i], 4);
+            mbar_init(&p_half[i], 4 + 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&bad_full[i], 1);
             mbar_init(&bad_free[i], 8);
-            mbar_init(&drained[i], 1);
             any_bad[i] = 0u;
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&part_full[i], 1);
-            mbar_init(&part_free[i], 8 + 2 + 1);
+            mbar_init(&part_free[i], 8 + 2);
         }
+        mbar_init(drained, 1);
         fence_mbar_init();
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&k_map);
@@ -458,13 +459,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const uint64_t limit_ns = p.a.wait_ns;
     bool ok = true;
-    // a wait of one thread, and one of a whole warp; once one has run out, the role ends
+    // a wait of one thread, and one of a whole warp (quick where the phase is complete:
+    // a serial chain of a few hundred cycles at every wait of the MMA warp is what its
+    // products wait for); once one has run out, the role ends
     auto wait_one = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && mbar_wait_bounded(bar, parity & 1u, p.a.status, kStatusTimeout, limit_ns);
         return ok;
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = __all_sync(0xFFFFFFFFu, wait_one(bar, parity));
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity & 1u)))
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, p.a.status, kStatusTimeout, limit_ns));
         return ok;
     };
     // the next part's description, or nullptr at the end of the run
@@ -581,89 +585,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_wait_bounded(&q_full[(use % QBUFS) * 2 + h], (use / QBUFS) & 1u, p.a.status, kStatusTimeout, limit_ns);
                     }
             }
-        } else if (warp < 11) {
-            // ---------------------------------------------- MMAs of one half
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMAs
             // (the whole warp walks the loop and one elected lane issues: the operands
-            // of the MMAs then stay in uniform registers)
-            const int h = warp - 9;
+            // of the MMAs then stay in uniform registers.  One warp for both halves: their
+            // products come one after the other, not both at half the rate, so that a half's
+            // scores are weighed while the other's products run)
             constexpr uint32_t idesc_s = idesc_bf16(kHalf, kTile, 0, 0);
             constexpr uint32_t idesc_o = idesc_bf16(kHalf, kDim, 0, 1);
+            const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2);
             const uint64_t kd = smem_desc(smem_u32(smem + C::OFF_K), 16, 1024, 2);
             const uint64_t vd = smem_desc(smem_u32(smem + C::OFF_V), kSlab, 1024, 2);
-            const uint32_t s_tmem = tmem + h * kTile, o_tmem = tmem + C::TMEM_O + h * kDim;
             const bool withhold = p.a.withhold && blockIdx.x == 0;
-            uint32_t g = 0, turns = 0, queries = 0, seen = 0;
+            uint32_t g = 0, turns[2] = {0, 0}, queries[2] = {0, 0};
             while (volatile Part* d = next_part()) {
-                const int lo = d->lo, hi = d->hi, end = d->end[h], masked = d->masked;
-                const uint32_t buf = (queries % QBUFS) * 2 + h;
-                const uint64_t qd = smem_desc(smem_u32(smem + buf * C::TILE), 16, 1024, 2);
-                // S of the half with tile j, the run's tile `tile`
-                auto scores = [&](int j, uint32_t tile) {
-                    const uint32_t slot = tile % STAGES;
-                    if (!wait(&k_full[slot], tile / STAGES))
-                        return;
-                    if (j >= end) {
-                        if (lane == 0)
-                            mbar_arrive(&k_free[slot]);
-                        return;
-                    }
-                    tc_fence_after_sync();
-                    const uint64_t k = kd + ((slot * C::TILE) >> 4);
-                    if (elect_one()) {
+                // (by shuffles: what the MMAs' operands depend on has to be uniform for the compiler too)
+                const int lo = uniform(d->lo), hi = uniform(d->hi);
+                const int end[2] = {uniform(d->end[0]), uniform(d->end[1])};
+                uint32_t buf[2] = {};
+                // S of a half with the tile in a slot of K
+                auto scores = [&](int h, uint32_t slot, bool last) {
+                    const uint64_t q = qd + ((buf[h] * C::TILE) >> 4), k = kd + ((slot * C::TILE) >> 4);
 #pragma unroll
-                        for (int i = 0; i < kDim / 16; ++i) {
-                            const uint64_t at = ((i >> 2) * kSlab + 32 * (i & 3)) >> 4;
-                            tc_mma_f16(s_tmem, qd + at, k + at, idesc_s, i != 0);
-                        }
-                        tc_commit(&s_full[h]);
-                        tc_commit(&k_free[slot]);
-                        if (j == end - 1)
-                            tc_commit(&q_free[buf]);
+                    for (int i = 0; i < kDim / 16; ++i) {
+                        const uint64_t at = ((i >> 2) * kSlab + 32 * (i & 3)) >> 4;
+                        tc_mma_f16(tmem + h * kTile, q + at, k + at, idesc_s, i != 0);
                     }
-                    __syncwarp();
+                    tc_commit(&s_full[h]);
+                    if (last)
+                        tc_commit(&q_free[buf[h]]);
                 };
-                if (end > lo) {
-                    wait(&q_full[buf], queries / QBUFS);
-                    ++queries;
-                }
-                if (ok && hi > lo)
-                    scores(lo, g);
-                for (int j = lo; ok && j < hi; ++j, ++g) {
-                    const uint32_t slot = g % STAGES;
-                    if (!wait(&v_full[slot], g / STAGES))
-                        break;
-                    if (j >= masked) {
-                        if (!wait(&v_seen[seen & 3u], seen >> 2))
+                // (the second half has the unit's last tile, unless it has no rows)
+                const int closing = end[1] > lo ? 1 : 0;
+                if (hi > lo && !wait(&k_full[g % STAGES], g / STAGES))
+                    break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    buf[h] = (queries[h] % QBUFS) * 2 + h;
+                    if (end[h] > lo) {
+                        if (!wait(&q_full[buf[h]], queries[h]++ / QBUFS))
                             break;
-                        ++seen;
-                    }
-                    if (j >= end) {
-                        if (lane == 0)
-                            mbar_arrive(&v_free[slot]);
-                    } else {
-                        const uint64_t v = vd + ((slot * C::TILE) >> 4);
-                        // half of the keys after the other, as their probabilities come
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            if (!wait(part == 0 ? &p_half[h] : &p_full[h], turns))
-                                break;
-                            tc_fence_after_sync();
-                            if (elect_one() && !withhold) {
-#pragma unroll
-                                for (int i = part * 4; i < part * 4 + 4; ++i)
-                                    tc_mma_f16_ts(o_tmem, s_tmem + 8 * i, v + ((2048 * i) >> 4), idesc_o, i != 0 || j != lo);
-                                if (part == 1) {
-                                    tc_commit(&v_free[slot]);
-                                    if (j == end - 1)
-                                        tc_commit(&o_full[h]);
-                                }
-                            }
-                            __syncwarp();
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            scores(h, g % STAGES, lo == end[h] - 1);
+                            if (h == closing)
+                                tc_commit(&k_free[g % STAGES]);
                         }
-                        ++turns;
+                        __syncwarp();
                     }
-                    if (ok && j + 1 < hi)
-                        scores(j + 1, g + 1);
+                }
+                for (int j = lo; ok && j < hi; ++j, ++g) {
+                    const uint32_t slot = g % STAGES, next = (g + 1) % STAGES;
+                    const uint64_t v = vd + ((slot * C::TILE) >> 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (j >= end[h])
+                            continue;
+                        // half of the keys after the other, as their probabilities come
+                        if (!wait(&p_half[h], turns[h]))
+                            break;
+                        tc_fence_after_sync();
+                        if (elect_one() && !withhold) {
+#pragma unroll
+                            for (int i = 0; i < kTile / 32; ++i)
+                                tc_mma_f16_ts(tmem + C::TMEM_O + h * kDim, tmem + h * kTile + 8 * i, v + ((2048 * i) >> 4),
+                                              idesc_o, i != 0 || j != lo);
+                        }
+                        __syncwarp();
+                        if (!wait(&p_full[h], turns[h]++))
+                            break;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            if (!withhold) {
+#pragma unroll
+                                for (int i = kTile / 32; i < kTile / 16; ++i)
+                                    tc_mma_f16_ts(tmem + C::TMEM_O + h * kDim, tmem + h * kTile + 8 * i, v + ((2048 * i) >> 4),
+                                                  idesc_o, 1);
+                                if (j == end[h] - 1)
+                                    tc_commit(&o_full[h]);
+                            }
+                            if (j + 1 < end[h])
+                                scores(h, next, j + 1 == end[h] - 1);
+                            if (h == closing) {
+                                tc_commit(&v_free[slot]);
+                                if (j + 1 < hi)
+                                    tc_commit(&k_free[next]);
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
                 if (!ok)
                     break;
@@ -671,14 +681,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // whatever was issued has ended before tensor and shared memory go
             if (elect_one())
-                tc_commit(&drained[h]);
+                tc_commit(drained);
             __syncwarp();
-            mbar_wait_bounded(&drained[h], 0, p.a.status, kStatusTimeout, limit_ns);
-        } else {
-            // ------------------------------------------- looks through values
-            uint32_t g = 0, seen = 0;
+            mbar_wait_bounded(drained, 0, p.a.status, kStatusTimeout, limit_ns);
+        } else if (warp == 10) {
+            // -------------- what the second product of a tile needs beside P
+            // its values, looked through where the tile is masked, and the next tile's keys:
+            // one more arrival on its barrier, so that the MMA warp has fewer waits
+            uint32_t g = 0, turns[2] = {0, 0};
             while (volatile Part* d = next_part()) {
                 const int lo = d->lo, hi = d->hi, masked = d->masked;
+                const int end[2] = {d->end[0], d->end[1]};
                 const uint32_t par = part_count & 1u;
                 if (!wait(&bad_free[par], (part_count >> 1) ^ 1u))
                     break;
@@ -686,56 +699,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     any_bad[par] = 0u;
                 bool cleared = false;
-                for (int j = max(lo, masked); j < hi; ++j) {
-                    const uint32_t tile = g + (j - lo), slot = tile % STAGES;
-                    if (!wait(&v_full[slot], tile / STAGES))
+                for (int j = lo; j < hi; ++j, ++g) {
+                    if (!wait(&v_full[g % STAGES], g / STAGES))
                         break;
-                    uint8_t* v = smem + C::OFF_V + slot * C::TILE;
-                    constexpr int PIECES = C::TILE / 16 / 32;
-                    __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+                    if (j >= masked) {
+                        uint8_t* v = smem + C::OFF_V + (g % STAGES) * C::TILE;
+                        constexpr int PIECES = C::TILE / 16 / 32;
+                        __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
 #pragma unroll 8
-                    for (int i = 0; i < PIECES; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
-                    }
-                    const bool found = !(__bfloat162float(top.x) < INFINITY && __bfloat162float(top.y) < INFINITY);
-                    if (__any_sync(0xFFFFFFFFu, found)) {
-                        if (!cleared) {
-                            for (int i = lane; i < 3 * kDim; i += 32)
-                                bad[i] = 0x7FFFFFFF;
-                            if (lane == 0)
-                                any_bad[par] = 1u;
-                            cleared = true;
-                        }
-                        __syncwarp();
                         for (int i = 0; i < PIECES; ++i) {
-                            const int piece = i * 32 + lane, in_slab = piece % (kSlab / 16), key = in_slab / 8;
-                            const int d0 = piece / (kSlab / 16) * 64 + ((in_slab & 7) ^ (key & 7)) * 8;
-                            uint16_t* e = reinterpret_cast<uint16_t*>(v + piece * 16);
-                            for (int k = 0; k < 8; ++k) {
-                                if ((e[k] & 0x7F80u) != 0x7F80u)
-                                    continue;
-                                const int kind = (e[k] & 0x7Fu) != 0u ? 2 : e[k] >> 15;
-                                atomicMin(&bad[kind * kDim + d0 + k], j * kTile + key);
-                                e[k] = 0;
-                            }
+                            const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
                         }
-                        fence_proxy_async_smem();
+                        const bool found = !(__bfloat162float(top.x) < INFINITY && __bfloat162float(top.y) < INFINITY);
+                        if (__any_sync(0xFFFFFFFFu, found)) {
+                            if (!cleared) {
+                                for (int i = lane; i < 3 * kDim; i += 32)
+                                    bad[i] = 0x7FFFFFFF;
+                                if (lane == 0)
+                                    any_bad[par] = 1u;
+                                cleared = true;
+                            }
+                            __syncwarp();
+                            for (int i = 0; i < PIECES; ++i) {
+                                const int piece = i * 32 + lane, in_slab = piece % (kSlab / 16), key = in_slab / 8;
+                                const int d0 = piece / (kSlab / 16) * 64 + ((in_slab & 7) ^ (key & 7)) * 8;
+                                uint16_t* e = reinterpret_cast<uint16_t*>(v + piece * 16);
+                                for (int k = 0; k < 8; ++k) {
+                                    if ((e[k] & 0x7F80u) != 0x7F80u)
+                                        continue;
+                                    const int kind = (e[k] & 0x7Fu) != 0u ? 2 : e[k] >> 15;
+                                    atomicMin(&bad[kind * kDim + d0 + k], j * kTile + key);
+                                    e[k] = 0;
+                                }
+                            }
+                            fence_proxy_async_smem();
+                        }
                     }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&v_seen[seen & 3u]);
-                    ++seen;
+                    if (j + 1 < hi && !wait(&k_full[(g + 1) % STAGES], (g + 1) / STAGES))
+                        break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (j >= end[h])
+                            continue;
+                        // (the half's tile before has to have all its arrivals)
+                        if (!wait(&p_half[h], turns[h]++ ^ 1u))
+                            break;
+                        if (lane == 0)
+                            mbar_arrive(&p_half[h]);
+                    }
+                    if (!ok)
+                        break;
                 }
                 if (!ok)
                     break;
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bad_full[par]);
-                g += hi - lo;
                 part_done();
             }
         }
@@ -815,6 +838,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kTile; c += 64) {
                     uint32_t w[32];
+                    if (c > 0) {  // (keeps the compiler from weighing these before the others are handed over)
+#pragma unroll
+                        for (int k = c; k < c + 64; ++k)
+                            asm volatile("" : "+f"(s[k]));
+                    }
 #pragma unroll
                     for (int k = c; k < c + 64; k += 2) {
                         fma_pair(s + k, s[k], s[k + 1], xs, minus);
@@ -854,7 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float scale = slot >= 0 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             const int64_t token = d->token + static_cast<int64_t>(tok);
             const int hq = d->q_head + head;
-            const int64_t part_row = (2 * static_cast<int64_t>(blockIdx.x) + slot) * kRows + h * kHalf + row;
+            const int64_t out_row = live ? token * p.a.ot + hq * p.a.oh : -1;
+            const int64_t part_half = (2 * static_cast<int64_t>(blockIdx.x) + slot) * 2 + h;
 #pragma unroll 1
             for (int c = 0; c < kDim; c += 32) {
                 float x[32];
@@ -870,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 32; ++k)
                     x[k] *= scale;
                 if (bad != nullptr) {
-#pragma unroll 4
+#pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         float add = 0.0f;
                         if (bad[c + k] < limit)
@@ -882,23 +911,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[k] += add;
                     }
                 }
-                if (live) {
-                    if (slot < 0) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + token * p.a.ot + hq * p.a.oh + c);
+                if (slot < 0) {
+                    // by way of shared memory, so that four lanes write 64 bytes of a row
+                    uint8_t* mine = smem + C::OFF_OUT + warp * 2048;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dst[k] = pack8(x + 8 * k);
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + part_row * kDim + c);
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8(x + 8 * k);
+                    __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int from = k * 8 + (lane >> 2);  // lane of the row
+                        const int64_t dst = __shfl_sync(0xFFFFFFFFu, out_row, from);
+                        const uint4 v = *reinterpret_cast<const uint4*>(mine + from * 64 + (((lane & 3) ^ ((from >> 1) & 3)) << 4));
+                        if (dst >= 0)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + dst + c + (lane & 3) * 8) = v;
                     }
+                    __syncwarp();
+                } else if (live) {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o) + (part_half * (kDim / 4) + c / 4) * kHalf + row;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[k * kHalf] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                 }
             }
             if (live) {
                 if (slot >= 0)
-                    p.part_ml[part_row] = make_float2(m, sum);
+                    p.part_ml[part_half * kHalf + row] = make_float2(m, sum);
                 else if (p.a.lse != nullptr)
                     p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
             }
@@ -920,27 +958,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the unit that begins in a CTA's run and goes on behind it: a
-// warp per row.
+// block has 32 rows, a lane each, and a warp 4 elements of every 32.
 constexpr int kJoinWarps = 8;
 
 template <int kDim>
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const PromptParams p)
 {
+    constexpr int W = kDim / (4 * kJoinWarps);  // groups of 4 elements of a thread
+    __shared__ uint2 rows[32][kDim / 4 + 1];
     grid_dependency_wait();
     launch_dependents();
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+    const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cut cut = p.cuts[c0];
     if (!cut.open)
-        return;
-    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-    Walk w;
-    w.b = cut.b;
-    w.sequence(p);
-    const int half = row / kHalf, of_half = static_cast<int>(div_by_magic(row - half * kHalf, p.heads_div));
-    const int tok = (2 * cut.block + half) * p.tokens + of_half;
-    const int group = p.a.q_heads / p.a.kv_heads;
-    const int key_head = cut.head / p.chunks, of_group = (cut.head - key_head * p.chunks) * kHalf + row - half * kHalf - of_half * p.heads;
-    if (of_half >= p.tokens || tok >= w.n || of_group >= group)
         return;
     // the unit's parts: this one, those that it runs through, and the one behind
     int parts = 2;
@@ -953,48 +983,52 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const Prom
         }
     }
     parts = min(parts, static_cast<int>(gridDim.x) - c0);
-    auto index = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(c0) + (i == 0 ? 1 : 2 * i)) * kRows + row; };
+    Walk w;
+    w.b = cut.b;
+    w.sequence(p);
+    const int half = blockIdx.y >> 2, group = p.a.q_heads / p.a.kv_heads, key_head = cut.head / p.chunks;
+    auto row_of = [&](int row, int64_t* token, int* hq) {  // of the half
+        const int of_half = static_cast<int>(div_by_magic(row, p.heads_div)), head = row - of_half * p.heads;
+        const int tok = (2 * cut.block + half) * p.tokens + of_half, of_group = (cut.head - key_head * p.chunks) * kHalf + head;
+        *token = static_cast<int64_t>(w.q0) + tok;
+        *hq = key_head * group + of_group;
+        return of_half < p.tokens && tok < w.n && of_group < group;
+    };
+    const int row0 = (blockIdx.y & 3) * 32, row = row0 + lane;
+    int64_t token;
+    int hq;
+    const bool live = row_of(row, &token, &hq);
+    auto index = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(c0) + (i == 0 ? 1 : 2 * i)) * 2 + half; };
     float mx = kUnset;
-    for (int i = lane; i < parts; i += 32)
-        mx = fmaxf(mx, p.part_ml[index(i)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-    constexpr int W = kDim / 32;  // elements of a lane
-    float o[W] = {}, sum = 0.0f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float mine = 0.0f, add = 0.0f;
-        if (i0 + lane < parts) {
-            const float2 ml = p.part_ml[index(i0 + lane)];
-            mine = exp2_approx(ml.x - mx);
-            add = mine * ml.y;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            add += __shfl_xor_sync(0xFFFFFFFFu, add, d);
-        sum += add;
-        const int here = min(32, parts - i0);
 #pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float f = __shfl_sync(0xFFFFFFFFu, mine, i);
-            const float* src = p.part_o + index(i0 + i) * kDim + lane * W;
+    for (int i = 0; i < parts; ++i)
+        mx = live ? fmaxf(mx, p.part_ml[index(i) * kHalf + row].x) : mx;
+    float4 o[W] = {};
+    float sum = 0.0f;
+#pragma unroll 2
+    for (int i = 0; i < (live ? parts : 0); ++i) {
+        const int64_t at = index(i);
+        const float2 ml = p.part_ml[at * kHalf + row];
+        const float f = exp2_approx(ml.x - mx);
+        sum += f * ml.y;
 #pragma unroll
-            for (int k = 0; k < W; k += 2) {
-                const float2 x = *reinterpret_cast<const float2*>(src + k);
-                o[k] += f * x.x;
-                o[k + 1] += f * x.y;
-            }
+        for (int k = 0; k < W; ++k) {
+            const float4 x = reinterpret_cast<const float4*>(p.part_o)[(at * (kDim / 4) + k * kJoinWarps + warp) * kHalf + row];
+            o[k].x += f * x.x, o[k].y += f * x.y, o[k].z += f * x.z, o[k].w += f * x.w;
         }
     }
     const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t token = w.q0 + tok;
-    const int hq = key_head * group + of_group;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.out) + token * p.a.ot + hq * p.a.oh + lane * W);
 #pragma unroll
-    for (int k = 0; k < W / 2; ++k)
-        dst[k] = pack2(o[2 * k] * scale, o[2 * k + 1] * scale);
-    if (lane == 0 && p.a.lse != nullptr)
+    for (int k = 0; k < W; ++k)
+        rows[lane][k * kJoinWarps + warp] = make_uint2(pack2(o[k].x * scale, o[k].y * scale), pack2(o[k].z * scale, o[k].w * scale));
+    if (warp == 0 && live && p.a.lse != nullptr)
         p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * (kDim / 4); i += kJoinWarps * 32) {
+        const int r = i / (kDim / 4), c = i % (kDim / 4);
+        if (row_of(row0 + r, &token, &hq))
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + token * p.a.ot + hq * p.a.oh + c * 4) = rows[r][c];
+    }
 }
 
 template <int kDim>
@@ -1037,7 +1071,7 @@ cudaError_t launch(const PromptParams& p, cudaStream_t stream)
     err = launch_pdl(prompt_attention_kernel<kDim>, dim3(ctas), dim3(kThreads), C::SMEM, stream, p, q_map, k_map, v_map);
     if (err != cudaSuccess || !p.may_cut)
         return err;
-    return launch_pdl(prompt_join_kernel<kDim>, dim3(ctas, kRows / kJoinWarps), dim3(kJoinWarps * 32), 0, stream, p);
+    return launch_pdl(prompt_join_kernel<kDim>, dim3(ctas, kRows / 32), dim3(kJoinWarps * 32), 0, stream, p);
 }
 
 // Places of the partial results in the workspace, of all the CTAs.
