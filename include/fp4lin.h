@@ -882,7 +882,8 @@ FP4LIN_API fp4_status fp4_gemv_nvfp4(const void* x_bf16, const uint8_t* w, const
  *   expert_ids  int32 [rows] (device)
  *   w, sw, bias [E][N][K/2], E consecutive SWIZZLED arrays, [E][N] or NULL, as
  *               for fp4_gemm_mxfp4_grouped
- * rows 0 .. 65535, 1 <= E <= 1024, rows_per_x >= 1; otherwise as above.      */
+ * rows 0 .. 65535, 1 <= E <= 1024, E * N below 2^31 - 256, rows_per_x >= 1;
+ * otherwise as above.                                                       */
 FP4LIN_API fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* expert_ids, int32_t E, int64_t rows,
                                   int32_t rows_per_x, const uint8_t* w, const uint8_t* sw,
                                   const void* bias_bf16, void* out_bf16, int64_t N, int64_t K, void* stream);

@@ -147,9 +147,10 @@ fp4_status gemv(const void* x, const uint8_t* w, const uint8_t* sw, float w_glob
     if (M == 0)
         return FP4_OK;
     fp4_status st = check_gemv(x, w, sw, bias, out, N, K);
-    if (st != FP4_OK || (st = device()) != FP4_OK)
-        return st;
     fp4lin::GemvArgs a = {};
+    if (st != FP4_OK || (st = device(&a.status)) != FP4_OK)
+        return st;
+    a.wait_ns = fp4lin::api_wait_limit_ns();
     a.x = x, a.w = w, a.sw = sw, a.bias = bias, a.out = out;
     a.M = static_cast<int>(M), a.N = N, a.K = K;
     a.nv = nv, a.w_global = w_global;
@@ -577,13 +578,16 @@ fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* expert_ids,
     fp4_status st = check_gemv(x_bf16, w, sw, bias_bf16, out_bf16, N, K);
     if (st != FP4_OK)
         return st;
+    if (E * N >= kMaxDim - 256)
+        return FP4_ERR_SHAPE;  // 32-bit rows
     if (!expert_ids)
         return FP4_ERR_INVALID_ARG;
     if (!aligned(expert_ids, 4))
         return FP4_ERR_ALIGNMENT;
-    if ((st = device()) != FP4_OK)
-        return st;
     fp4lin::GemvArgs a = {};
+    if ((st = device(&a.status)) != FP4_OK)
+        return st;
+    a.wait_ns = fp4lin::api_wait_limit_ns();
     a.x = x_bf16, a.w = w, a.sw = sw, a.bias = bias_bf16, a.out = out_bf16;
     a.M = static_cast<int>(rows), a.N = N, a.K = K;
     a.w_global = 1.0f;

@@ -60,6 +60,8 @@ struct GemvArgs {
     float w_global;
     const int32_t* expert_ids;  // nullable: one weight for all rows
     int E, rows_per_x;
+    unsigned int* status;
+    unsigned long long wait_ns;
 };
 
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream);

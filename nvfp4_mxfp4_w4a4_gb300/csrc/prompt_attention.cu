@@ -25,9 +25,8 @@
 // second kernel joins.  Where all units are short, they are dealt out whole.
 //
 // Warps: 0-3 and 4-7 the softmax of the halves (they also write the results), 8
-// goes over the run's units and loads queries, keys and values (TMA), 9 issues the
-// MMAs, 10 looks through values and sees to their loads (11 fills the register
-// group).
+// loads queries, keys and values (TMA), 9 issues the MMAs, 10 looks through values
+// and sees to their loads, 11 goes over the run's units, a few ahead.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -57,8 +56,9 @@ constexpr float kSlack = 8.0f;       // a score this far above its reference mov
 // a row's reference before its first seen key: the lowest float32, which no score lies under
 constexpr float kUnset = -3.402823466e38f;
 // registers per thread: at launch, and dealt out anew to the softmax and the others
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kLaunchRegs * kThreads, "register split");
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 184, kOtherRegs = 128;
+constexpr int kAllRegs = 256 * kSoftmaxRegs + 128 * kOtherRegs;
+static_assert(kAllRegs <= kLaunchRegs * kThreads, "register split");
 
 // What a CTA leaves to the join: whether its run begins within a unit that goes on
 // behind it, and the unit that begins in it and goes on.
@@ -124,6 +124,20 @@ __device__ __forceinline__ void set_registers()
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// The rest of a bounded wait whose first look found the phase incomplete.
+__device__ __forceinline__ bool wait_longer(uint32_t bar, uint32_t parity, unsigned int* status, uint64_t limit_ns)
+{
+    const uint64_t t0 = global_timer_ns();
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity))
+                return true;
+    } while (global_timer_ns() - t0 <= limit_ns);
+    atomicOr(status, kStatusTimeout);
+    return false;
 }
 
 // ---------------------------------------------------------------- the line
@@ -357,7 +371,7 @@ struct alignas(16) Part {
     int token;       // first query of the unit
     int tokens;      // of the sequence from there on
     int first_seen;  // keys seen by that query, before they are clamped to [0, m]
-    int m;
+    int k0, m;       // the sequence's keys
     int key_head, q_head, q_heads;  // the chunk's first query head, and how many
     int slot;        // of the partial results, -1: the part is the whole unit
     int masked;      // first tile in which some row sees not all keys
@@ -394,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int STAGES = C::STAGES, QBUFS = C::QBUFS;
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (by an offset, not a cast of the address: the compiler has to see shared memory)
+    uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* k_full = bars;               // [STAGES] a tile has landed
     uint64_t* k_free = k_full + STAGES;    // [STAGES] both halves' products with it have ended
@@ -438,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(&part_full[i], 1);
-            mbar_init(&part_free[i], 8 + 2);
+            mbar_init(&part_free[i], 8 + 3);
         }
         mbar_init(drained, 1);
         fence_mbar_init();
@@ -459,16 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const uint64_t limit_ns = p.a.wait_ns;
     bool ok = true;
-    // a wait of one thread, and one of a whole warp (quick where the phase is complete:
-    // a serial chain of a few hundred cycles at every wait of the MMA warp is what its
-    // products wait for); once one has run out, the role ends
+    // a wait of one thread, and one of a whole warp (quick where the phase is complete: a
+    // few hundred cycles of serial code at every wait of the MMA warp would be time that
+    // its products wait for); once one has run out, the role ends
     auto wait_one = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && mbar_wait_bounded(bar, parity & 1u, p.a.status, kStatusTimeout, limit_ns);
+        const uint32_t at = smem_u32(bar);
+        if (!mbar_try_wait(at, parity & 1u))
+            ok = ok && wait_longer(at, parity & 1u, p.a.status, limit_ns);
         return ok;
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity & 1u)))
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, p.a.status, kStatusTimeout, limit_ns));
+        const uint32_t at = smem_u32(bar);
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(at, parity & 1u)))
+            ok = __all_sync(0xFFFFFFFFu, ok && wait_longer(at, parity & 1u, p.a.status, limit_ns));
         return ok;
     };
     // the next part's description, or nullptr at the end of the run
@@ -489,19 +507,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) {
         set_registers<kOtherRegs>();
         if (!have) {
-            if (p.may_cut && warp == 8 && lane == 0)
+            if (p.may_cut && warp == 11 && lane == 0)
                 p.cuts[blockIdx.x] = Cut{};
-        } else if (warp == 8) {
-            // ------------------------------- the run; queries, keys and values
+        } else if (warp == 11) {
+            // -------------------------------------------------------- the run
             if (lane == 0) {
                 Run r = *run;
-                bool started = false, more = true;
+                bool started = false;
                 Cut cut = {};
-                uint32_t g = 0, queries[2] = {0, 0};  // tiles, and a half's Q, so far
-                while (ok) {
-                    // the part's description
+                const int group = p.a.q_heads / p.a.kv_heads;
+                while (true) {
                     const uint32_t i = part_count % kParts;
-                    more = r.part(p, started);
+                    const bool more = r.part(p, started);
                     if (!wait_one(&part_free[i], (part_count / kParts) ^ 1u))
                         break;
                     volatile Part& d = parts[i];
@@ -511,18 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const Walk& w = r.w;
-                    const int key_head = w.head / p.chunks, chunk = w.head - key_head * p.chunks;
+                    const int key_head = p.chunks == 1 ? w.head : w.head / p.chunks, chunk = w.head - key_head * p.chunks;
                     const int first = 2 * w.block * p.tokens;
-                    const int group = p.a.q_heads / p.a.kv_heads;
-                    const int q_head = key_head * group + chunk * kHalf;
-                    const int end[2] = {max(r.lo, min(r.hi, w.tiles(p, 0))), max(r.lo, min(r.hi, w.tiles(p, 1)))};
                     d.lo = r.lo, d.hi = r.hi;
-                    d.end[0] = end[0], d.end[1] = end[1];
+                    d.end[0] = max(r.lo, min(r.hi, w.tiles(p, 0)));
+                    d.end[1] = max(r.lo, min(r.hi, w.tiles(p, 1)));
                     d.token = w.q0 + first;
                     d.tokens = w.n - first;
                     d.first_seen = p.a.causal ? first + 1 + w.m - w.n : w.m;
-                    d.m = w.m;
-                    d.key_head = key_head, d.q_head = q_head;
+                    d.k0 = w.k0, d.m = w.m;
+                    d.key_head = key_head, d.q_head = key_head * group + chunk * kHalf;
                     d.q_heads = min(p.heads, group - chunk * kHalf);
                     d.slot = r.lo == 0 && r.hi == r.tiles ? -1 : r.lo > 0 ? 0 : 1;
                     d.masked = w.limit(p, first) / kTile;
@@ -534,57 +549,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             cut.open = 1, cut.b = w.b, cut.head = w.head, cut.block = w.block;
                     }
-                    // its tiles; the queries behind the first keys, whose place is free earlier
-                    for (int j = r.lo; ok && j < r.hi; ++j, ++g) {
-                        const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1u;
-                        const int at = w.k0 + j * kTile;
-                        if (!wait_one(&k_free[slot], phase ^ 1u))
-                            break;
+                }
+                if (p.may_cut)
+                    p.cuts[blockIdx.x] = cut;
+            }
+        } else if (warp == 8) {
+            // ------------------------------------------ queries, keys and values
+            uint32_t g = 0, queries[2] = {0, 0};  // tiles, and a half's Q, so far
+            auto landed = [&](uint64_t* bar, uint32_t parity) { wait_longer(smem_u32(bar), parity, p.a.status, limit_ns); };
+            while (volatile Part* d = next_part()) {
+                const int lo = d->lo, hi = d->hi, key_head = d->key_head, q_head = d->q_head, token = d->token, k0 = d->k0;
+                const int end[2] = {d->end[0], d->end[1]};
+                for (int j = lo; ok && j < hi; ++j, ++g) {
+                    const uint32_t slot = g % STAGES, phase = (g / STAGES) & 1u;
+                    if (!wait(&k_free[slot], phase ^ 1u))
+                        break;
+                    if (elect_one()) {
                         mbar_arrive_expect_tx(&k_full[slot], C::TILE);
 #pragma unroll
                         for (int s = 0; s < C::SLABS; ++s)
-                            tma_load_3d(smem + C::OFF_K + slot * C::TILE + s * kSlab, &k_map, &k_full[slot], s * 64, at, key_head);
-                        if (j == r.lo) {
+                            tma_load_3d(smem + C::OFF_K + slot * C::TILE + s * kSlab, &k_map, &k_full[slot], s * 64,
+                                        k0 + j * kTile, key_head);
+                    }
+                    __syncwarp();
+                    if (j == lo) {  // (the queries behind the first keys, whose place is free earlier)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                if (end[h] == r.lo)
-                                    continue;
-                                const uint32_t buf = (queries[h] % QBUFS) * 2 + h;
-                                if (!wait_one(&q_free[buf], (queries[h] / QBUFS) ^ 1u))
-                                    break;
-                                ++queries[h];
+                        for (int h = 0; h < 2; ++h) {
+                            if (end[h] == lo)
+                                continue;
+                            const uint32_t buf = (queries[h] % QBUFS) * 2 + h;
+                            if (!wait(&q_free[buf], (queries[h] / QBUFS) ^ 1u))
+                                break;
+                            ++queries[h];
+                            if (elect_one()) {
                                 mbar_arrive_expect_tx(&q_full[buf], p.tokens * p.heads * kDim * 2);
 #pragma unroll
                                 for (int s = 0; s < C::SLABS; ++s)
                                     tma_load_3d(smem + buf * C::TILE + s * kSlab, &q_map, &q_full[buf], s * 64, q_head,
-                                                w.q0 + first + h * p.tokens);
+                                                token + h * p.tokens);
                             }
+                            __syncwarp();
                         }
-                        if (!wait_one(&v_free[slot], phase ^ 1u)) {
-                            mbar_wait_bounded(&k_full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
-                            break;
-                        }
+                    }
+                    if (!ok || !wait(&v_free[slot], phase ^ 1u)) {
+                        landed(&k_full[slot], phase);
+                        break;
+                    }
+                    if (elect_one()) {
                         mbar_arrive_expect_tx(&v_full[slot], C::TILE);
 #pragma unroll
                         for (int s = 0; s < C::SLABS; ++s)
-                            tma_load_3d(smem + C::OFF_V + slot * C::TILE + s * kSlab, &v_map, &v_full[slot], s * 64, at, key_head);
+                            tma_load_3d(smem + C::OFF_V + slot * C::TILE + s * kSlab, &v_map, &v_full[slot], s * 64,
+                                        k0 + j * kTile, key_head);
                     }
+                    __syncwarp();
                 }
-                if (p.may_cut)
-                    p.cuts[blockIdx.x] = cut;
-                // nothing of this CTA may be in flight when it ends
-                for (uint32_t i = 1; i <= STAGES && i <= g; ++i) {
-                    const uint32_t slot = (g - i) % STAGES, phase = ((g - i) / STAGES) & 1u;
-                    mbar_wait_bounded(&k_full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
-                    mbar_wait_bounded(&v_full[slot], phase, p.a.status, kStatusTimeout, limit_ns);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    for (uint32_t i = 1; i <= QBUFS && i <= queries[h]; ++i) {
-                        const uint32_t use = queries[h] - i;
-                        mbar_wait_bounded(&q_full[(use % QBUFS) * 2 + h], (use / QBUFS) & 1u, p.a.status, kStatusTimeout, limit_ns);
-                    }
+                if (!ok)
+                    break;
+                part_done();
             }
+            // nothing of this CTA may be in flight when it ends
+            for (uint32_t i = 1; i <= STAGES && i <= g; ++i) {
+                const uint32_t slot = (g - i) % STAGES, phase = ((g - i) / STAGES) & 1u;
+                landed(&k_full[slot], phase);
+                landed(&v_full[slot], phase);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                for (uint32_t i = 1; i <= QBUFS && i <= queries[h]; ++i) {
+                    const uint32_t use = queries[h] - i;
+                    landed(&q_full[(use % QBUFS) * 2 + h], (use / QBUFS) & 1u);
+                }
         } else if (warp == 9) {
             // ------------------------------------------------------------ MMAs
             // (the whole warp walks the loop and one elected lane issues: the operands
@@ -683,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one())
                 tc_commit(drained);
             __syncwarp();
-            mbar_wait_bounded(drained, 0, p.a.status, kStatusTimeout, limit_ns);
+            wait_longer(smem_u32(drained), 0, p.a.status, limit_ns);
         } else if (warp == 10) {
             // -------------- what the second product of a tile needs beside P
             // its values, looked through where the tile is masked, and the next tile's keys:
@@ -799,21 +834,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_all(&s_full[h], turns))
                     break;
                 ++turns;
-                float s[kTile], mx[4];
+                // the tile's maximum: a by-product of reading it, but for what is masked.  Half
+                // of the scores stay in registers, the others are read again (all 128 would
+                // take code of 128 columns for everything, which the instruction cache has to
+                // bring in for every few tiles of a short prompt)
+                float s[64], top;
+                const int seen = limit - j * kTile;
+                const bool masked = (j + 1) * kTile > free_keys;
+                if (masked) {
+                    top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 32) {
+                        tmem_ld_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s));
+                        tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32)
-                    mx[c / 32] = tmem_ld_max_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s + c));
-                tmem_ld_wait();
-                if ((j + 1) * kTile > free_keys) {
-                    const int seen = limit - j * kTile;
-                    mx[0] = mx[1] = mx[2] = mx[3] = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kTile; ++c) {
-                        s[c] = c < seen ? s[c] : -INFINITY;
-                        mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                        for (int k = 0; k < 32; ++k)
+                            top = k < seen - c ? fmaxf(top, s[k]) : top;
                     }
+                    tmem_ld_32x32b_x32(s_addr, reinterpret_cast<uint32_t*>(s));
+                    tmem_ld_32x32b_x32(s_addr + 32, reinterpret_cast<uint32_t*>(s + 32));
+                    tmem_ld_wait();
+                } else {
+                    float mx[4];
+                    mx[2] = tmem_ld_max_32x32b_x32(s_addr + 64, reinterpret_cast<uint32_t*>(s));
+                    mx[3] = tmem_ld_max_32x32b_x32(s_addr + 96, reinterpret_cast<uint32_t*>(s + 32));
+                    mx[0] = tmem_ld_max_32x32b_x32(s_addr, reinterpret_cast<uint32_t*>(s));
+                    mx[1] = tmem_ld_max_32x32b_x32(s_addr + 32, reinterpret_cast<uint32_t*>(s + 32));
+                    tmem_ld_wait();
+                    top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.xscale;
+                top *= p.xscale;
                 if (__any_sync(0xFFFFFFFFu, live && top > m + kSlack)) {
                     const float next = fmaxf(m, top);
                     const float factor = exp2_approx(m - next);
@@ -835,20 +885,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float minus = -m;
                 // half of the keys after the other: the MMAs begin with the first
-#pragma unroll
+                float2 more = make_float2(0.0f, 0.0f);
+#pragma unroll 1
                 for (int c = 0; c < kTile; c += 64) {
                     uint32_t w[32];
-                    if (c > 0) {  // (keeps the compiler from weighing these before the others are handed over)
+                    if (masked) {
 #pragma unroll
-                        for (int k = c; k < c + 64; ++k)
-                            asm volatile("" : "+f"(s[k]));
+                        for (int k = 0; k < 64; ++k)
+                            s[k] = k < seen - c ? s[k] : -INFINITY;
                     }
 #pragma unroll
-                    for (int k = c; k < c + 64; k += 2) {
-                        fma_pair(s + k, s[k], s[k + 1], xs, minus);
-                        s[k] = exp2_approx(s[k]);
-                        s[k + 1] = exp2_approx(s[k + 1]);
-                        w[(k - c) / 2] = pack2(s[k], s[k + 1]);
+                    for (int q = 0; q < 64; q += 32) {
+#pragma unroll
+                        for (int k = q; k < q + 32; k += 2) {
+                            float x[2];
+                            fma_pair(x, s[k], s[k + 1], xs, minus);
+                            x[0] = exp2_approx(x[0]);
+                            x[1] = exp2_approx(x[1]);
+                            if (k & 2)
+                                more = add_pair(more, x[0], x[1]);
+                            else
+                                l = add_pair(l, x[0], x[1]);
+                            w[k / 2] = pack2(x[0], x[1]);
+                        }
+                        if (c == 0)
+                            tmem_ld_32x32b_x32(s_addr + 64 + q, reinterpret_cast<uint32_t*>(s + q));
                     }
                     tmem_st_32x32b_x32(s_addr + c / 2, w);
                     tmem_st_wait();
@@ -856,13 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(c == 0 ? &p_half[h] : &p_full[h]);
-                }
-                // (the sum while the MMAs run)
-                float2 more = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int k = 0; k < kTile; k += 4) {
-                    l = add_pair(l, s[k], s[k + 1]);
-                    more = add_pair(more, s[k + 2], s[k + 3]);
+                    tmem_ld_wait();
                 }
                 l = add_pair(l, more.x, more.y);
             }
@@ -872,74 +927,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_all(&o_full[h], uses);
                 ++uses;
             }
-            if (ok)
-                wait_all(&bad_full[part_count & 1u], part_count >> 1);
-            if (!ok)
+            if (!ok || !wait(&bad_full[part_count & 1u], part_count >> 1))
                 break;
-            const int slot = d->slot;
             const int* bad = any_bad[part_count & 1u] ? reinterpret_cast<const int*>(smem + C::OFF_BAD) + (part_count & 1u) * 3 * kDim : nullptr;
+            const int slot = d->slot;
             const float sum = l.x + l.y;
             const float scale = slot >= 0 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             const int64_t token = d->token + static_cast<int64_t>(tok);
             const int hq = d->q_head + head;
             const int64_t out_row = live ? token * p.a.ot + hq * p.a.oh : -1;
             const int64_t part_half = (2 * static_cast<int64_t>(blockIdx.x) + slot) * 2 + h;
+            uint8_t* mine = smem + C::OFF_OUT + warp * 2048;
 #pragma unroll 1
-            for (int c = 0; c < kDim; c += 32) {
-                float x[32];
-                if (some) {
-                    tmem_ld_32x32b_x32(o_addr + c, reinterpret_cast<uint32_t*>(x));
-                    tmem_ld_wait();
-                } else {
+                                for (int c = 0; c < kDim; c += 32) {
+                                    float x[32];
+                                    if (some) {
+                                        tmem_ld_32x32b_x32(o_addr + c, reinterpret_cast<uint32_t*>(x));
+                                        tmem_ld_wait();
+                                    } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        x[k] = 0.0f;
-                }
+                                        for (int k = 0; k < 32; ++k)
+                                            x[k] = 0.0f;
+                                    }
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    x[k] *= scale;
-                if (bad != nullptr) {
+                                    for (int k = 0; k < 32; ++k)
+                                        x[k] *= scale;
+                                    if (bad != nullptr) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float add = 0.0f;
-                        if (bad[c + k] < limit)
-                            add += INFINITY;
-                        if (bad[kDim + c + k] < limit)
-                            add -= INFINITY;
-                        if (bad[2 * kDim + c + k] < limit)
-                            add = __uint_as_float(0x7FC00000u);
-                        x[k] += add;
-                    }
-                }
-                if (slot < 0) {
-                    // by way of shared memory, so that four lanes write 64 bytes of a row
-                    uint8_t* mine = smem + C::OFF_OUT + warp * 2048;
+                                        for (int k = 0; k < 32; ++k) {
+                                            float add = 0.0f;
+                                            if (bad[c + k] < limit)
+                                                add += INFINITY;
+                                            if (bad[kDim + c + k] < limit)
+                                                add -= INFINITY;
+                                            if (bad[2 * kDim + c + k] < limit)
+                                                add = __uint_as_float(0x7FC00000u);
+                                            x[k] += add;
+                                        }
+                                    }
+                                    if (slot < 0) {
+                                        // by way of shared memory, so that four lanes write 64 bytes of a row
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4*>(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8(x + 8 * k);
-                    __syncwarp();
+                                        for (int k = 0; k < 4; ++k)
+                                            *reinterpret_cast<uint4*>(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8(x + 8 * k);
+                                        __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int from = k * 8 + (lane >> 2);  // lane of the row
-                        const int64_t dst = __shfl_sync(0xFFFFFFFFu, out_row, from);
-                        const uint4 v = *reinterpret_cast<const uint4*>(mine + from * 64 + (((lane & 3) ^ ((from >> 1) & 3)) << 4));
-                        if (dst >= 0)
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + dst + c + (lane & 3) * 8) = v;
-                    }
-                    __syncwarp();
-                } else if (live) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o) + (part_half * (kDim / 4) + c / 4) * kHalf + row;
+                                        for (int k = 0; k < 4; ++k) {
+                                            const int from = k * 8 + (lane >> 2);  // lane of the row
+                                            const int64_t dst = __shfl_sync(0xFFFFFFFFu, out_row, from);
+                                            const uint4 v = *reinterpret_cast<const uint4*>(mine + from * 64 + (((lane & 3) ^ ((from >> 1) & 3)) << 4));
+                                            if (dst >= 0)
+                                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + dst + c + (lane & 3) * 8) = v;
+                                        }
+                                        __syncwarp();
+                                    } else if (live) {
+                                        float4* dst = reinterpret_cast<float4*>(p.part_o) + (part_half * (kDim / 4) + c / 4) * kHalf + row;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        dst[k * kHalf] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-                }
-            }
-            if (live) {
-                if (slot >= 0)
-                    p.part_ml[part_half * kHalf + row] = make_float2(m, sum);
-                else if (p.a.lse != nullptr)
-                    p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
-            }
+                                        for (int k = 0; k < 8; ++k)
+                                            dst[k * kHalf] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                                    }
+                                }
+                                if (live) {
+                                    if (slot >= 0)
+                                        p.part_ml[part_half * kHalf + row] = make_float2(m, sum);
+                                    else if (p.a.lse != nullptr)
+                                        p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+                                }
             // O, and what was found in the values, may be written again
             tc_fence_before_sync();
             __syncwarp();
@@ -1055,7 +1108,7 @@ cudaError_t launch(const PromptParams& p, cudaStream_t stream)
             err = cudaFuncGetAttributes(&fa, prompt_attention_kernel<kDim>);
             if (err != cudaSuccess)
                 return err;
-            if (fa.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs)
+            if (fa.numRegs * kThreads < kAllRegs)
                 return cudaErrorInvalidConfiguration;
             configured[dev] = ctx;
         }
