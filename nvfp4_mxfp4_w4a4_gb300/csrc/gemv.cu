@@ -50,8 +50,7 @@ constexpr int kChunks = 8;              // of a stage
 constexpr int kGroups = 2;              // of warps, which take the stages in turns
 constexpr int kWarps = kGroups * kChunks;  // that multiply
 constexpr int kStageK = kChunks * kChunk;
-constexpr int kLoaders = kStageK / 256; // warps that load, a slab of a stage each
-constexpr int kThreads = (kWarps + kLoaders + 1) * 32;  // and one that adds up
+constexpr int kThreads = (kWarps + 2) * 32;  // and one that loads, one that adds up
 constexpr int kSetRows = 32;
 constexpr int kMostStages = 12;
 constexpr int kMaxSmem = 224 * 1024;
@@ -63,6 +62,7 @@ struct GemvParams {
     int chunks;  // of K
     int sets;    // of a weight's rows
     int stages;
+    bool slabs;  // the map's third dimension: K is whole slabs, a stage is one copy
     int per;     // sets of a CTA (of all rows' weights with experts)
     int64_t all;
 };
@@ -141,19 +141,23 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t w)
 struct Place {
     int row, set;
     int x_row;   // first row of x
-    int expert;  // -1: none
+    int id;      // expert, not checked
 
     __device__ __forceinline__ void find(const GemvParams& p, int64_t v)
     {
         const bool experts = p.a.expert_ids != nullptr;
         row = experts ? static_cast<int>(v / p.sets) : 0;
         set = static_cast<int>(v - static_cast<int64_t>(row) * p.sets);
-        expert = x_row = 0;
+        id = x_row = 0;
         if (experts) {
             x_row = row / p.a.rows_per_x;
-            expert = __ldg(p.a.expert_ids + row);
-            expert = expert >= 0 && expert < p.a.E ? expert : -1;
+            id = __ldg(p.a.expert_ids + row);
         }
+    }
+    // (-1: none)
+    __device__ __forceinline__ int expert(const GemvParams& p) const
+    {
+        return p.a.expert_ids == nullptr || (id >= 0 && id < p.a.E) ? id : -1;
     }
     __device__ __forceinline__ void next(const GemvParams& p, int64_t v)
     {
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     __half* xs = reinterpret_cast<__half*>(taken + 2);                      // [tokens][pitch]
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&full[i], kLoaders);
+            mbar_init(&full[i], 1);
             mbar_init(&free_[i], kChunks);
         }
         for (int i = 0; i < 2; ++i) {
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     if (first >= end)
         return;
 
-    if (warp == kWarps + kLoaders) {
+    if (warp == kWarps + 1) {
         // ------------------------------------------------------------ results
         // the warps' sums of a set, in their order, while the next set is multiplied
         Place at;
@@ -227,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 return;
             const int n = at.set * kSetRows + lane;
             float bias = 0.0f;
-            if (a.bias != nullptr && at.expert >= 0 && n < N)
-                bias = __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[at.expert * a.N + n]);
+            if (a.bias != nullptr && at.expert(p) >= 0 && n < N)
+                bias = __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[at.expert(p) * a.N + n]);
             for (int t = 0; t < tokens; ++t) {
                 float sum = 0.0f;
 #pragma unroll
@@ -243,39 +247,37 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
         }
         return;
     }
-    if (warp >= kWarps) {
+    if (warp == kWarps) {
         // ------------------------------------------------------------ weights
         if (lane == 0) {
-            const int slab = warp - kWarps;
             Place at;
             at.find(p, first);
             Turn turn;
             uint32_t issued = 0;
             bool ok = true;
             for (int64_t v = first; ok && v < end; at.next(p, ++v)) {
-                if (at.expert < 0)
+                const int expert = at.expert(p);
+                if (expert < 0)
                     continue;
                 // (rows past the last are zeros, or the next expert's: they are not written)
-                const int row0 = static_cast<int>(at.expert * a.N) + at.set * kSetRows;
-                const uint8_t* scales = a.sw + at.expert * p.expert_scales + static_cast<int64_t>(at.set >> 2) * p.kb4 * 512;
+                const int row0 = static_cast<int>(expert * a.N) + at.set * kSetRows;
+                const uint8_t* scales = a.sw + expert * p.expert_scales + static_cast<int64_t>(at.set >> 2) * p.kb4 * 512;
                 for (int step = 0; step < steps; ++step, turn.next(p.stages), ++issued) {
-                    const uint32_t slot = turn.slot;
-                    ok = mbar_wait_bounded(&free_[slot], turn.phase ^ 1u, a.status, kStatusTimeout, a.wait_ns);
+                    ok = mbar_wait_bounded(&free_[turn.slot], turn.phase ^ 1u, a.status, kStatusTimeout, a.wait_ns);
                     if (!ok)
                         break;
-                    // the slab, and its two chunks' scales
-                    uint8_t* to = ring + slot * BYTES;
-                    const int k0 = step * kStageK + slab * 256;
-                    if (k0 >= K) {
-                        mbar_arrive(&full[slot]);
-                        continue;
+                    uint8_t* to = ring + turn.slot * BYTES;
+                    uint64_t* bar = &full[turn.slot];
+                    const uint32_t bytes = min(kChunks * RUN, p.kb4 * 512 - step * (kChunks * RUN));
+                    const int slabs = p.slabs ? kStageK / 256 : min(kStageK / 256, (K - step * kStageK + 255) / 256);
+                    mbar_arrive_expect_tx(bar, slabs * kSlab + bytes);
+                    if (p.slabs) {
+                        tma_load_3d(to, &w_map, bar, 0, row0, step * (kStageK / 256));
+                    } else {
+                        for (int i = 0; i < slabs; ++i)
+                            tma_load_2d(to + i * kSlab, &w_map, bar, step * (kStageK / 2) + i * 128, row0);
                     }
-                    constexpr int RUNS = 2 * RUN / 512;
-                    const int run0 = (step * kLoaders + slab) * RUNS;
-                    const uint32_t bytes = min(RUNS, p.kb4 - run0) * 512;
-                    mbar_arrive_expect_tx(&full[slot], kSlab + bytes);
-                    tma_load_2d(to + slab * kSlab, &w_map, &full[slot], k0 / 2, row0);
-                    bulk_load(to + kCodeBytes + slab * 2 * RUN, scales + static_cast<int64_t>(run0) * 512, bytes, &full[slot]);
+                    bulk_load(to + kCodeBytes, scales + static_cast<int64_t>(step) * (kChunks * RUN), bytes, bar);
                 }
             }
             // (every copy is waited for by the warps that multiply, unless they gave up)
@@ -347,8 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
             }
             named_barrier_sync(1, kWarps * 32);
         }
+        const bool live_set = at.expert(p) >= 0;
         float acc[4][2] = {};  // rows g + 8 q, tokens 2 j and 2 j + 1 (of 1 or 2: both, of the lane's blocks)
-        for (int step = 0; ok && at.expert >= 0 && step < steps; ++step, turn.next(p.stages), odd ^= 1u) {
+        for (int step = 0; ok && live_set && step < steps; ++step, turn.next(p.stages), odd ^= 1u) {
             if (odd != static_cast<uint32_t>(group))
                 continue;
             const uint32_t slot = turn.slot;
@@ -477,6 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
             for (int t = 0; t < 2; ++t) {
                 float sum = acc[q][t];
                 if constexpr (!kWide) {
+                    if (t >= tokens)
+                        continue;
                     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
                     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
                     if (j == t)
@@ -528,9 +533,12 @@ cudaError_t launch(const GemvParams& p, int tokens, cudaStream_t stream)
     q.stages = static_cast<int>(std::min<int64_t>({static_cast<int64_t>((kMaxSmem - fixed) / stage), kMostStages, steps}));
     if (fixed + 2 * stage > kMaxSmem || q.stages < 1)
         return cudaErrorInvalidValue;
-    // (make_operand_map's bytes: rows of K / 2 of all the weights)
+    // (make_operand_map's bytes: rows of K / 2 of all the weights.  A copy costs its issue, some
+    // 300 cycles: with K % 256 == 0 a stage is one copy of four slabs, else four)
     CUtensorMap w_map;
-    if (!make_operand_map(&w_map, p.a.w, p.a.N * (p.a.expert_ids != nullptr ? p.a.E : 1), p.a.K / 2, kSetRows, 1, kOpBytes))
+    q.slabs = p.a.K % 256 == 0;
+    if (!make_operand_map(&w_map, p.a.w, p.a.N * (p.a.expert_ids != nullptr ? p.a.E : 1), p.a.K / 2, kSetRows,
+                          q.slabs ? kStageK / 256 : 1, kOpBytes))
         return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>((q.all + q.per - 1) / q.per);
     return launch_pdl(kern, dim3(grid), dim3(kThreads), fixed + q.stages * stage, stream, q, w_map);
