@@ -50,7 +50,8 @@ constexpr int kChunks = 8;              // of a stage
 constexpr int kGroups = 2;              // of warps, which take the stages in turns
 constexpr int kWarps = kGroups * kChunks;  // that multiply
 constexpr int kStageK = kChunks * kChunk;
-constexpr int kThreads = (kWarps + 2) * 32;  // and one that loads, one that adds up
+constexpr int kLoaders = 2;             // that load, stages in turns too
+constexpr int kThreads = (kWarps + kLoaders + 1) * 32;  // and one that adds up
 constexpr int kSetRows = 32;
 constexpr int kMostStages = 12;
 constexpr int kMaxSmem = 224 * 1024;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     if (first >= end)
         return;
 
-    if (warp == kWarps + 1) {
+    if (warp == kWarps + kLoaders) {
         // ------------------------------------------------------------ results
         // the warps' sums of a set, in their order, while the next set is multiplied
         Place at;
@@ -247,13 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
         }
         return;
     }
-    if (warp == kWarps) {
+    if (warp >= kWarps) {
         // ------------------------------------------------------------ weights
         if (lane == 0) {
             Place at;
             at.find(p, first);
             Turn turn;
-            uint32_t issued = 0;
+            uint32_t issued = 0;  // of all stages
+            const uint32_t mine = warp - kWarps;
             bool ok = true;
             for (int64_t v = first; ok && v < end; at.next(p, ++v)) {
                 const int expert = at.expert(p);
@@ -263,6 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 const int row0 = static_cast<int>(expert * a.N) + at.set * kSetRows;
                 const uint8_t* scales = a.sw + expert * p.expert_scales + static_cast<int64_t>(at.set >> 2) * p.kb4 * 512;
                 for (int step = 0; step < steps; ++step, turn.next(p.stages), ++issued) {
+                    if ((issued & (kLoaders - 1)) != mine)
+                        continue;
                     ok = mbar_wait_bounded(&free_[turn.slot], turn.phase ^ 1u, a.status, kStatusTimeout, a.wait_ns);
                     if (!ok)
                         break;
@@ -285,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 if (turn.slot == 0)
                     turn.slot = p.stages, turn.phase ^= 1u;
                 --turn.slot;
-                mbar_wait_bounded(&full[turn.slot], turn.phase, a.status, kStatusTimeout, a.wait_ns);
+                if (((issued - 1 - i) & (kLoaders - 1)) == mine)
+                    mbar_wait_bounded(&full[turn.slot], turn.phase, a.status, kStatusTimeout, a.wait_ns);
             }
         }
         return;
@@ -309,43 +314,54 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     const uint32_t b_step = reads ? kChunk * 2 : 0, b_block = reads ? 64 : 0;
     for (int64_t v = first; ok && v < end; at.next(p, ++v), ++sets) {
         if (at.x_row != x_row) {
-            // activations: four lanes a block of 32 (whole warps go round: their lanes exchange)
+            // activations: a lane has 8 elements of every token, four lanes a block of 32 (whole
+            // warps go round: their lanes exchange)
             if (x_row >= 0)
                 named_barrier_sync(1, kWarps * 32);
             x_row = at.x_row;
             const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + static_cast<int64_t>(x_row) * K;
-            for (int t = 0; t < tokens; ++t)
             for (int k0 = warp * 256; k0 < padded; k0 += kWarps * 256) {
                 const int k = k0 + lane * 8;
-                const bool live = k < padded;
-                uint4 q = make_uint4(0, 0, 0, 0);
-                if (live && k < K)
-                    q = __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * K + k));
-                float f[8];
-                unpack8(q, f);
-                uint32_t top = 0;
+                uint4 q[TOK];
 #pragma unroll
-                for (int n = 0; n < 8; ++n)
-                    top = max(top, __float_as_uint(f[n]) & 0x7FFFFFFFu);
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                const uint32_t e = max(top >> 23, 15u);
-                const bool finite = e < 255u;
-                const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - e)
-                uint32_t h[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    float lo = f[2 * n], hi = f[2 * n + 1];
-                    // (beside NaN or Inf the finite ones do not matter)
-                    lo = finite ? lo * up : (isfinite(lo) ? 0.0f : lo);
-                    hi = finite ? hi * up : (isfinite(hi) ? 0.0f : hi);
-                    const __half2 v2 = __floats2half2_rn(lo, hi);
-                    h[n] = *reinterpret_cast<const uint32_t*>(&v2);
+                for (int t = 0; t < TOK; ++t) {
+                    q[t] = make_uint4(0, 0, 0, 0);
+                    if (t < tokens && k < K)
+                        q[t] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * K + k));
                 }
-                if (live)
-                    *reinterpret_cast<uint4*>(xs + t * pitch + k) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (live && j == 0)
-                    xscale[(k / 32) * TOK + t] = finite ? __uint_as_float((e - 14u) << 23) : 1.0f;
+#pragma unroll
+                for (int t = 0; t < TOK; ++t) {
+                    if (t >= tokens)
+                        break;
+                    const uint32_t w[4] = {q[t].x, q[t].y, q[t].z, q[t].w};
+                    // (the largest magnitude as bits: NaN and Inf come out on top)
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        top = max(top, max(w[n] & 0x7FFFu, (w[n] >> 16) & 0x7FFFu));
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    const uint32_t e = max(top >> 7, 15u);
+                    const bool finite = e < 255u;
+                    const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - e)
+                    uint32_t h[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        float lo = bf_lo(w[n]), hi = bf_hi(w[n]);
+                        if (finite) {
+                            lo *= up, hi *= up;
+                        } else {  // (beside NaN or Inf the finite ones do not matter)
+                            lo = isfinite(lo) ? 0.0f : lo, hi = isfinite(hi) ? 0.0f : hi;
+                        }
+                        const __half2 v2 = __floats2half2_rn(lo, hi);
+                        h[n] = *reinterpret_cast<const uint32_t*>(&v2);
+                    }
+                    if (k < padded) {
+                        *reinterpret_cast<uint4*>(xs + t * pitch + k) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if (j == 0)
+                            xscale[(k / 32) * TOK + t] = finite ? __uint_as_float((e - 14u) << 23) : 1.0f;
+                    }
+                }
             }
             named_barrier_sync(1, kWarps * 32);
         }
