@@ -11,7 +11,12 @@ once.
 A step's tokens are the drafted tokens of each sequence (one per sequence for
 plain decoding, a chain or a tree of them otherwise): their keys and values are
 appended to the cache at `slots` and then attended together with the context.
-Everything is enqueued on the current CUDA stream; nothing synchronizes.
+Whole prompts of any length go through
+
+    out = block.prompt(x, positions, slots, q_offsets)
+
+which attends their own keys and values in bf16, as they come from the projection,
+and leaves them in the cache for the steps to come.  Everything is enqueued on the current CUDA stream; nothing synchronizes.
 """
 from __future__ import annotations
 
@@ -72,15 +77,22 @@ class AttentionBlock:
     [hidden, q_heads head_dim]; cache: allocate_cache(...); rope: fp4lin.rope_params.
     max_draft and max_seq_len choose the attention kernel and the cut of the
     contexts: a block for pieces of a prompt decodes single tokens slower than one
-    made for them, which may share its cache, weights and rope."""
+    made for them, which may share its cache, weights and rope.
+    q_norm, k_norm (both or neither): bf16 [head_dim], the weights of a norm of every
+    head of the queries and keys before the rotation; head_dim 64 or 128.
+    prompts: allocate what prompt() needs."""
 
     def __init__(self, qkv: Fp8Linear, o: Fp8Linear, cache: L.kv_cache, rope: L.rope_params, q_heads: int,
-                 max_tokens: int, max_batch: int, max_seq_len: int, max_draft: int):
+                 max_tokens: int, max_batch: int, max_seq_len: int, max_draft: int, q_norm: torch.Tensor | None = None,
+                 k_norm: torch.Tensor | None = None, norm_eps: float = 1e-6, prompts: bool = False):
         c = cache.struct
         self.qkv, self.o, self.cache, self.rope = qkv, o, cache, rope
         self.q_heads, self.kv_heads, self.head_dim = q_heads, c.kv_heads, c.head_dim
         if qkv.N != (q_heads + 2 * c.kv_heads) * c.head_dim or o.K != q_heads * c.head_dim:
             raise ValueError("the projections do not fit the heads")
+        if (q_norm is None) != (k_norm is None):
+            raise ValueError("q_norm and k_norm: both or neither")
+        self.q_norm, self.k_norm, self.norm_eps = q_norm, k_norm, norm_eps
         self.max_tokens, self.max_batch = max_tokens, max_batch
         self.max_seq_len, self.max_draft = max_seq_len, max_draft
         self.projected = torch.empty((max_tokens, qkv.N), dtype=torch.bfloat16, device="cuda")
@@ -92,6 +104,17 @@ class AttentionBlock:
         attention = max(L.fp4_kv_attention_workspace_size(b, min(max_tokens, b * max_draft), q_heads, c.kv_heads, c.head_dim,
                                                           max_seq_len, max_draft) for b in range(1, max_batch + 1))
         self.attention_ws = torch.empty(max(attention, 1), dtype=torch.uint8, device="cuda")
+        self.prompt_ws = None
+        if prompts:
+            need = L.fp4_prompt_attention_workspace_size(max_batch, max_tokens, max_tokens, q_heads, c.kv_heads, c.head_dim)
+            self.prompt_ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+
+    def _project(self, x):
+        """The queries, keys and values of x, slices of one buffer."""
+        T, hq, hkv, d = x.shape[0], self.q_heads, self.kv_heads, self.head_dim
+        qkv = self.qkv(x, self.projected[:T], self.linear_ws)
+        return (qkv[:, :hq * d].unflatten(1, (hq, d)), qkv[:, hq * d:(hq + hkv) * d].unflatten(1, (hkv, d)),
+                qkv[:, (hq + hkv) * d:].unflatten(1, (hkv, d)))
 
     def step(self, x, positions, slots, block_table, context_lens, q_offsets, tree_mask=None):
         """x: bf16 [tokens, hidden]; positions: int32 [tokens]; slots: int64
@@ -101,18 +124,41 @@ class AttentionBlock:
         Returns bf16 [tokens, hidden], a view of a buffer that the next step reuses.
         More than max_draft tokens of one sequence are an error: where the sum over
         the sequences shows it, a ValueError, otherwise NaN in the rows past the bound."""
-        T, hq, hkv, d = x.shape[0], self.q_heads, self.kv_heads, self.head_dim
+        T = x.shape[0]
         if T > self.max_tokens or block_table.shape[0] > self.max_batch:
             raise ValueError("more tokens or sequences than the block was made for")
         if T > block_table.shape[0] * self.max_draft:
             raise ValueError("more tokens than max_draft for each sequence")
-        qkv = self.qkv(x, self.projected[:T], self.linear_ws)
-        q = qkv[:, :hq * d].unflatten(1, (hq, d))
-        k = qkv[:, hq * d:(hq + hkv) * d].unflatten(1, (hkv, d))
-        v = qkv[:, (hq + hkv) * d:].unflatten(1, (hkv, d))
-        L.fp4_rope(q, q, positions, self.rope)
-        L.fp4_kv_append(self.cache, k, v, slots, rope=self.rope, positions=positions)
+        q, k, v = self._project(x)
+        if self.q_norm is None:
+            L.fp4_rope(q, q, positions, self.rope)
+            L.fp4_kv_append(self.cache, k, v, slots, rope=self.rope, positions=positions)
+        else:
+            L.fp4_qk_norm_rope(q, k, q, k, self.q_norm, self.k_norm, self.norm_eps, positions, self.rope)
+            L.fp4_kv_append(self.cache, k, v, slots)
         a = self.attended[:T]
-        L.fp4_kv_attention(self.cache, q, a.unflatten(1, (hq, d)), block_table, context_lens, q_offsets, self.max_seq_len,
-                           self.max_draft, self.attention_ws, tree_mask=tree_mask)
+        L.fp4_kv_attention(self.cache, q, a.unflatten(1, (self.q_heads, self.head_dim)), block_table, context_lens, q_offsets,
+                           self.max_seq_len, self.max_draft, self.attention_ws, tree_mask=tree_mask)
+        return self.o(a, self.out[:T], self.linear_ws)
+
+    def prompt(self, x, positions, slots, q_offsets):
+        """Whole prompts, packed: x: bf16 [tokens, hidden]; positions: int32 [tokens];
+        slots: int64 [tokens]; q_offsets: int32 [batch + 1], ascending from 0 to tokens.
+        Every token sees its sequence up to itself.  The keys are rotated (and normed)
+        to bf16, attended as such, and quantized into the cache from there.
+        Returns bf16 [tokens, hidden], a view of a buffer that the next call reuses."""
+        T = x.shape[0]
+        if self.prompt_ws is None:
+            raise ValueError("the block was not made for prompts")
+        if T > self.max_tokens or q_offsets.numel() - 1 > self.max_batch:
+            raise ValueError("more tokens or sequences than the block was made for")
+        q, k, v = self._project(x)
+        if self.q_norm is None:
+            L.fp4_rope(q, q, positions, self.rope)
+            L.fp4_rope(k, k, positions, self.rope)
+        else:
+            L.fp4_qk_norm_rope(q, k, q, k, self.q_norm, self.k_norm, self.norm_eps, positions, self.rope)
+        L.fp4_kv_append(self.cache, k, v, slots)
+        a = self.attended[:T]
+        L.fp4_prompt_attention(q, k, v, a.unflatten(1, (self.q_heads, self.head_dim)), q_offsets, None, self.prompt_ws)
         return self.o(a, self.out[:T], self.linear_ws)

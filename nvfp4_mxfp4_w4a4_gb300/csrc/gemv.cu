@@ -54,7 +54,7 @@ constexpr int kLoaders = 2;             // that load, stages in turns too
 constexpr int kThreads = (kWarps + kLoaders + 1) * 32;  // and one that adds up
 constexpr int kSetRows = 32;
 constexpr int kMostStages = 12;
-constexpr int kMaxSmem = 224 * 1024;
+constexpr int kMaxSmem = 227 * 1024;
 
 struct GemvParams {
     GemvArgs a;
@@ -167,6 +167,9 @@ struct Place {
     }
 };
 
+// Sets whose sums have a place (8 tokens' take 16 KB).
+__host__ __device__ constexpr uint32_t sum_buffers(bool wide) { return wide ? 1 : 2; }
+
 // A place in the ring and the parity of its round.
 struct Turn {
     uint32_t slot = 0, phase = 0;
@@ -182,6 +185,7 @@ template <bool kWide, bool kNv>
 __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, const __grid_constant__ CUtensorMap w_map)
 {
     constexpr int TOK = kWide ? 8 : 2;
+    constexpr uint32_t SUMS = sum_buffers(kWide);
     constexpr int PAD = kWide ? 32 : 0;  // elements between tokens, so that they fall in different banks
     constexpr int BYTES = stage_bytes<kNv>(), RUN = kNv ? 1024 : 512;
     extern __shared__ uint4 smem_raw[];
@@ -192,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     const int N = static_cast<int>(a.N), K = static_cast<int>(a.K);
     // (by an offset, not a cast of the address: the compiler has to see shared memory)
     uint8_t* ring = reinterpret_cast<uint8_t*>(smem_raw) + ((0u - smem_u32(smem_raw)) & 1023u);
-    float* red = reinterpret_cast<float*>(ring + p.stages * BYTES);        // [2][kWarps][TOK][kSetRows]
-    float* xscale = red + 2 * kWarps * TOK * kSetRows;                      // [padded / 32][TOK]
+    float* red = reinterpret_cast<float*>(ring + p.stages * BYTES);        // [SUMS][kWarps][TOK][kSetRows]
+    float* xscale = red + SUMS * kWarps * TOK * kSetRows;                      // [padded / 32][TOK]
     uint4* zeros = reinterpret_cast<uint4*>(xscale + TOK * (padded / 32));  // [4]
     uint64_t* full = reinterpret_cast<uint64_t*>(zeros + 4);                // [kMostStages]
     uint64_t* free_ = full + kMostStages;                                   // [kMostStages]
@@ -227,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
         at.find(p, first);
         uint32_t sets = 0;
         for (int64_t v = first; v < end; at.next(p, ++v), ++sets) {
-            const uint32_t parity = sets & 1u;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&summed[parity], sets >> 1 & 1u, a.status, kStatusTimeout, a.wait_ns)))
+            const uint32_t place = sets % SUMS;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&summed[place], sets / SUMS & 1u, a.status, kStatusTimeout, a.wait_ns)))
                 return;
             const int n = at.set * kSetRows + lane;
             float bias = 0.0f;
@@ -238,13 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 float sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    sum += red[((parity * kWarps + w) * TOK + t) * kSetRows + lane];
+                    sum += red[((place * kWarps + w) * TOK + t) * kSetRows + lane];
                 if (n < N)
                     static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(at.row + t) * N + n] = __float2bfloat16(sum * a.w_global + bias);
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&taken[parity]);
+                mbar_arrive(&taken[place]);
         }
         return;
     }
@@ -484,12 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 mbar_arrive(&free_[slot]);
         }
         // (1 or 2 tokens: the blocks of a quad, then) this warp's sums
-        const uint32_t parity = sets & 1u;
-        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&taken[parity]), (sets >> 1 & 1u) ^ 1u)))
-            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&taken[parity], (sets >> 1 & 1u) ^ 1u, a.status, kStatusTimeout, a.wait_ns));
+        const uint32_t place = sets % SUMS;
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&taken[place]), (sets / SUMS & 1u) ^ 1u)))
+            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&taken[place], (sets / SUMS & 1u) ^ 1u, a.status, kStatusTimeout, a.wait_ns));
         if (!ok)
             break;
-        float* mine = red + (parity * kWarps + warp) * TOK * kSetRows;
+        float* mine = red + (place * kWarps + warp) * TOK * kSetRows;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
             }
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(&summed[parity]);
+            mbar_arrive(&summed[place]);
     }
 }
 
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
 size_t fixed_bytes(int chunks, int tokens, bool wide)
 {
     const size_t padded = static_cast<size_t>(chunks) * kChunk, tok = wide ? 8 : 2;
-    return 1024 + 2 * kWarps * tok * kSetRows * 4 + tok * (padded / 32) * 4 + 64 + (2 * kMostStages + 4) * 8 + tokens * (padded + (wide ? 32 : 0)) * 2;
+    return 1024 + sum_buffers(wide) * kWarps * tok * kSetRows * 4 + tok * (padded / 32) * 4 + 64 + (2 * kMostStages + 4) * 8 + tokens * (padded + (wide ? 32 : 0)) * 2;
 }
 
 template <bool kWide, bool kNv>
@@ -546,8 +550,12 @@ cudaError_t launch(const GemvParams& p, int tokens, cudaStream_t stream)
     const int64_t sms = sm_count();
     q.per = static_cast<int>((q.all + sms - 1) / sms);
     const int64_t steps = static_cast<int64_t>((p.chunks + kChunks - 1) / kChunks) * q.per;
-    q.stages = static_cast<int>(std::min<int64_t>({static_cast<int64_t>((kMaxSmem - fixed) / stage), kMostStages, steps}));
-    if (fixed + 2 * stage > kMaxSmem || q.stages < 1)
+    // An even number: a place of the ring then belongs to one loading warp and one group, which
+    // wait for its rounds one by one.  (With an odd one a place changes hands every round; a
+    // warp that is ahead could take the parity of the round before the last for the last's.)
+    static_assert(kGroups == 2 && kLoaders == 2 && kMostStages % 2 == 0, "places of the ring");
+    q.stages = static_cast<int>(std::min<int64_t>({static_cast<int64_t>((kMaxSmem - fixed) / stage), kMostStages, steps + 1}) / 2 * 2);
+    if (fixed + 2 * stage > kMaxSmem || q.stages < 2)
         return cudaErrorInvalidValue;
     // (make_operand_map's bytes: rows of K / 2 of all the weights.  A copy costs its issue, some
     // 300 cycles: with K % 256 == 0 a stage is one copy of four slabs, else four)

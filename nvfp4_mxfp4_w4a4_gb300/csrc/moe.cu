@@ -168,11 +168,16 @@ __global__ void __launch_bounds__(kThreads) moe_gather_kernel(const __nv_bfloat1
                                                               __nv_bfloat16* __restrict__ sorted, int across_log)
 {
     const Place p = place_of(across_log);
+    const bool live = p.token < tokens && p.at < width;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    // (before the sort has ended: what came before it, and may have written x, ended before
+    // the sort let this kernel start)
+    if (live)
+        v = *reinterpret_cast<const uint4*>(x + p.token * xt + p.at);
     grid_dependency_wait();
     launch_dependents();
-    if (p.token >= tokens || p.at >= width)
+    if (!live)
         return;
-    const uint4 v = *reinterpret_cast<const uint4*>(x + p.token * xt + p.at);
     for (int j = 0; j < top_k; ++j) {
         const int64_t row = row_of[p.token * top_k + j];
         if (row >= 0)

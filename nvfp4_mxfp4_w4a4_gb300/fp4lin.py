@@ -692,7 +692,8 @@ def fp4_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, eps=1e-6, positions
     """q, q_out: bf16 [tokens, q_heads, head_dim]; k, k_out: bf16 [tokens,
     kv_heads, head_dim] or None; q_weight, k_weight: bf16 [head_dim]; with `rope`
     the heads are rotated after their norm (positions: int32 [tokens])."""
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     (tokens, heads, dim), qt, qh, qot, qoh = _pair(q, q_out, "q, q_out")
     kv = kt = kh = kot = koh = kp = ko = kw = 0
     if k is not None:
@@ -718,7 +719,8 @@ def fp4_prompt_attention(q, k, v, out, q_offsets, k_offsets=None, workspace=None
     head_dim]; q_offsets, k_offsets: int32 [batch + 1] (k_offsets None: the same);
     lse: float32 [tokens, q_heads] or None; softmax_scale defaults to
     head_dim ** -0.5."""
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     (tokens, heads, dim), qt, qh, ot, oh = _pair(q, out, "q, out")
     if k.numel() == 0 and k.shape == v.shape:  # (no keys: such tensors may have any strides)
         (keys, kv, kv_dim), kt, kh, vt, vh = k.shape, 0, 0, 0, 0
@@ -758,7 +760,8 @@ def _packed(w, sw, count, N, K, group):
 
 
 def _gemv(x, w, sw, bias, out, M, N, K, group):
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     at = _packed(w, sw, 1, N, K, group)
     return (_vector(x, M * K, "x"), *at), (None if bias is None else _vector(bias, N, "bias"), _vector(out, M * N, "out"))
 
@@ -777,7 +780,8 @@ def fp4_gemv_nvfp4(x_bf16, w, sw, w_global, bias_bf16, out_bf16, M, N, K, stream
 
 def fp4_gemv_mxfp4_experts(x_bf16, expert_ids, E, rows, rows_per_x, w, sw, bias_bf16, out_bf16, N, K, stream=None):
     """out[r] = W[expert_ids[r]] x[r // rows_per_x] (+ bias of the expert); expert_ids: int32 [rows]."""
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     wp, sp = _packed(w, sw, E, N, K, 32)
     _expect(expert_ids, _torch.int32, rows, "expert_ids")
     x = _vector(x_bf16, -(-rows // max(rows_per_x, 1)) * K, "x")
@@ -811,7 +815,8 @@ def _choices(row_of, weights, top_k, tokens):
 def fp4_moe_dispatch(x, expert_ids, E, sorted_x, row_offsets, row_of, stream=None):
     """x: bf16 [tokens, width]; expert_ids, row_of: int32 [tokens, top_k];
     sorted_x: bf16 [tokens * top_k, width]; row_offsets: int32 [E + 1]."""
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     tokens, width, xt = _matrix(x, "x")
     if expert_ids.dim() != 2 or expert_ids.shape[0] != tokens:
         raise ValueError("expert_ids are [tokens, top_k]")
@@ -829,7 +834,8 @@ def fp4_moe_dispatch(x, expert_ids, E, sorted_x, row_offsets, row_of, stream=Non
 def fp4_moe_combine(y, row_of, weights, out, top_k=None, stream=None):
     """y: bf16 [rows, width]; row_of: int32 [tokens, top_k] or None (row t * top_k
     + j); weights: float32 [tokens, top_k] or None (1); out: bf16 [tokens, width]."""
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     rows, width, _ = _matrix(y, "y", True)
     tokens, out_width, ot = _matrix(out, "out")
     if out_width != width:
@@ -842,7 +848,8 @@ def fp4_moe_combine(y, row_of, weights, out, top_k=None, stream=None):
 def fp4_moe_combine_backward(grad_out, y, row_of, weights, grad_y, grad_weights=None, top_k=None, stream=None):
     """grad_out: bf16 [tokens, width]; y, grad_y: bf16 [rows, width] (y None where
     grad_weights is); grad_weights: float32 [tokens, top_k]."""
-    _need_torch()
+    if _torch is None:
+        _need_torch()
     tokens, width, gt = _matrix(grad_out, "grad_out")
     rows, grad_width, _ = _matrix(grad_y, "grad_y", True)
     if grad_width != width:

@@ -236,3 +236,11 @@ def _refused_more(L, call, before, **kw):
     with pytest.raises(ValueError):
         call(**kw)
     assert len(L._calls) == before
+
+
+def test_packed_arguments(L):
+    """What the binding packs is the structures of the header, field by field."""
+    v = tuple(range(1 << 40, (1 << 40) + 16)) + (5, 6, 7, 0.375)
+    assert L._norm_args(*v) == bytes(L.fp4_qk_norm_args(*v))
+    v = tuple(range(1 << 40, (1 << 40) + 17)) + (2, 3, 4, 5, 1, 0.375)
+    assert L._prompt_args(*v) == bytes(L.fp4_prompt_attention_args(*v))
