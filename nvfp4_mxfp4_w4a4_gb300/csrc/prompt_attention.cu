@@ -304,7 +304,10 @@ __device__ bool find_run(const PromptParams& p, uint8_t* scratch, Run* shared)
     for (int w = 0; w < kWarps; ++w)
         longest = max(longest, scan->longest[w]);
     const int whole = !p.may_cut || longest <= kWholeTiles;
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, int64_t(whole ? 1 : kLeastRun));
+    // (a division of 32 bits where that is enough: those of 64 take some 100 instructions)
+    const int64_t up = total + gridDim.x - 1;
+    const int64_t share = up < (int64_t(1) << 32) ? static_cast<uint32_t>(up) / gridDim.x : up / gridDim.x;
+    const int64_t per = max(share, int64_t(whole ? 1 : kLeastRun));
     const int64_t start = blockIdx.x * per;
     const int64_t count = min(per, total - start);
     int64_t base = 0;
@@ -328,7 +331,9 @@ __device__ bool find_run(const PromptParams& p, uint8_t* scratch, Run* shared)
         Run r;
         r.w.b = scan->b;
         r.w.sequence(p);
-        r.w.head = static_cast<int>(scan->offset / scan->per_head);
+        const int64_t offset = scan->offset, per_head = scan->per_head;
+        r.w.head = offset < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(offset) / static_cast<uint32_t>(min(per_head, offset + 1)))
+                                               : static_cast<int>(offset / per_head);
         int64_t in_head = scan->offset - r.w.head * scan->per_head;
         // the block that the start falls into, 32 at a time
         int first = 0;
@@ -841,10 +846,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s[64], top;
                 const int seen = limit - j * kTile;
                 const bool masked = (j + 1) * kTile > free_keys;
+                int most = kTile;  // keys from here on nobody of the warp sees
                 if (masked) {
+                    most = __reduce_max_sync(0xFFFFFFFFu, live ? seen : 0);
                     top = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32) {
+                    for (int c = 0; c < min(most, kTile); c += 32) {
                         tmem_ld_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s));
                         tmem_ld_wait();
 #pragma unroll
@@ -884,41 +891,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float minus = -m;
-                // half of the keys after the other: the MMAs begin with the first
+                // half of the keys after the other: the MMAs begin with the first.  (Masked tiles
+                // have code of their own: a branch in the others' costs them a tenth.)
                 float2 more = make_float2(0.0f, 0.0f);
+                auto weigh = [&](auto edge) {
+                    constexpr bool kEdge = decltype(edge)::value;
 #pragma unroll 1
-                for (int c = 0; c < kTile; c += 64) {
-                    uint32_t w[32];
-                    if (masked) {
+                    for (int c = 0; c < kTile; c += 64) {
+                        uint32_t w[32];
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            s[k] = k < seen - c ? s[k] : -INFINITY;
-                    }
+                        for (int q = 0; q < 64; q += 32) {
+                            if (kEdge && c + q >= most) {
 #pragma unroll
-                    for (int q = 0; q < 64; q += 32) {
+                                for (int k = q; k < q + 32; k += 2)
+                                    w[k / 2] = 0u;
+                                continue;
+                            }
 #pragma unroll
-                        for (int k = q; k < q + 32; k += 2) {
-                            float x[2];
-                            fma_pair(x, s[k], s[k + 1], xs, minus);
-                            x[0] = exp2_approx(x[0]);
-                            x[1] = exp2_approx(x[1]);
-                            if (k & 2)
-                                more = add_pair(more, x[0], x[1]);
-                            else
-                                l = add_pair(l, x[0], x[1]);
-                            w[k / 2] = pack2(x[0], x[1]);
+                            for (int k = q; k < q + 32; k += 2) {
+                                float x[2] = {s[k], s[k + 1]};
+                                if (kEdge) {
+                                    x[0] = k < seen - c ? x[0] : -INFINITY;
+                                    x[1] = k + 1 < seen - c ? x[1] : -INFINITY;
+                                }
+                                fma_pair(x, x[0], x[1], xs, minus);
+                                x[0] = exp2_approx(x[0]);
+                                x[1] = exp2_approx(x[1]);
+                                if (k & 2)
+                                    more = add_pair(more, x[0], x[1]);
+                                else
+                                    l = add_pair(l, x[0], x[1]);
+                                w[k / 2] = pack2(x[0], x[1]);
+                            }
+                            if (c == 0)
+                                tmem_ld_32x32b_x32(s_addr + 64 + q, reinterpret_cast<uint32_t*>(s + q));
                         }
-                        if (c == 0)
-                            tmem_ld_32x32b_x32(s_addr + 64 + q, reinterpret_cast<uint32_t*>(s + q));
+                        tmem_st_32x32b_x32(s_addr + c / 2, w);
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(c == 0 ? &p_half[h] : &p_full[h]);
+                        tmem_ld_wait();
                     }
-                    tmem_st_32x32b_x32(s_addr + c / 2, w);
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(c == 0 ? &p_half[h] : &p_full[h]);
-                    tmem_ld_wait();
-                }
+                };
+                if (masked)
+                    weigh(std::true_type());
+                else
+                    weigh(std::false_type());
                 l = add_pair(l, more.x, more.y);
             }
             // ------------------------------------------------------- results
