@@ -784,8 +784,9 @@ FP4LIN_API fp4_status fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_a
  * launch for both.  With `rope` NULL there is no rotation (positions is not
  * read).  Only the norm where there are no keys: kv_heads = 0, k and k_out
  * NULL (and k_weight).
- * head_dim 64, 128 or 256; strides in elements, multiples of 8; pointers
- * 16-byte aligned.  An output may be its own input (same strides) and must
+ * head_dim 64, 128 or 256; tokens * heads * head_dim / 16 (of both) below
+ * 2^32 - 1024; strides in elements, multiples of 8; pointers 16-byte aligned.
+ * An output may be its own input (same strides) and must
  * not overlap an input otherwise.                                           */
 typedef struct {
     const void* q_bf16;          /* [tokens][q_heads][head_dim] */
@@ -819,8 +820,9 @@ FP4LIN_API fp4_status fp4_qk_norm_rope(const fp4_qk_norm_args* args, const fp4_r
  *        product with v, sums are float32
  *   lse  float32 [tokens][q_heads] or NULL: log of the sum of
  *        exp(softmax_scale q . k); -inf for a query that sees no key
- * What a query does not see has no influence on it, NaN and Inf included.
- * Queries behind the last sequence are not written.  Offsets are clamped to
+ * What a query does not see has no influence on it, NaN and Inf included (an
+ * Inf among the values that it sees gives Inf, or NaN where the weight is below
+ * float32's range).  Queries behind the last sequence are not written.  Offsets are clamped to
  * [0, tokens] (and each end to its start), so that wrong ones give wrong
  * numbers but no access outside the tensors.
  * head_dim 64 or 128; strides in elements, multiples of 8, those of q, k and v
@@ -897,7 +899,7 @@ FP4LIN_API fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* 
  *   row_offsets  int32 [E + 1]: first row of each expert, then the rows in all
  *   row_of       int32 [tokens][top_k]: the row of each choice, -1 for none
  * Rows of one expert are in the order of (token, choice).  tokens * top_k below
- * 2^31 - 256, top_k 1 .. 64, 1 <= E <= 1024, width a multiple of 8 up to 2^20; strides in
+ * 2^31 - 2^14, top_k 1 .. 64, 1 <= E <= 1024, width a multiple of 8 up to 2^20; strides in
  * elements, multiples of 8; bf16 pointers 16-byte aligned, others 4-byte.    */
 
 /* Fills row_offsets and row_of, and copies every choice's token to its row of

@@ -159,7 +159,7 @@ fp4_status gemv(const void* x, const uint8_t* w, const uint8_t* sw, float w_glob
 
 fp4_status check_choices(int64_t tokens, int32_t top_k, int64_t width, int64_t stride)
 {
-    if (tokens < 0 || top_k <= 0 || top_k > 64 || tokens >= kMaxDim || tokens * top_k >= kMaxDim - 256 || width <= 0 ||
+    if (tokens < 0 || top_k <= 0 || top_k > 64 || tokens >= kMaxDim || tokens * top_k >= kMaxDim - 16384 || width <= 0 ||
         width % 8 != 0 || width > (int64_t(1) << 20) || stride < 0)
         return FP4_ERR_SHAPE;
     return stride % 8 == 0 ? FP4_OK : FP4_ERR_ALIGNMENT;

@@ -800,13 +800,15 @@ def _matrix(t, what, contiguous=False):
     return rows, width, a if rows > 1 else width
 
 
-def _choices(row_of, weights, top_k, tokens):
-    if row_of is not None:
-        top_k = row_of.shape[-1]
-        _expect(row_of, _torch.int32, tokens * top_k, "row_of")
-    if weights is not None:
-        top_k = weights.shape[-1] if top_k is None else top_k
-        _expect(weights, _torch.float32, tokens * top_k, "weights")
+def _choices(row_of, weights, top_k, tokens, grad=None):
+    """top_k, from the tensors [tokens, top_k] that there are."""
+    for t, kind, what in ((row_of, _torch.int32, "row_of"), (weights, _torch.float32, "weights"), (grad, _torch.float32, "grad_weights")):
+        if t is None:
+            continue
+        if t.dim() != 2 or t.shape[0] != tokens or (top_k is not None and t.shape[1] != top_k):
+            raise ValueError("%s: [tokens, top_k]" % what)
+        top_k = t.shape[1]
+        _expect(t, kind, tokens * top_k, what)
     if top_k is None:
         raise ValueError("top_k: needed without row_of and weights")
     return top_k
@@ -822,6 +824,8 @@ def fp4_moe_dispatch(x, expert_ids, E, sorted_x, row_offsets, row_of, stream=Non
         raise ValueError("expert_ids are [tokens, top_k]")
     top_k = expert_ids.shape[1]
     _expect(expert_ids, _torch.int32, tokens * top_k, "expert_ids")
+    if row_of.shape != expert_ids.shape:
+        raise ValueError("row_of and expert_ids have the same shape")
     _expect(row_of, _torch.int32, tokens * top_k, "row_of")
     _expect(row_offsets, _torch.int32, E + 1, "row_offsets")
     rows, sorted_width, _ = _matrix(sorted_x, "sorted_x", True)
@@ -854,9 +858,8 @@ def fp4_moe_combine_backward(grad_out, y, row_of, weights, grad_y, grad_weights=
     rows, grad_width, _ = _matrix(grad_y, "grad_y", True)
     if grad_width != width:
         raise ValueError("grad_out and grad_y have the same width")
-    top_k = _choices(row_of, weights, top_k, tokens)
+    top_k = _choices(row_of, weights, top_k, tokens, grad_weights)
     if grad_weights is not None:
-        _expect(grad_weights, _torch.float32, tokens * top_k, "grad_weights")
         if _matrix(y, "y", True)[:2] != (rows, width):
             raise ValueError("y and grad_y have the same shape")
     _check(load().fp4_moe_combine_backward(grad_out.data_ptr(), _ptr(y), _ptr(row_of), _ptr(weights), tokens, top_k, rows,

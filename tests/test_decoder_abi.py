@@ -215,7 +215,8 @@ def test_moe_binding(L):
         L.fp4_moe_combine(y, rows, w, out, **kw)
 
     for bad in (dict(y=_z(6, 128)[:, :64]), dict(out=_z(3, 72)), dict(out=_z(4, 64)), dict(w=_z(2, 2, dtype=F32)),
-                dict(w=_z(3, 2)), dict(rows=_z(3, 2, dtype=I64)), dict(rows=None, w=None)):
+                dict(w=_z(3, 2)), dict(rows=_z(3, 2, dtype=I64)), dict(rows=None, w=None), dict(w=_z(3, 3, dtype=F32)),
+                dict(rows=_z(2, 3, dtype=I32)), dict(rows=_z(6, dtype=I32)), dict(top_k=3)):
         _refused_more(L, combine, 1, **bad)
     combine()
     combine(rows=None)
@@ -225,7 +226,7 @@ def test_moe_binding(L):
         L.fp4_moe_combine_backward(g, y, rows, w, gy, gw)
 
     for bad in (dict(g=_z(4, 64)), dict(g=_z(3, 72)), dict(y=_z(5, 64)), dict(gy=_z(6, 64, dtype=F32)),
-                dict(gw=_z(3, 1, dtype=F32)), dict(gy=_z(6, 128)[:, :64])):
+                dict(gw=_z(3, 1, dtype=F32)), dict(gw=_z(3, 3, dtype=F32)), dict(gy=_z(6, 128)[:, :64])):
         _refused_more(L, backward, 4, **bad)
     backward()
     backward(y=None, gw=None)

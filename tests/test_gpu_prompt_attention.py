@@ -136,6 +136,23 @@ def test_formula(L, lens, heads, group, dim, layout, causal):
     p.check(causal)
 
 
+@pytest.mark.parametrize("heads,group,dim", [(2, 130, 64), (1, 256, 128), (1, 100, 64), (2, 17, 128)])
+def test_many_heads(L, heads, group, dim):
+    """More query heads of a key head than a tile has rows, and groups that leave rows over."""
+    for causal in (True, False):
+        p = Problem([(3, 3), (1, 140), (9, 4)], heads, group, dim, seed=group)
+        p.run(L, causal)
+        p.check(causal)
+
+
+def test_one_key_head_of_many_sequences(L):
+    """More sequences than a block has threads, empty ones among them."""
+    lens = [((i * 7) % 5, (i * 7) % 5 + (i % 3)) if i % 4 else (0, 2) for i in range(700)]
+    p = Problem(lens, 1, 2, 64, seed=11)
+    p.run(L)
+    p.check()
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_long_prompt(L, dim):
     """A prompt of many tiles; rows spread over it against the formula."""
