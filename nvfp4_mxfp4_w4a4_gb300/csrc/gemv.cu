@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     }
     if (warp >= kWarps) {
         // ------------------------------------------------------------ weights
-        if (lane == 0) {
+        {  // (the whole warp walks the loop: the copies' operands are then uniform)
             Place at;
             at.find(p, first);
             Turn turn;
@@ -271,21 +271,25 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 for (int step = 0; step < steps; ++step, turn.next(p.stages), ++issued) {
                     if ((issued & (kLoaders - 1)) != mine)
                         continue;
-                    ok = mbar_wait_bounded(&free_[turn.slot], turn.phase ^ 1u, a.status, kStatusTimeout, a.wait_ns);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&free_[turn.slot]), turn.phase ^ 1u)))
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&free_[turn.slot], turn.phase ^ 1u, a.status, kStatusTimeout, a.wait_ns));
                     if (!ok)
                         break;
                     uint8_t* to = ring + turn.slot * BYTES;
                     uint64_t* bar = &full[turn.slot];
                     const uint32_t bytes = min(kChunks * RUN, p.kb4 * 512 - step * (kChunks * RUN));
                     const int slabs = p.slabs ? kStageK / 256 : min(kStageK / 256, (K - step * kStageK + 255) / 256);
-                    mbar_arrive_expect_tx(bar, slabs * kSlab + bytes);
-                    if (p.slabs) {
-                        tma_load_3d(to, &w_map, bar, 0, row0, step * (kStageK / 256));
-                    } else {
-                        for (int i = 0; i < slabs; ++i)
-                            tma_load_2d(to + i * kSlab, &w_map, bar, step * (kStageK / 2) + i * 128, row0);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, slabs * kSlab + bytes);
+                        if (p.slabs) {
+                            tma_load_3d(to, &w_map, bar, 0, row0, step * (kStageK / 256));
+                        } else {
+                            for (int i = 0; i < slabs; ++i)
+                                tma_load_2d(to + i * kSlab, &w_map, bar, step * (kStageK / 2) + i * 128, row0);
+                        }
+                        bulk_load(to + kCodeBytes, scales + static_cast<int64_t>(step) * (kChunks * RUN), bytes, bar);
                     }
-                    bulk_load(to + kCodeBytes, scales + static_cast<int64_t>(step) * (kChunks * RUN), bytes, bar);
+                    __syncwarp();
                 }
             }
             // (every copy is waited for by the warps that multiply, unless they gave up)
@@ -379,6 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], turn.phase, a.status, kStatusTimeout, a.wait_ns));
             if (!ok)
                 break;
+            // the stage may be loaded again as soon as its codes and scales are in registers
+            auto release = [&]() {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&free_[slot]);
+            };
             const int c = step * kChunks + chunk;
             if (c < p.chunks) {
                 // piece i of row g + 8 q is at codes + 1024 q + ((i ^ g) << 4)
@@ -396,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                         scw[q] = *reinterpret_cast<const uint32_t*>(scales + q * 128 + (kNv && live ? (j >> 1) * 512 : 0));
                         cw[q] = *reinterpret_cast<const uint4*>(codes + q * 1024 + (((piece + j) ^ g) << 4));
                     }
+                    release();
                     const float2 xsc = *reinterpret_cast<const float2*>(xscale + (c * 4 + j) * TOK);
                     uint32_t pairs[4];  // NVFP4: both groups' scales of a row
                     if constexpr (kNv) {
@@ -442,12 +453,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                         }
                     }
                 } else {
-                    uint32_t scw[4], scv[4];
+                    uint32_t scw[4], scv[4], cw[4][4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         scw[q] = *reinterpret_cast<const uint32_t*>(scales + q * 128);
                         scv[q] = kNv ? *reinterpret_cast<const uint32_t*>(scales + q * 128 + 512) : 0u;
+#pragma unroll
+                        for (int bl = 0; bl < 4; ++bl)
+                            cw[q][bl] = *reinterpret_cast<const uint32_t*>(codes + q * 1024 + (((piece + bl) ^ g) << 4) + j * 4);
                     }
+                    release();
 #pragma unroll
                     for (int bl = 0; bl < 4; ++bl) {
                         if (!whole && c * kChunk + 32 * bl >= K)
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 const int q = 2 * t + r;
-                                e2m1x8(*reinterpret_cast<const uint32_t*>(codes + q * 1024 + (((piece + bl) ^ g) << 4) + j * 4), h[r]);
+                                e2m1x8(cw[q][bl], h[r]);
                                 if constexpr (kNv) {
                                     const uint32_t both = e4m3x2((bl < 2 ? scw[q] : scv[q]) >> ((bl & 1) * 16));
                                     const uint32_t f = __byte_perm(both, 0, j < 2 ? 0x1010 : 0x3232);
@@ -482,10 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                         }
                     }
                 }
+            } else {
+                release();
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&free_[slot]);
         }
         // (1 or 2 tokens: the blocks of a quad, then) this warp's sums
         const uint32_t place = sets % SUMS;
