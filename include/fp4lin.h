@@ -900,7 +900,8 @@ FP4LIN_API fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* 
  *   row_of       int32 [tokens][top_k]: the row of each choice, -1 for none
  * Rows of one expert are in the order of (token, choice).  tokens * top_k below
  * 2^31 - 2^14, top_k 1 .. 64, 1 <= E <= 1024, width a multiple of 8 up to 2^20; strides in
- * elements, multiples of 8; bf16 pointers 16-byte aligned, others 4-byte.    */
+ * elements, multiples of 8; bf16 pointers 16-byte aligned, others 4-byte.
+ * Outputs must not overlap inputs.                                          */
 
 /* Fills row_offsets and row_of, and copies every choice's token to its row of
  * sorted [tokens * top_k][width].  Rows from row_offsets[E] on are not written
