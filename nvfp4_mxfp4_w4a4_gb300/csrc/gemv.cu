@@ -63,7 +63,6 @@ struct GemvParams {
     int chunks;  // of K
     int sets;    // of a weight's rows
     int stages;
-    bool slabs;  // the map's third dimension: K is whole slabs, a stage is one copy
     int per;     // sets of a CTA (of all rows' weights with experts)
     int64_t all;
 };
@@ -278,15 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                     uint8_t* to = ring + turn.slot * BYTES;
                     uint64_t* bar = &full[turn.slot];
                     const uint32_t bytes = min(kChunks * RUN, p.kb4 * 512 - step * (kChunks * RUN));
-                    const int slabs = p.slabs ? kStageK / 256 : min(kStageK / 256, (K - step * kStageK + 255) / 256);
+                    const int slabs = min(kStageK / 256, (K - step * kStageK + 255) / 256);
                     if (elect_one()) {
                         mbar_arrive_expect_tx(bar, slabs * kSlab + bytes);
-                        if (p.slabs) {
-                            tma_load_3d(to, &w_map, bar, 0, row0, step * (kStageK / 256));
-                        } else {
-                            for (int i = 0; i < slabs; ++i)
-                                tma_load_2d(to + i * kSlab, &w_map, bar, step * (kStageK / 2) + i * 128, row0);
-                        }
+                        for (int i = 0; i < slabs; ++i)
+                            tma_load_2d(to + i * kSlab, &w_map, bar, step * (kStageK / 2) + i * 128, row0);
                         bulk_load(to + kCodeBytes, scales + static_cast<int64_t>(step) * (kChunks * RUN), bytes, bar);
                     }
                     __syncwarp();
@@ -571,12 +566,10 @@ cudaError_t launch(const GemvParams& p, int tokens, cudaStream_t stream)
     q.stages = static_cast<int>(std::min<int64_t>({static_cast<int64_t>((kMaxSmem - fixed) / stage), kMostStages, steps + 1}) / 2 * 2);
     if (fixed + 2 * stage > kMaxSmem || q.stages < 2)
         return cudaErrorInvalidValue;
-    // (make_operand_map's bytes: rows of K / 2 of all the weights.  A copy costs its issue, some
-    // 300 cycles: with K % 256 == 0 a stage is one copy of four slabs, else four)
+    // (make_operand_map's bytes: rows of K / 2 of all the weights.  One copy of a stage's four
+    // slabs, where K allows it, measured the same as four)
     CUtensorMap w_map;
-    q.slabs = p.a.K % 256 == 0;
-    if (!make_operand_map(&w_map, p.a.w, p.a.N * (p.a.expert_ids != nullptr ? p.a.E : 1), p.a.K / 2, kSetRows,
-                          q.slabs ? kStageK / 256 : 1, kOpBytes))
+    if (!make_operand_map(&w_map, p.a.w, p.a.N * (p.a.expert_ids != nullptr ? p.a.E : 1), p.a.K / 2, kSetRows, 1, kOpBytes))
         return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>((q.all + q.per - 1) / q.per);
     return launch_pdl(kern, dim3(grid), dim3(kThreads), fixed + q.stages * stage, stream, q, w_map);
@@ -595,7 +588,9 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream)
     if (a.expert_ids != nullptr)
         return launch<false, false>(p, 1, stream);
     // the activations of a launch's rows have to fit into shared memory beside two stages:
-    // long ones go a few at a time
+    // long ones go a few at a time.  1 or 2 tokens, in the narrow / the wide form: 8.3 / 8.9 and
+    // 9.4 / 9.1 us at 14336 x 4096, 15.1 / 17.2 and 16.7 / 17.6 us at 18432 x 7168, 4.3 / 4.4 and
+    // 5.0 / 4.8 us at 4096 x 4096
     int step = a.M;
     while (step > 1 && fixed_bytes(p.chunks, step, step > 2) + 2 * (a.nv ? stage_bytes<true>() : stage_bytes<false>()) > kMaxSmem)
         --step;
