@@ -869,8 +869,10 @@ FP4LIN_API fp4_status fp4_prompt_attention(const fp4_prompt_attention_args* args
  *                   w_global
  * Products of codes and activations are exact, sums are float32, one rounding.
  * (Activations below 2^-31 of the largest of their block of 32 are rounded to
- * multiples of 2^-38 of it; sums below 2^-126 may become zero.)  A NaN scale or
- * a NaN or Inf activation reaches the outputs that it is a part of.
+ * multiples of 2^-38 of it; sums below 2^-126 may become zero; where a scale
+ * times the largest activation of its block passes 2^141, the output may be Inf
+ * or NaN whatever the codes.)  A NaN scale or a NaN or Inf activation reaches
+ * the outputs that it is a part of.
  * M 0 .. 8 (0: nothing to do); N up to 2^24, K a multiple of 32 up to 65536;
  * x, w, sw and out 16-byte aligned, bias (or NULL) 2-byte.  No workspace.    */
 FP4LIN_API fp4_status fp4_gemv_mxfp4(const void* x_bf16, const uint8_t* w, const uint8_t* sw, const void* bias_bf16,

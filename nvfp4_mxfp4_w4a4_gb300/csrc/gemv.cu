@@ -143,6 +143,21 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t w)
     return r;
 }
 
+// acc[i] += d[i] * (f * x[i]), both at once.
+__device__ __forceinline__ void add_scaled(float* acc, const float* d, float f, float2 x)
+{
+    asm("{\n\t.reg .b64 a, b, c, e;\n\t"
+        "mov.b64 a, {%4, %4};\n\t"
+        "mov.b64 b, {%5, %6};\n\t"
+        "mov.b64 c, {%2, %3};\n\t"
+        "mov.b64 e, {%0, %1};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\t"
+        "fma.rn.f32x2 e, c, a, e;\n\t"
+        "mov.b64 {%0, %1}, e;\n\t}"
+        : "+f"(acc[0]), "+f"(acc[1])
+        : "f"(d[0]), "f"(d[1]), "f"(f), "f"(x.x), "f"(x.y));
+}
+
 // A place among a CTA's sets: the output's row (with experts) and the set of the
 // weight's rows.
 struct Place {
@@ -345,10 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                         break;
                     const uint32_t w[4] = {q[t].x, q[t].y, q[t].z, q[t].w};
                     // (the largest magnitude as bits: NaN and Inf come out on top)
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        top = max(top, max(w[n] & 0x7FFFu, (w[n] >> 16) & 0x7FFFu));
+                    const uint32_t two = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                                  __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+                    uint32_t top = max(two & 0xFFFFu, two >> 16);
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                     const uint32_t e = max(top >> 7, 15u);
@@ -492,10 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                             float2 f = make_float2(1.0f, 1.0f);
                             if constexpr (!kNv)
                                 f = e8m0x2(__byte_perm(scw[2 * t], scw[2 * t + 1], bl * 0x11 + 0x40));
-                            acc[2 * t][0] += d[0] * (f.x * xsc.x);
-                            acc[2 * t][1] += d[1] * (f.x * xsc.y);
-                            acc[2 * t + 1][0] += d[2] * (f.y * xsc.x);
-                            acc[2 * t + 1][1] += d[3] * (f.y * xsc.y);
+                            add_scaled(acc[2 * t], d, f.x, xsc);
+                            add_scaled(acc[2 * t + 1], d + 2, f.y, xsc);
                         }
                     }
                 }
