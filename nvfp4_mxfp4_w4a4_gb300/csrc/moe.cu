@@ -2,7 +2,8 @@
 // grouped by expert, and back: the steps before and behind the grouped GEMM.
 //
 //   dispatch   a stable counting sort of the pairs by expert (row_offsets,
-//              row_of), then every token's vector to the rows of its choices
+//              row_of), then every token's vector to the rows of its choices;
+//              in one launch where the pairs are few
 //   combine    out[t] = sum_j w[t, j] y[row_of[t, j]]
 //   backward   grad_y[row_of[t, j]] = w[t, j] grad[t],
 //              grad_w[t, j] = <grad[t], y[row_of[t, j]]>
@@ -10,7 +11,7 @@
 // All are bound by HBM but for the smallest calls, where the launches count: 4096
 // tokens x 8 of 64 experts, 4096 wide, are 302 MB in 44.8 us (0.99 of a plain
 // copy's rate) behind a sort of 8; the same tokens' sum 44 us, its gradient 87 us
-// (604 MB, 1.0).  32 tokens: 5.1 us sorted and copied, 3.2 us summed, on the device.
+// (604 MB, 1.0).  32 tokens: 3.2 us sorted and copied, 3.2 us summed, on the device.
 // Nothing is added by atomics: every result has one order.
 #include <cuda_bf16.h>
 
@@ -228,6 +229,109 @@ __global__ void __launch_bounds__(kThreads) moe_gather_kernel(const __nv_bfloat1
     }
 }
 
+// Few pairs: every block finds the rows of its own tokens' choices by counting, over
+// all pairs, those of lower experts and the earlier ones of the same.  Block 0 also
+// writes the offsets.  At most kFewPairs pairs, kFewOwn of them a block's: one launch
+// takes 3.2 us for 256 pairs, 4096 wide, and 4.0 for 1024 where the sort and the copies
+// take 5.2 and 6.4; 16 choices a block 4.3 against 5.7, but 32 6.1 against 5.6.
+constexpr int kFewPairs = 1024, kFewOwn = 16;
+
+__global__ void __launch_bounds__(kThreads) moe_dispatch_few_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                    const int32_t* __restrict__ ids, int tokens, int top_k,
+                                                                    int E, int64_t width, int64_t xt,
+                                                                    __nv_bfloat16* __restrict__ sorted,
+                                                                    int32_t* __restrict__ row_offsets,
+                                                                    int32_t* __restrict__ row_of, int across_log)
+{
+    constexpr int kWarps = kThreads / 32, kMine = kFewPairs / kThreads;
+    constexpr int kNone = 0x7FFFFFFF;  // of no expert: behind all
+    __shared__ int own[kFewOwn], part[kWarps][kFewOwn];
+    extern __shared__ int counts[];  // [E], block 0's
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Place p = place_of(across_log);
+    const bool live = p.token < tokens && p.at < width;
+    const int pairs = tokens * top_k;
+    const int down = kThreads >> across_log;
+    const int first = static_cast<int>(blockIdx.x) * down * top_k;  // pair of the block
+    const int owned = min(down * top_k, pairs - first);
+    grid_dependency_wait();
+    launch_dependents();
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (live)
+        v = *reinterpret_cast<const uint4*>(x + p.token * xt + p.at);
+    int mine[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int q = k * kThreads + threadIdx.x;
+        const int e = q < pairs ? __ldg(ids + q) : -1;
+        mine[k] = e >= 0 && e < E ? e : kNone;
+        if (q >= first && q < first + owned)
+            own[q - first] = mine[k];
+    }
+    __syncthreads();
+    for (int o = 0; o < owned; ++o) {
+        const int e = own[o], at = first + o;
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k)
+            n += mine[k] < e || (mine[k] == e && k * kThreads + static_cast<int>(threadIdx.x) < at);
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        if (lane == 0)
+            part[warp][o] = n;
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < owned; o += kThreads) {
+        int row = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            row += part[w][o];
+        row = own[o] != kNone ? row : -1;
+        own[o] = row;
+        if (blockIdx.y == 0)
+            row_of[first + o] = row;
+    }
+    __syncthreads();
+    if (live) {
+        const int* rows = own + (threadIdx.x >> across_log) * top_k;
+        for (int j = 0; j < top_k; ++j)
+            if (rows[j] >= 0)
+                *reinterpret_cast<uint4*>(sorted + rows[j] * width + p.at) = v;
+    }
+    if (blockIdx.x != 0 || blockIdx.y != 0)
+        return;
+    for (int e = threadIdx.x; e < E; e += kThreads)
+        counts[e] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k)
+        if (mine[k] != kNone)
+            atomicAdd(&counts[mine[k]], 1);  // (whole numbers: in any order)
+    __syncthreads();
+    // a thread has a run of experts
+    const int run = (E + kThreads - 1) / kThreads, e0 = min(threadIdx.x * run, E), e1 = min(e0 + run, E);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e)
+        sum += counts[e];
+    int before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        before += lane >= d ? y : 0;
+    }
+    if (lane == 31)
+        part[0][warp] = before;
+    __syncthreads();
+    before -= sum;
+    for (int w = 0; w < warp; ++w)
+        before += part[0][w];
+    for (int e = e0; e < e1; ++e) {
+        row_offsets[e] = before;
+        before += counts[e];
+    }
+    if (threadIdx.x == kThreads - 1)
+        row_offsets[E] = before;
+}
+
 __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const __nv_bfloat16* __restrict__ y, const int32_t* __restrict__ row_of,
                                                                const float* __restrict__ weights, int64_t tokens, int top_k,
                                                                int64_t rows, int64_t width, __nv_bfloat16* __restrict__ out,
@@ -305,6 +409,12 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const __nv_bf
 cudaError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t tokens, int top_k, int E, int64_t width, int64_t xt,
                                 void* sorted, int32_t* row_offsets, int32_t* row_of, cudaStream_t stream)
 {
+    const int64_t pairs = tokens * top_k;
+    const Shape s = shape_of(tokens, width);
+    if (tokens > 0 && pairs <= kFewPairs && (kThreads >> s.across_log) * top_k <= kFewOwn)
+        return launch_pdl(moe_dispatch_few_kernel, s.grid, dim3(kThreads), static_cast<size_t>(E) * 4, stream,
+                          static_cast<const __nv_bfloat16*>(x), ids, static_cast<int>(tokens), top_k, E, width, xt,
+                          static_cast<__nv_bfloat16*>(sorted), row_offsets, row_of, s.across_log);
     // per device and context, once: the shared-memory opt-in
     static std::mutex mu;
     static unsigned long long configured[64] = {};
@@ -324,7 +434,6 @@ cudaError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t token
             configured[dev] = ctx;
         }
     }
-    const int64_t pairs = tokens * top_k;
     // one step of a CTA, or a cluster: 2048 pairs in 6.6 / 5.9 us, 8192 in 11.6 / 6.0, 32768 in
     // 31.8 / 8.4 (11.9 with 4 CTAs); up to 1024 the same
     const int ctas = pairs <= kSortThreads ? 1 : kSortCluster;
@@ -344,7 +453,6 @@ cudaError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t token
     err = cudaLaunchKernelEx(&cfg, ctas == 1 ? moe_sort_kernel<1> : moe_sort_kernel<kSortCluster>, ids, static_cast<int>(pairs), E, row_offsets, row_of);
     if (err != cudaSuccess || tokens == 0)
         return err;
-    const Shape s = shape_of(tokens, width);
     return launch_pdl(moe_gather_kernel, s.grid, dim3(kThreads), 0, stream, static_cast<const __nv_bfloat16*>(x), row_of, tokens,
                       top_k, width, xt, static_cast<__nv_bfloat16*>(sorted), s.across_log);
 }

@@ -750,39 +750,41 @@ def fp4_prompt_attention(q, k, v, out, q_offsets, k_offsets=None, workspace=None
 # ------------------------------------- around the FP4 weights: few rows, experts
 
 
-def _packed(w, sw, count, N, K, group):
-    """The addresses of `count` packed weights [N, K / 2] and their swizzled scales."""
-    need = count * -(-N // 128) * -(-K // (4 * group)) * 512
-    for t, n, what in ((w, count * N * K // 2, "w"), (sw, need, "sw")):
-        if t.element_size() != 1 or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError("%s: a contiguous device tensor of bytes with at least %d elements" % (what, n))
-    return w.data_ptr(), sw.data_ptr()
+def _bytes(t, count, what):
+    if t.numel() < count or t.element_size() != 1 or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s: a contiguous device tensor of bytes with at least %d elements" % (what, count))
+    return t.data_ptr()
 
 
-def _gemv(x, w, sw, bias, out, M, N, K, group):
-    if _torch is None:
-        _need_torch()
-    at = _packed(w, sw, 1, N, K, group)
-    return (_vector(x, M * K, "x"), *at), (None if bias is None else _vector(bias, N, "bias"), _vector(out, M * N, "out"))
+def _scale_bytes(N, K, group):
+    return -(-N // 128) * -(-K // (4 * group)) * 512
 
 
 def fp4_gemv_mxfp4(x_bf16, w, sw, bias_bf16, out_bf16, M, N, K, stream=None):
     """bf16 rows [M, K] x MXFP4 weights, M up to 8, activations not quantized."""
-    a, b = _gemv(x_bf16, w, sw, bias_bf16, out_bf16, M, N, K, 32)
-    _check(load().fp4_gemv_mxfp4(*a, *b, M, N, K, _stream(stream)), "fp4_gemv_mxfp4")
+    if _torch is None:
+        _need_torch()
+    _check(load().fp4_gemv_mxfp4(_vector(x_bf16, M * K, "x"), _bytes(w, N * K // 2, "w"),
+                                 _bytes(sw, _scale_bytes(N, K, 32), "sw"),
+                                 None if bias_bf16 is None else _vector(bias_bf16, N, "bias"),
+                                 _vector(out_bf16, M * N, "out"), M, N, K, _stream(stream)), "fp4_gemv_mxfp4")
 
 
 def fp4_gemv_nvfp4(x_bf16, w, sw, w_global, bias_bf16, out_bf16, M, N, K, stream=None):
     """bf16 rows [M, K] x NVFP4 weights (swizzled E4M3 scales, times w_global)."""
-    a, b = _gemv(x_bf16, w, sw, bias_bf16, out_bf16, M, N, K, 16)
-    _check(load().fp4_gemv_nvfp4(*a, w_global, *b, M, N, K, _stream(stream)), "fp4_gemv_nvfp4")
+    if _torch is None:
+        _need_torch()
+    _check(load().fp4_gemv_nvfp4(_vector(x_bf16, M * K, "x"), _bytes(w, N * K // 2, "w"),
+                                 _bytes(sw, _scale_bytes(N, K, 16), "sw"), w_global,
+                                 None if bias_bf16 is None else _vector(bias_bf16, N, "bias"),
+                                 _vector(out_bf16, M * N, "out"), M, N, K, _stream(stream)), "fp4_gemv_nvfp4")
 
 
 def fp4_gemv_mxfp4_experts(x_bf16, expert_ids, E, rows, rows_per_x, w, sw, bias_bf16, out_bf16, N, K, stream=None):
     """out[r] = W[expert_ids[r]] x[r // rows_per_x] (+ bias of the expert); expert_ids: int32 [rows]."""
     if _torch is None:
         _need_torch()
-    wp, sp = _packed(w, sw, E, N, K, 32)
+    wp, sp = _bytes(w, E * N * K // 2, "w"), _bytes(sw, E * _scale_bytes(N, K, 32), "sw")
     _expect(expert_ids, _torch.int32, rows, "expert_ids")
     x = _vector(x_bf16, -(-rows // max(rows_per_x, 1)) * K, "x")
     bias = None if bias_bf16 is None else _vector(bias_bf16, E * N, "bias")

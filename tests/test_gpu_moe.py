@@ -66,6 +66,17 @@ def test_dispatch(L, tokens, top, E, width, kind):
     assert torch.equal(to.cpu(), expect)
 
 
+# Few pairs: whole blocks of one token, blocks of several, the last one short, 64 choices.
+FEW = [(128, 8, 1024, 1032), (1024, 1, 64, 520), (16, 64, 100, 1024), (7, 16, 33, 256), (61, 4, 1, 72), (9, 3, 2, 1048), (1, 64, 1024, 2048),
+       (63, 8, 33, 512), (61, 4, 1, 256), (64, 16, 9, 4104)]
+
+
+@pytest.mark.parametrize("kind", ["plain", "padded", "one", "none"])
+@pytest.mark.parametrize("tokens,top,E,width", FEW)
+def test_dispatch_of_few(L, tokens, top, E, width, kind):
+    test_dispatch(L, tokens, top, E, width, kind)
+
+
 def fast_rows(ids, E):
     key = np.where((ids >= 0) & (ids < E), ids, E).reshape(-1)
     order = np.argsort(key, kind="stable")
