@@ -11,8 +11,8 @@
 // stage.  The warps' sums of a set are added up by one more warp, in one order.
 //
 // On the device, weights in L2 where they fit: MXFP4, 1 token, 4096 x 4096 4.6 us;
-// NVFP4, 3 tokens, 14336 x 4096 10.3; MXFP4, 8 tokens, 18429 x 7168 21.2; 8 experts
-// of 2048 x 4096 10.8.  The loads alone take 3.1 / 5.0 / 9.1 / 6.1 us, all but the
+// NVFP4, 3 tokens, 14336 x 4096 10.3; MXFP4, 8 tokens, 18429 x 7168 20.1; 8 experts
+// of 2048 x 4096 10.9.  The loads alone take 3.1 / 5.0 / 9.1 / 6.1 us, all but the
 // decoding and the MMAs 3.2 / 5.6 / 12.6 / 6.2.  So what bounds it are the 190 to 250
 // instructions per 32 rows x 128 elements, 64 of them conversions of two codes that
 // take the ALU two cycles each.

@@ -24,10 +24,12 @@
 // per SM.  A unit whose tiles fall to several CTAs leaves partial results, which a
 // second kernel joins.  Where all units are short, they are dealt out whole.
 //
-// 16381 tokens, 8 x 4 heads of 128, causal: 1328 us, 0.87 of the rate of a large bf16
-// product; the tensor pipe is busy 77 % of a run's cycles, the exponentials' 39 %.
-// 16 sequences of up to 509 tokens, heads of 64: 40 us, of which a unit of two tiles
-// is 6: load, S, weights, P V and results one behind the other.
+// 16381 tokens, 8 x 4 heads of 128, causal: 1265 to 1365 us (from GPU to GPU), 0.84 to
+// 0.91 of the rate of a large bf16 product; the tensor pipe is busy 77 % of a run's
+// cycles, the exponentials' 39 %.  16 sequences of up to 509 tokens, heads of 64: 37
+// us, 5 of them before the first unit's products; a unit of two tiles is load, S,
+// weights, P V and results one behind the other, and a fifth of the time its warps
+// wait for instructions.
 //
 // Warps: 0-3 and 4-7 the softmax of the halves (they also write the results), 8
 // loads queries, keys and values (TMA), 9 issues the MMAs, 10 looks through values
@@ -853,21 +855,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s[64], top;
                 const int seen = limit - j * kTile;
                 const bool masked = (j + 1) * kTile > free_keys;
-                int most = kTile;  // keys from here on nobody of the warp sees
+                // the warp's rows see all keys below `least` and none from `most` on
+                int least = kTile, most = kTile;
                 if (masked) {
                     most = __reduce_max_sync(0xFFFFFFFFu, live ? seen : 0);
+                    least = __reduce_min_sync(0xFFFFFFFFu, live ? seen : kTile);
                     top = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < min(most, kTile); c += 32) {
-                        tmem_ld_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s));
+                        float t = tmem_ld_max_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s));
                         tmem_ld_wait();
+                        if (c + 32 > least) {
+                            t = -INFINITY;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            top = k < seen - c ? fmaxf(top, s[k]) : top;
+                            for (int k = 0; k < 32; ++k)
+                                t = k < seen - c ? fmaxf(t, s[k]) : t;
+                        }
+                        top = fmaxf(top, t);
                     }
-                    tmem_ld_32x32b_x32(s_addr, reinterpret_cast<uint32_t*>(s));
-                    tmem_ld_32x32b_x32(s_addr + 32, reinterpret_cast<uint32_t*>(s + 32));
-                    tmem_ld_wait();
                 } else {
                     float mx[4];
                     mx[2] = tmem_ld_max_32x32b_x32(s_addr + 64, reinterpret_cast<uint32_t*>(s));
@@ -898,54 +903,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float minus = -m;
-                // half of the keys after the other: the MMAs begin with the first.  (Masked tiles
-                // have code of their own: a branch in the others' costs them a tenth.)
+                // half of the keys after the other: the MMAs begin with the first
                 float2 more = make_float2(0.0f, 0.0f);
-                auto weigh = [&](auto edge) {
-                    constexpr bool kEdge = decltype(edge)::value;
+                auto weigh = [&](float x0, float x1, int k) {
+                    float x[2];
+                    fma_pair(x, x0, x1, xs, minus);
+                    x[0] = exp2_approx(x[0]);
+                    x[1] = exp2_approx(x[1]);
+                    if (k & 2)
+                        more = add_pair(more, x[0], x[1]);
+                    else
+                        l = add_pair(l, x[0], x[1]);
+                    return pack2(x[0], x[1]);
+                };
+                auto written = [&](uint64_t* bar) {
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar);
+                };
+                // (masked tiles have code of their own, since a branch in the others' costs them a
+                // tenth, and short code, 32 keys at a time: short prompts take 37.3 us with it, 40.3
+                // with the others' 64; those in 32 as well: a long prompt 1383 us against 1324)
+                if (masked) {
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t w[16] = {};
+                        if (c < most) {
+                            tmem_ld_32x32b_x32(s_addr + c, reinterpret_cast<uint32_t*>(s));
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                w[k / 2] = weigh(k < seen - c ? s[k] : -INFINITY, k + 1 < seen - c ? s[k + 1] : -INFINITY, k);
+                        }
+                        tmem_st_32x32b_x16(s_addr + c / 2, w);
+                        if (c & 32)
+                            written(c == 32 ? &p_half[h] : &p_full[h]);
+                    }
+                } else {
 #pragma unroll 1
                     for (int c = 0; c < kTile; c += 64) {
                         uint32_t w[32];
 #pragma unroll
                         for (int q = 0; q < 64; q += 32) {
-                            if (kEdge && c + q >= most) {
 #pragma unroll
-                                for (int k = q; k < q + 32; k += 2)
-                                    w[k / 2] = 0u;
-                                continue;
-                            }
-#pragma unroll
-                            for (int k = q; k < q + 32; k += 2) {
-                                float x[2] = {s[k], s[k + 1]};
-                                if (kEdge) {
-                                    x[0] = k < seen - c ? x[0] : -INFINITY;
-                                    x[1] = k + 1 < seen - c ? x[1] : -INFINITY;
-                                }
-                                fma_pair(x, x[0], x[1], xs, minus);
-                                x[0] = exp2_approx(x[0]);
-                                x[1] = exp2_approx(x[1]);
-                                if (k & 2)
-                                    more = add_pair(more, x[0], x[1]);
-                                else
-                                    l = add_pair(l, x[0], x[1]);
-                                w[k / 2] = pack2(x[0], x[1]);
-                            }
+                            for (int k = q; k < q + 32; k += 2)
+                                w[k / 2] = weigh(s[k], s[k + 1], k);
                             if (c == 0)
                                 tmem_ld_32x32b_x32(s_addr + 64 + q, reinterpret_cast<uint32_t*>(s + q));
                         }
                         tmem_st_32x32b_x32(s_addr + c / 2, w);
-                        tmem_st_wait();
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(c == 0 ? &p_half[h] : &p_full[h]);
+                        written(c == 0 ? &p_half[h] : &p_full[h]);
                         tmem_ld_wait();
                     }
-                };
-                if (masked)
-                    weigh(std::true_type());
-                else
-                    weigh(std::false_type());
+                }
                 l = add_pair(l, more.x, more.y);
             }
             // ------------------------------------------------------- results
@@ -966,60 +978,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t part_half = (2 * static_cast<int64_t>(blockIdx.x) + slot) * 2 + h;
             uint8_t* mine = smem + C::OFF_OUT + warp * 2048;
 #pragma unroll 1
-                                for (int c = 0; c < kDim; c += 32) {
-                                    float x[32];
-                                    if (some) {
-                                        tmem_ld_32x32b_x32(o_addr + c, reinterpret_cast<uint32_t*>(x));
-                                        tmem_ld_wait();
-                                    } else {
+            for (int c = 0; c < kDim; c += 32) {
+                float x[32];
+                if (some) {
+                    tmem_ld_32x32b_x32(o_addr + c, reinterpret_cast<uint32_t*>(x));
+                    tmem_ld_wait();
+                } else {
 #pragma unroll
-                                        for (int k = 0; k < 32; ++k)
-                                            x[k] = 0.0f;
-                                    }
+                    for (int k = 0; k < 32; ++k)
+                        x[k] = 0.0f;
+                }
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k)
-                                        x[k] *= scale;
-                                    if (bad != nullptr) {
+                for (int k = 0; k < 32; ++k)
+                    x[k] *= scale;
+                if (bad != nullptr) {
 #pragma unroll
-                                        for (int k = 0; k < 32; ++k) {
-                                            float add = 0.0f;
-                                            if (bad[c + k] < limit)
-                                                add += INFINITY;
-                                            if (bad[kDim + c + k] < limit)
-                                                add -= INFINITY;
-                                            if (bad[2 * kDim + c + k] < limit)
-                                                add = __uint_as_float(0x7FC00000u);
-                                            x[k] += add;
-                                        }
-                                    }
-                                    if (slot < 0) {
-                                        // by way of shared memory, so that four lanes write 64 bytes of a row
+                    for (int k = 0; k < 32; ++k) {
+                        float add = 0.0f;
+                        if (bad[c + k] < limit)
+                            add += INFINITY;
+                        if (bad[kDim + c + k] < limit)
+                            add -= INFINITY;
+                        if (bad[2 * kDim + c + k] < limit)
+                            add = __uint_as_float(0x7FC00000u);
+                        x[k] += add;
+                    }
+                }
+                if (slot < 0) {
+                    // by way of shared memory, so that four lanes write 64 bytes of a row
 #pragma unroll
-                                        for (int k = 0; k < 4; ++k)
-                                            *reinterpret_cast<uint4*>(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8(x + 8 * k);
-                                        __syncwarp();
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(mine + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) = pack8(x + 8 * k);
+                    __syncwarp();
 #pragma unroll
-                                        for (int k = 0; k < 4; ++k) {
-                                            const int from = k * 8 + (lane >> 2);  // lane of the row
-                                            const int64_t dst = __shfl_sync(0xFFFFFFFFu, out_row, from);
-                                            const uint4 v = *reinterpret_cast<const uint4*>(mine + from * 64 + (((lane & 3) ^ ((from >> 1) & 3)) << 4));
-                                            if (dst >= 0)
-                                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + dst + c + (lane & 3) * 8) = v;
-                                        }
-                                        __syncwarp();
-                                    } else if (live) {
-                                        float4* dst = reinterpret_cast<float4*>(p.part_o) + (part_half * (kDim / 4) + c / 4) * kHalf + row;
+                    for (int k = 0; k < 4; ++k) {
+                        const int from = k * 8 + (lane >> 2);  // lane of the row
+                        const int64_t dst = __shfl_sync(0xFFFFFFFFu, out_row, from);
+                        const uint4 v = *reinterpret_cast<const uint4*>(mine + from * 64 + (((lane & 3) ^ ((from >> 1) & 3)) << 4));
+                        if (dst >= 0)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + dst + c + (lane & 3) * 8) = v;
+                    }
+                    __syncwarp();
+                } else if (live) {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o) + (part_half * (kDim / 4) + c / 4) * kHalf + row;
 #pragma unroll
-                                        for (int k = 0; k < 8; ++k)
-                                            dst[k * kHalf] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-                                    }
-                                }
-                                if (live) {
-                                    if (slot >= 0)
-                                        p.part_ml[part_half * kHalf + row] = make_float2(m, sum);
-                                    else if (p.a.lse != nullptr)
-                                        p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
-                                }
+                    for (int k = 0; k < 8; ++k)
+                        dst[k * kHalf] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                }
+            }
+            if (live) {
+                if (slot >= 0)
+                    p.part_ml[part_half * kHalf + row] = make_float2(m, sum);
+                else if (p.a.lse != nullptr)
+                    p.a.lse[token * p.a.q_heads + hq] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+            }
             // O, and what was found in the values, may be written again
             tc_fence_before_sync();
             __syncwarp();
