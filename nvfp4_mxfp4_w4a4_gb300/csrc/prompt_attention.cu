@@ -54,10 +54,12 @@ constexpr int kRows = 2 * kHalf;     // of a unit
 constexpr int kTile = 128;           // keys of a tile
 constexpr int kSlab = 128 * 128;     // bytes of 64 bf16 elements of 128 rows or keys
 constexpr int kThreads = 384;
-constexpr int kUnitPlaces = 3;       // of a unit's start and end on the line (2: 1318 us, 3: 1323, 5: 1329)
+// places of a unit's start and end on the line (2 to 5: 38.2 / 37.4 / 37.4 / 39.6 us for the short
+// prompts above, 1305 to 1313 for the long one)
+constexpr int kUnitPlaces = 3;
 constexpr int kLeastRun = kUnitPlaces + 4;
-// units of at most so many tiles are never cut (a prompt of 16381 tokens uncut: 1404 us against
-// 1323; 16 of up to 509 tokens cut: 42 us, with the join's launch, against 39)
+// units of at most so many tiles are never cut (the long prompt uncut: 1379 us against 1311; the
+// short ones cut: 39.0 us against 37.4, 36.5 without the join's launch)
 constexpr int kWholeTiles = 8;
 constexpr int kParts = 4;            // of the run whose descriptions are in shared memory
 constexpr int kWarpSequences = 96;   // up to so many sequences, a warp adds one up
