@@ -38,7 +38,6 @@
 
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "decoder_ops.h"
 #include "formats.cuh"
