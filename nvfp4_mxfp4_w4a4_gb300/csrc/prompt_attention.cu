@@ -884,8 +884,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 }
                 top *= p.xscale;
-                if (__any_sync(0xFFFFFFFFu, live && top > m + kSlack)) {
-                    const float next = fmaxf(m, top);
+                const bool moves = top > m + kSlack;
+                if (__any_sync(0xFFFFFFFFu, live && moves)) {
+                    // (a row whose own score does not ask for it keeps its reference, a factor of one: what
+                    // the warp's other rows see has no part in its bits)
+                    const float next = moves ? top : m;
                     const float factor = exp2_approx(m - next);
                     m = next;
                     l.x *= factor;
