@@ -138,7 +138,9 @@ FP4LIN_API fp4_status fp4_get_device_status(void);
  *                          fp4_prompt_attention launch, the first CTA
  *                          leaves out its products with the values: its waits
  *                          expire, what it would have written is not written,
- *                          and the status is the same.  0: off.
+ *                          and the status is the same.  In a matrix-vector
+ *                          product (fp4_gemv_*) the first CTA leaves out its
+ *                          first load, with the same result.  0: off.
  * Returns FP4_ERR_INVALID_ARG for other values.  Not for production use.    */
 FP4LIN_API fp4_status fp4_debug_set_wait_fault(uint64_t wait_limit_ns, int32_t withhold_split_signal);
 

@@ -151,6 +151,7 @@ fp4_status gemv(const void* x, const uint8_t* w, const uint8_t* sw, float w_glob
     if (st != FP4_OK || (st = device(&a.status)) != FP4_OK)
         return st;
     a.wait_ns = fp4lin::api_wait_limit_ns();
+    a.withhold = fp4lin::api_withhold_signal();
     a.x = x, a.w = w, a.sw = sw, a.bias = bias, a.out = out;
     a.M = static_cast<int>(M), a.N = N, a.K = K;
     a.nv = nv, a.w_global = w_global;
@@ -588,6 +589,7 @@ fp4_status fp4_gemv_mxfp4_experts(const void* x_bf16, const int32_t* expert_ids,
     if ((st = device(&a.status)) != FP4_OK)
         return st;
     a.wait_ns = fp4lin::api_wait_limit_ns();
+    a.withhold = fp4lin::api_withhold_signal();
     a.x = x_bf16, a.w = w, a.sw = sw, a.bias = bias_bf16, a.out = out_bf16;
     a.M = static_cast<int>(rows), a.N = N, a.K = K;
     a.w_global = 1.0f;

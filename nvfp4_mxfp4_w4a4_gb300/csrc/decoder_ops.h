@@ -62,6 +62,7 @@ struct GemvArgs {
     int E, rows_per_x;
     unsigned int* status;
     unsigned long long wait_ns;
+    bool withhold;  // test hook
 };
 
 cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream);

@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
                     uint64_t* bar = &full[turn.slot];
                     const uint32_t bytes = min(kChunks * RUN, p.kb4 * 512 - step * (kChunks * RUN));
                     const int slabs = min(kStageK / 256, (K - step * kStageK + 255) / 256);
-                    if (elect_one()) {
+                    // (test hook: the first CTA's first stage never comes)
+                    if (elect_one() && !(a.withhold && blockIdx.x == 0 && issued == 0)) {
                         mbar_arrive_expect_tx(bar, slabs * kSlab + bytes);
                         for (int i = 0; i < slabs; ++i)
                             tma_load_2d(to + i * kSlab, &w_map, bar, step * (kStageK / 2) + i * 128, row0);
@@ -337,12 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
     const uint32_t b_at = reads ? static_cast<uint32_t>(reinterpret_cast<uint8_t*>(xs + (kWide ? g * pitch + 8 * j : (g & 1) * pitch + 32 * j)) - ring)
                                 : static_cast<uint32_t>(reinterpret_cast<uint8_t*>(zeros) - ring);
     const uint32_t b_step = reads ? kChunk * 2 : 0, b_block = reads ? 64 : 0;
-    for (int64_t v = first; ok && v < end; at.next(p, ++v), ++sets) {
+    // A warp whose wait has run out multiplies no more, but goes on to the barriers: they count
+    // all 16 warps and know no limit, so that the warps give up together, at the next of them.
+    for (int64_t v = first; v < end; at.next(p, ++v), ++sets) {
         if (at.x_row != x_row) {
             // activations: a lane has 8 elements of every token, four lanes a block of 32 (whole
             // warps go round: their lanes exchange)
-            if (x_row >= 0)
-                named_barrier_sync(1, kWarps * 32);
+            if (x_row >= 0 && named_barrier_or(1, kWarps * 32, !ok))
+                break;
             x_row = at.x_row;
             const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + static_cast<int64_t>(x_row) * K;
             for (int k0 = warp * 256; k0 < padded; k0 += kWarps * 256) {
@@ -389,9 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
             }
             named_barrier_sync(1, kWarps * 32);
         }
+        if (!ok)
+            continue;
         const bool live_set = at.expert(p) >= 0;
         float acc[4][2] = {};  // rows g + 8 q, tokens 2 j and 2 j + 1 (of 1 or 2: both, of the lane's blocks)
-        for (int step = 0; ok && live_set && step < steps; ++step, turn.next(p.stages), odd ^= 1u) {
+        for (int step = 0; live_set && step < steps; ++step, turn.next(p.stages), odd ^= 1u) {
             if (odd != static_cast<uint32_t>(group))
                 continue;
             const uint32_t slot = turn.slot;
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvParams p, c
         if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(&taken[place]), (sets / SUMS & 1u) ^ 1u)))
             ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_bounded(&taken[place], (sets / SUMS & 1u) ^ 1u, a.status, kStatusTimeout, a.wait_ns));
         if (!ok)
-            break;
+            continue;
         float* mine = red + (place * kWarps + warp) * TOK * kSetRows;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
