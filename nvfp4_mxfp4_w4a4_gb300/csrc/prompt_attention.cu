@@ -1043,6 +1043,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bad_free[part_count & 1u]);
             part_done();
         }
+        // a wait ran out: these rows' partial results may be missing, which a reference that is
+        // NaN (as none ever is) tells the join
+        if (!ok && p.may_cut) {
+            for (int slot = 0; slot < 2; ++slot)
+                p.part_ml[((2 * static_cast<int64_t>(blockIdx.x) + slot) * 2 + h) * kHalf + row].x = __uint_as_float(0x7FC00000u);
+        }
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -1096,9 +1102,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const Prom
     const bool live = row_of(row, &token, &hq);
     auto index = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(c0) + (i == 0 ? 1 : 2 * i)) * 2 + half; };
     float mx = kUnset;
+    bool missing = false;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i)
-        mx = live ? fmaxf(mx, p.part_ml[index(i) * kHalf + row].x) : mx;
+    for (int i = 0; i < parts; ++i) {
+        const float m = live ? p.part_ml[index(i) * kHalf + row].x : kUnset;
+        mx = fmaxf(mx, m);
+        missing |= m != m;
+    }
+    if (__any_sync(0xFFFFFFFFu, missing))  // (a part whose waits ran out: the block's rows, one warp's there, stay as they are)
+        return;
     float4 o[W] = {};
     float sum = 0.0f;
 #pragma unroll 2
