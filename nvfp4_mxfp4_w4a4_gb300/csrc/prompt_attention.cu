@@ -787,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
                             fence_proxy_async_smem();
+                            __syncwarp();  // (a vote orders no memory)
                         }
                     }
                     if (j + 1 < hi && !wait(&k_full[(g + 1) % STAGES], (g + 1) / STAGES))
