@@ -232,19 +232,20 @@ struct Run {
     }
 };
 
-// This CTA's run; false if it has none.  All threads call it; `scratch` is free
+// What find_run's threads tell one another.
+struct Scan {
+    int64_t weight[kWarpSequences];  // places of a sequence's key head
+    int64_t warp_sum[kThreads / 32];
+    int64_t offset, per_head;
+    int longest[kThreads / 32];
+    int b;
+};
+
+// This CTA's run; false if it has none.  All threads call it; `scan` is free
 // afterwards.
-__device__ bool find_run(const PromptParams& p, uint8_t* scratch, Run* shared)
+__device__ bool find_run(const PromptParams& p, Scan* scan, Run* shared)
 {
     constexpr int kWarps = kThreads / 32;
-    struct Scan {
-        int64_t weight[kWarpSequences];  // places of a sequence's key head
-        int64_t warp_sum[kWarps];
-        int64_t offset, per_head;
-        int longest[kWarps];
-        int b;
-    };
-    Scan* scan = reinterpret_cast<Scan*>(scratch);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int batch = p.a.batch;
     const bool by_warp = batch <= kWarpSequences;
@@ -410,7 +411,7 @@ struct Cfg {
     static constexpr int SMEM = OFF_PARTS + kParts * static_cast<int>(sizeof(Part)) + 1024;  // + alignment slack
     static constexpr int TMEM_COLS = 512;  // S of the halves, then O
     static constexpr int TMEM_O = 2 * kTile;
-    static_assert(sizeof(Run) <= 128, "");
+    static_assert(sizeof(Run) <= 128 && sizeof(Scan) <= OFF_BAR - OFF_OUT, "");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -482,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     grid_dependency_wait();
     launch_dependents();
-    const bool have = find_run(p, smem, run);
+    // (in a place that no copy writes: nothing would order these writes before the copies')
+    const bool have = find_run(p, reinterpret_cast<Scan*>(smem + C::OFF_OUT), run);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();

@@ -25,3 +25,13 @@ def test_fenced_writes_meet_a_barrier_before_the_arrival(path):
         barrier = re.search(r"__syncwarp\(\);|__syncthreads\(\);|named_barrier_sync\(", rest)
         told = re.search(r"mbar_arrive|tma_store|bulk_store|bulk_commit", rest)
         assert barrier and (not told or barrier.start() < told.start()), text[:m.start()].count("\n") + 1
+
+
+def test_scratch_of_prompt_attention_is_no_place_of_a_copy():
+    """What finds a CTA's run writes shared memory as threads do; the copies that follow
+    go elsewhere (a CTA barrier does not order the two)."""
+    text = source(os.path.join(CSRC, "prompt_attention.cu"))
+    scratch = re.search(r"= find_run\(p, (?:reinterpret_cast<Scan\*>\()?smem( \+ C::(\w+))?", text)
+    copied = set(re.findall(r"tma_load_3d\(smem \+ (?:C::(OFF_\w+) \+)?", text))
+    assert copied == {"", "OFF_K", "OFF_V"}       # queries, keys, values
+    assert scratch and (scratch.group(2) or "") not in copied
