@@ -164,10 +164,10 @@ struct Walk {
         group_rows(p.a.k_offsets, b, static_cast<int>(p.a.keys), &k0, &m);
         blocks = (n + 2 * p.tokens - 1) / (2 * p.tokens);
     }
-    // Keys that query i of the sequence sees.
+    // Keys that query i of the sequence sees.  (n before m: n + m may pass 2^31)
     __device__ __forceinline__ int limit(const PromptParams& p, int i) const
     {
-        return p.a.causal ? max(min(i + 1 + m - n, m), 0) : m;
+        return p.a.causal ? max(min(i + 1 - n + m, m), 0) : m;
     }
     __device__ __forceinline__ int tiles(const PromptParams& p, int half) const
     {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     d.end[1] = max(r.lo, min(r.hi, w.tiles(p, 1)));
                     d.token = w.q0 + first;
                     d.tokens = w.n - first;
-                    d.first_seen = p.a.causal ? first + 1 + w.m - w.n : w.m;
+                    d.first_seen = p.a.causal ? first + 1 - w.n + w.m : w.m;
                     d.k0 = w.k0, d.m = w.m;
                     d.key_head = key_head, d.q_head = key_head * group + chunk * kHalf;
                     d.q_heads = min(p.heads, group - chunk * kHalf);
