@@ -10,12 +10,17 @@
 // of the set's rows, 128 (a chunk) for each of 8 warps, the other 8 have the next
 // stage.  The warps' sums of a set are added up by one more warp, in one order.
 //
-// On the device, weights in L2 where they fit: MXFP4, 1 token, 4096 x 4096 4.6 us;
-// NVFP4, 3 tokens, 14336 x 4096 10.3; MXFP4, 8 tokens, 18429 x 7168 20.1; 8 experts
-// of 2048 x 4096 10.9.  The loads alone take 3.1 / 5.0 / 9.1 / 6.1 us, all but the
-// decoding and the MMAs 3.2 / 5.6 / 12.6 / 6.2.  So what bounds it are the 190 to 250
-// instructions per 32 rows x 128 elements, 64 of them conversions of two codes that
-// take the ALU two cycles each.
+// On the device, weights in L2 (and from memory, other weights each call): MXFP4, 1
+// token, 4096 x 4096 4.6 us (5.8); NVFP4, 3 tokens, 14336 x 4096 10.4 (12.1); MXFP4, 8
+// tokens, 18429 x 7168 20.2 (22.6); 8 experts of 2048 x 4096 10.9 (12.4).  The loads
+// alone take 3.1 / 5.0 / 9.1 / 6.1 us, all but the decoding and the MMAs 3.2 / 5.6 /
+// 12.6 / 6.2, so the decoding is what a call takes longer for: 190 to 250 instructions
+// per 32 rows x 128 elements, 64 of them conversions of two codes that take the ALU two
+// cycles each.  But they do not fill any pipe (issue slots 41 to 59 % busy, the ALU 35
+// to 49 %, the tensor pipe 14 to 18 %): the rest is what does not overlap with them,
+// the launch, the activations' way into shared memory before the first product (3 us
+// at 8 tokens of 7168), the first stages, and four multiplying warps a scheduler that
+// wait for shared memory, for one another's stages and for the last sums.
 //
 // Decoding goes through one conversion per two codes (E2M1 -> f16, exact), the
 // products through m16n8k16 MMAs with float32 sums.  Codes of MXFP4 never meet
@@ -612,9 +617,11 @@ cudaError_t launch_gemv(const GemvArgs& a, cudaStream_t stream)
     if (a.expert_ids != nullptr)
         return launch<false, false>(p, 1, stream);
     // the activations of a launch's rows have to fit into shared memory beside two stages:
-    // long ones go a few at a time.  1 or 2 tokens, in the narrow / the wide form: 8.3 / 8.9 and
-    // 9.4 / 9.1 us at 14336 x 4096, 15.1 / 17.2 and 16.7 / 17.6 us at 18432 x 7168, 4.3 / 4.4 and
-    // 5.0 / 4.8 us at 4096 x 4096
+    // long ones go a few at a time.  1 and 2 tokens, in the narrow / the wide form: MXFP4 4.5 / 4.5
+    // and 5.2 / 4.9 us at 4096 x 4096, 8.6 / 8.9 and 9.6 / 9.2 at 14336 x 4096, 15.4 / 16.7 and
+    // 17.0 / 17.2 at 18432 x 7168; NVFP4 4.9 / 4.9 and 5.5 / 5.2, 9.6 / 9.9 and 10.5 / 10.1, 17.4 /
+    // 19.0 and 18.8 / 19.4: the narrow form gains more at the large ones than it loses for two
+    // tokens at the small ones
     int step = a.M;
     while (step > 1 && fixed_bytes(p.chunks, step, step > 2) + 2 * (a.nv ? stage_bytes<true>() : stage_bytes<false>()) > kMaxSmem)
         --step;

@@ -10,8 +10,9 @@
 //
 // All are bound by HBM but for the smallest calls, where the launches count: 4096
 // tokens x 8 of 64 experts, 4096 wide, are 302 MB in 44.8 us (0.99 of a plain
-// copy's rate) behind a sort of 8; the same tokens' sum 44 us, its gradient 87 us
-// (604 MB, 1.0).  32 tokens: 3.2 us sorted and copied, 3.2 us summed, on the device.
+// copy's rate) behind a sort of 8; the same tokens' sum 52 us (302 MB, 0.86), its
+// gradient 89 us (571 MB, 0.95).  32 tokens: 3.3 us sorted and copied, 3.2 us summed,
+// on the device; one token's sum 3.0.
 // Nothing is added by atomics: every result has one order.
 #include <cuda_bf16.h>
 
@@ -435,7 +436,8 @@ cudaError_t launch_moe_dispatch(const void* x, const int32_t* ids, int64_t token
         }
     }
     // one step of a CTA, or a cluster: 2048 pairs in 6.6 / 5.9 us, 8192 in 11.6 / 6.0, 32768 in
-    // 31.8 / 8.4 (11.9 with 4 CTAs); up to 1024 the same
+    // 31.8 / 8.4 (11.9 with 4 CTAs); up to 1024 the same.  Beyond that the cluster's 8 CTAs are
+    // all there is: a million pairs, rows of 8 elements, take 118 us, nearly all of it the sort
     const int ctas = pairs <= kSortThreads ? 1 : kSortCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);

@@ -26,10 +26,17 @@
 //
 // 16381 tokens, 8 x 4 heads of 128, causal: 1265 to 1365 us (from GPU to GPU), 0.84 to
 // 0.91 of the rate of a large bf16 product; the tensor pipe is busy 77 % of a run's
-// cycles, the exponentials' 39 %.  16 sequences of up to 509 tokens, heads of 64: 37
-// us, 5 of them before the first unit's products; a unit of two tiles is load, S,
-// weights, P V and results one behind the other, and a fifth of the time its warps
-// wait for instructions.
+// cycles, the exponentials' 39 %.  Heads of 64: 1013 us, 0.57 of that rate (a tile's
+// exponentials take as long as its products, so that neither hides the hand-over).  A
+// chunk of 2048 tokens behind 14333 keys, heads of 128: 312 us (0.86), one of 512: 101
+// (0.70).  16 sequences of up to 509 tokens, heads of 64: 38 us, 5 of them before the
+// first unit's products; a unit of two tiles is load, S, weights, P V and results one
+// behind the other, and a seventh of the time its warps wait for instructions.
+//
+// The weights go to the second product as bf16 (off by 2^-8 of each at most, their sum is
+// of the unrounded ones): its operands have one type, the values are bf16, and f16
+// values would lose their range.  A second product with what the rounding leaves would
+// be half as many operations again in a kernel that the tensor pipe bounds.
 //
 // Warps: 0-3 and 4-7 the softmax of the halves (they also write the results), 8
 // loads queries, keys and values (TMA), 9 issues the MMAs, 10 looks through values
@@ -58,7 +65,9 @@ constexpr int kThreads = 384;
 constexpr int kUnitPlaces = 3;
 constexpr int kLeastRun = kUnitPlaces + 4;
 // units of at most so many tiles are never cut (the long prompt uncut: 1379 us against 1311; the
-// short ones cut: 39.0 us against 37.4, 36.5 without the join's launch)
+// short ones cut: 39.0 us against 37.4, 36.5 without the join's launch; one prompt of 1000 tokens
+// with fewer units than there are SMs, 1 / 2 / 8 key heads x 4 of 128, 17.9 / 18.1 / 20.2 us
+// whole, 21.7 / 22.0 / 23.9 cut, with 4 of 64 17.1 and 21.2 for 8 key heads)
 constexpr int kWholeTiles = 8;
 constexpr int kParts = 4;            // of the run whose descriptions are in shared memory
 constexpr int kWarpSequences = 96;   // up to so many sequences, a warp adds one up

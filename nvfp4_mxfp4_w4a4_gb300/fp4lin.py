@@ -286,8 +286,9 @@ def fp4_get_device_status() -> int:
 
 
 def fp4_debug_set_wait_fault(wait_limit_ns: int = 0, withhold_split_signal: int = 0):
-    """Test hook: limit of the GEMMs' bounded device waits (0 = the default
-    1 s) and whether a split-K partial withholds its ready signal."""
+    """Test hook: limit of the kernels' bounded device waits (0 = the default
+    1 s) and whether a split-K partial withholds its ready signal (attention and
+    matrix-vector products: the first CTA a product or a load)."""
     _check(load().fp4_debug_set_wait_fault(wait_limit_ns, withhold_split_signal), "fp4_debug_set_wait_fault")
 
 
