@@ -1057,9 +1057,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // a wait ran out: these rows' partial results may be missing, which a reference that is
         // NaN (as none ever is) tells the join
-        if (!ok && p.may_cut) {
-            for (int slot = 0; slot < 2; ++slot)
-                p.part_ml[((2 * static_cast<int64_t>(blockIdx.x) + slot) * 2 + h) * kHalf + row].x = __uint_as_float(0x7FC00000u);
+        if (__builtin_expect(!ok, 0) && p.may_cut) {
+            float2* at = p.part_ml + (4 * static_cast<int64_t>(blockIdx.x) + h) * kHalf + row;
+            at[0].x = at[2 * kHalf].x = __uint_as_float(0x7FC00000u);  // (both places of the CTA)
         }
     }
     __syncwarp();
