@@ -155,3 +155,138 @@ def test_a_million_narrow_pairs(L):
     assert np.array_equal(rows.cpu().numpy(), row_of) and np.array_equal(off.cpu().numpy(), offsets)
     t, j = np.nonzero(row_of >= 0)
     assert torch.equal(to[torch.from_numpy(row_of[t, j]).long().cuda()], x[torch.from_numpy(t).cuda()])
+
+
+def test_dispatch_in_a_graph_and_on_two_streams(L):
+    """The sort over a cluster with the copies behind it, where the call before them in
+    the graph has only just written the vectors."""
+    import torch
+
+    r = np.random.default_rng(7)
+    tokens, top, E, width = 3001, 4, 1024, 264
+    sources = [torch.from_numpy(r.standard_normal((tokens, width)).astype(np.float32)).bfloat16().cuda() for _ in range(2)]
+    routes = [dev(routing(r, tokens, top, E, "padded")) for _ in range(2)]
+
+    def buffers():
+        return (torch.empty(tokens * top, width, dtype=torch.bfloat16, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                torch.empty(tokens, top, dtype=torch.int32, device="cuda"))
+
+    def right(x, ids, to, off, rows):
+        row_of, offsets = fast_rows(ids.cpu().numpy(), E)
+        assert np.array_equal(rows.cpu().numpy(), row_of) and np.array_equal(off.cpu().numpy(), offsets)
+        t, j = np.nonzero(row_of >= 0)
+        assert torch.equal(to[torch.from_numpy(row_of[t, j]).long().cuda()], x[torch.from_numpy(t).cuda()])
+
+    x, ids, src, src_ids = torch.empty_like(sources[0]), torch.empty_like(routes[0]), torch.empty_like(sources[0]), torch.empty_like(routes[0])
+    got = buffers()
+    src.copy_(sources[0])
+    src_ids.copy_(routes[0])
+    L.fp4_moe_dispatch(sources[0], routes[0], E, *got)
+    right(sources[0], routes[0], *got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.copy_(src)
+        ids.copy_(src_ids)
+        L.fp4_moe_dispatch(x, ids, E, *got)
+    for i in range(30):
+        src.copy_(sources[i % 2])
+        src_ids.copy_(routes[i % 2])
+        graph.replay()
+        if i % 2 or i == 0:
+            right(sources[i % 2], routes[i % 2], *got)
+    both = [buffers() for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(100):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                L.fp4_moe_dispatch(sources[i], routes[i], E, *both[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        right(sources[i], routes[i], *both[i])
+
+
+def test_most_sequences(L):
+    """65535 sequences, nearly all of them empty or of a token or two."""
+    n = np.zeros(65535, np.int64)
+    n[::9], n[4::31], n[65534], n[30000] = 1, 2, 300, 700
+    m = n + (np.arange(65535) % 3) * (n > 0)
+    p = Problem(list(zip(n.tolist(), m.tolist())), 1, 2, 64, seed=8)
+    p.run(L)
+    p.check()
+    assert L.fp4_get_device_status() == 0
+
+
+def test_offsets_past_32_bits(L):
+    """Token strides that bring the last rows more than 2^31 elements in, for every operator
+    that takes strides."""
+    import torch
+
+    r = np.random.default_rng(9)
+    T, wide, heads, dim = 2200, 1 << 20, 2, 64
+    base = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")
+    assert (T - 1) * wide > 2 ** 31
+
+    def place(k, n):
+        return base[:, 4096 * k:4096 * k + n]
+
+    p = Problem([(T, T)], heads, 2, dim, seed=9, extra=0)
+    p.run(L)
+    p.check()
+    out, lse = p.out.clone(), p.lse.clone()
+    for i, name in enumerate(("q", "k", "v", "out")):
+        t = getattr(p, name)
+        far = place(i, t.shape[1] * dim).unflatten(1, (t.shape[1], dim))
+        far.copy_(t)
+        setattr(p, name, far)
+    p.out.fill_(7.0)
+    p.run(L)
+    assert torch.equal(p.out, out) and torch.equal(p.lse, lse)
+    # norms of heads
+    w = torch.from_numpy(r.standard_normal(dim).astype(np.float32)).bfloat16().cuda()
+    near = [torch.empty(T, h, dim, dtype=torch.bfloat16, device="cuda") for h in (4, 2)]
+    L.fp4_qk_norm_rope(p.q.contiguous(), p.k.contiguous(), *near, w, w)
+    far = [place(4, 4 * dim).unflatten(1, (4, dim)), place(5, 2 * dim).unflatten(1, (2, dim))]
+    L.fp4_qk_norm_rope(p.q, p.k, *far, w, w)
+    assert all(torch.equal(a, b) for a, b in zip(near, far))
+    # experts' rows and back
+    x, top, E = place(0, 256), 2, 7
+    ids = dev(routing(r, T, top, E, "plain"))
+    to, want = (torch.empty(T * top, 256, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    off, rows = torch.empty(E + 1, dtype=torch.int32, device="cuda"), torch.empty(T, top, dtype=torch.int32, device="cuda")
+    L.fp4_moe_dispatch(x.contiguous(), ids, E, want, off, rows)
+    L.fp4_moe_dispatch(x, ids, E, to, off, rows)
+    assert torch.equal(to, want)
+    p2 = dev(r.random((T, top)).astype(np.float32))
+    near = torch.empty(T, 256, dtype=torch.bfloat16, device="cuda")
+    L.fp4_moe_combine(to, rows, p2, near)
+    L.fp4_moe_combine(to, rows, p2, place(6, 256))
+    assert torch.equal(near, place(6, 256))
+    a, b = torch.empty_like(to), torch.empty_like(to)
+    ga, gb = torch.empty_like(p2), torch.empty_like(p2)
+    L.fp4_moe_combine_backward(near, to, rows, p2, a, ga)
+    L.fp4_moe_combine_backward(place(6, 256), to, rows, p2, b, gb)
+    assert torch.equal(a, b) and torch.equal(ga, gb)
+
+
+def test_experts_past_32_bits(L):
+    """Weights of more than 2^32 bytes: the last experts' rows against their own products."""
+    import torch
+
+    E, n, k = 300, 8200, 4096
+    g = torch.Generator(device="cuda").manual_seed(10)
+    w = torch.randint(0, 256, (E, n, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    sw = torch.randint(118, 124, (E, L.fp4_sf_bytes(n, k)), dtype=torch.uint8, device="cuda", generator=g)
+    assert w.numel() > 2 ** 32
+    r = np.random.default_rng(10)
+    ids = np.array([E - 1, 0, E - 2, 255], np.int32)
+    x = acts(r, 1, k).cuda()
+    out = torch.empty(4, n, dtype=torch.bfloat16, device="cuda")
+    L.fp4_gemv_mxfp4_experts(x, dev(ids), E, 4, 4, w, sw, None, out, n, k)
+    one, size = torch.empty(1, n, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, dtype=torch.bfloat16, device="cuda")
+    for i, e in enumerate(ids):
+        L.fp4_gemv_mxfp4(x, w[e], sw[e], None, one, 1, n, k)
+        L.fp4_gemv_mxfp4(x.abs(), w[e] & 0x77, sw[e], None, size, 1, n, k)    # sums of magnitudes
+        # (the same products summed in another order, and two roundings)
+        assert ((out[i].double() - one[0].double()).abs() <= 2.0 ** -7 * one[0].double().abs()
+                + 1.01 * 2 * (k / 16 + 40) * 2.0 ** -23 * size[0].double()).all()
